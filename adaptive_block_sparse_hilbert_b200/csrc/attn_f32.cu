@@ -17,7 +17,7 @@ template <int D>
 __global__ void __launch_bounds__(64) attn_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                       const float* __restrict__ v, const int32_t* __restrict__ row_ptr,
                                                       const int32_t* __restrict__ col_idx, int dense, float* __restrict__ o,
-                                                      int N, int nB, float scale) {
+                                                      float* __restrict__ lse, int N, int nB, float scale) {
   extern __shared__ float smem_f32[];
   float(*sk)[D + 1] = reinterpret_cast<float(*)[D + 1]>(smem_f32);
   float(*sv)[D] = reinterpret_cast<float(*)[D]>(smem_f32 + kBlock * (D + 1));
@@ -70,32 +70,34 @@ __global__ void __launch_bounds__(64) attn_f32_kernel(const float* __restrict__ 
     float* ob = o + (bh * N + i) * D;
 #pragma unroll
     for (int c = 0; c < D; ++c) ob[c] = acc[c] * inv;
+    if (lse) lse[bh * N + i] = l > 0.0f ? m + logf(l) : -INFINITY;
   }
 }
 
 template <int D>
 static cudaError_t launch_f32_t(dim3 grid, const float* q, const float* k, const float* v, const int32_t* row_ptr,
-                                const int32_t* col_idx, bool dense, float* o, int N, int nB, float scale,
-                                cudaStream_t st) {
+                                const int32_t* col_idx, bool dense, float* o, float* lse, int N, int nB,
+                                float scale, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(kBlock) * (2 * D + 1) * sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_f32_kernel<D><<<grid, 64, smem, st>>>(q, k, v, row_ptr, col_idx, dense ? 1 : 0, o, N, nB, scale);
+  attn_f32_kernel<D><<<grid, 64, smem, st>>>(q, k, v, row_ptr, col_idx, dense ? 1 : 0, o, lse, N, nB, scale);
   return cudaGetLastError();
 }
 
 cudaError_t launch_attn_f32(const Dims& Dm, const float* q, const float* k, const float* v, const int32_t* row_ptr,
-                            const int32_t* col_idx, bool dense, float* o, float scale, cudaStream_t st) {
+                            const int32_t* col_idx, bool dense, float* o, float* lse, float scale,
+                            cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(Dm.nB), static_cast<unsigned>(Dm.BH));
   const int N = static_cast<int>(Dm.N), nB = static_cast<int>(Dm.nB);
   switch (Dm.d) {
     case 32:
-      return launch_f32_t<32>(grid, q, k, v, row_ptr, col_idx, dense, o, N, nB, scale, st);
+      return launch_f32_t<32>(grid, q, k, v, row_ptr, col_idx, dense, o, lse, N, nB, scale, st);
     case 64:
-      return launch_f32_t<64>(grid, q, k, v, row_ptr, col_idx, dense, o, N, nB, scale, st);
+      return launch_f32_t<64>(grid, q, k, v, row_ptr, col_idx, dense, o, lse, N, nB, scale, st);
     case 128:
-      return launch_f32_t<128>(grid, q, k, v, row_ptr, col_idx, dense, o, N, nB, scale, st);
+      return launch_f32_t<128>(grid, q, k, v, row_ptr, col_idx, dense, o, lse, N, nB, scale, st);
     default:
       return cudaErrorInvalidValue;
   }

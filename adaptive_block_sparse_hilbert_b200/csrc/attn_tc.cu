@@ -89,7 +89,7 @@ constexpr size_t attn_smem_bytes() {
 template <int D, bool DENSE, bool VF16>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     attn_bf16_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, __nv_bfloat16* __restrict__ out,
+                     const __grid_constant__ CUtensorMap tmv, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                      const int32_t* __restrict__ tile_ptr, const int32_t* __restrict__ tile_col,
                      const int32_t* __restrict__ worklist, int slot0, int ntiles, int N, int nB, int nPairs, float scale_log2,
                      uint64_t kWaitLimitNs, uint32_t diag_flags, int32_t* dev_status, int64_t* cta_trace) {
@@ -400,6 +400,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       const float inv_l = l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
       const int grow = t * kBM + row;
       const bool valid = grow < N && n_iter > 0;
+      // ln sum exp(scale s) = ln 2 (m_ref + log2 l): the statistics are held in log2 units
+      if (!DENSE && lse != nullptr && grow < N && tile_ok)
+        lse[static_cast<int64_t>(bh) * N + grow] =
+            l_sum > 0.0f ? 0.6931471805599453f * (m_ref + log2f(l_sum)) : -INFINITY;
       uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(bh) * N + grow) * D);
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -489,7 +493,7 @@ static bool make_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, 
 
 template <int D, bool DENSE, bool VF16>
 static cudaError_t launch_attn_t(const Dims& Dm, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                 const fva_mask* m, void* o, float scale_log2, int first_slot, int n_slots,
+                                 const fva_mask* m, void* o, float* lse, float scale_log2, int first_slot, int n_slots,
                                  int32_t* dev_status, cudaStream_t st) {
   const size_t smem = attn_smem_bytes<D>();
   cudaError_t e = cudaFuncSetAttribute(attn_bf16_kernel<D, DENSE, VF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -498,7 +502,7 @@ static cudaError_t launch_attn_t(const Dims& Dm, const CUtensorMap& mq, const CU
   const unsigned grid = static_cast<unsigned>(DENSE ? Dm.tiles : n_slots);
   if (grid == 0) return cudaSuccess;
   attn_bf16_kernel<D, DENSE, VF16><<<grid, kAttnThreads, smem, st>>>(
-      mq, mk, mv, static_cast<__nv_bfloat16*>(o), DENSE ? nullptr : m->tile_ptr, DENSE ? nullptr : m->tile_col,
+      mq, mk, mv, static_cast<__nv_bfloat16*>(o), lse, DENSE ? nullptr : m->tile_ptr, DENSE ? nullptr : m->tile_col,
       DENSE ? nullptr : m->worklist, DENSE ? 0 : first_slot, static_cast<int>(Dm.tiles), static_cast<int>(Dm.N), static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs),
       scale_log2, attn_wait_limit_ns(), attn_diag_flags(), dev_status, g_cta_trace);
   return cudaGetLastError();
@@ -506,18 +510,18 @@ static cudaError_t launch_attn_t(const Dims& Dm, const CUtensorMap& mq, const CU
 
 template <int D>
 static cudaError_t launch_attn_d(const Dims& Dm, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                 bool v_f16, const fva_mask* m, bool dense, void* o, float scale_log2, int first_slot,
-                                 int n_slots, int32_t* dev_status, cudaStream_t st) {
+                                 bool v_f16, const fva_mask* m, bool dense, void* o, float* lse, float scale_log2,
+                                 int first_slot, int n_slots, int32_t* dev_status, cudaStream_t st) {
   if (v_f16) {
-    return dense ? launch_attn_t<D, true, true>(Dm, mq, mk, mv, m, o, scale_log2, 0, 0, dev_status, st)
-                 : launch_attn_t<D, false, true>(Dm, mq, mk, mv, m, o, scale_log2, first_slot, n_slots, dev_status, st);
+    return dense ? launch_attn_t<D, true, true>(Dm, mq, mk, mv, m, o, lse, scale_log2, 0, 0, dev_status, st)
+                 : launch_attn_t<D, false, true>(Dm, mq, mk, mv, m, o, lse, scale_log2, first_slot, n_slots, dev_status, st);
   }
-  return dense ? launch_attn_t<D, true, false>(Dm, mq, mk, mv, m, o, scale_log2, 0, 0, dev_status, st)
-               : launch_attn_t<D, false, false>(Dm, mq, mk, mv, m, o, scale_log2, first_slot, n_slots, dev_status, st);
+  return dense ? launch_attn_t<D, true, false>(Dm, mq, mk, mv, m, o, lse, scale_log2, 0, 0, dev_status, st)
+               : launch_attn_t<D, false, false>(Dm, mq, mk, mv, m, o, lse, scale_log2, first_slot, n_slots, dev_status, st);
 }
 
 cudaError_t launch_attn_bf16(const Dims& Dm, const void* q, const void* k, const void* v, bool v_f16,
-                             const fva_mask* m, bool dense, void* o, float scale, int64_t first_slot, int64_t n_slots,
+                             const fva_mask* m, bool dense, void* o, float* lse, float scale, int64_t first_slot, int64_t n_slots,
                              int32_t* dev_status, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, q, Dm.BH, Dm.N, Dm.d, false) || !make_map(&mk, k, Dm.BH, Dm.N, Dm.d, false) ||
@@ -525,8 +529,8 @@ cudaError_t launch_attn_bf16(const Dims& Dm, const void* q, const void* k, const
     return cudaErrorInvalidValue;
   const float scale_log2 = scale * 1.4426950408889634f;
   const int fs = static_cast<int>(first_slot), ns = static_cast<int>(n_slots);
-  if (Dm.d == 128) return launch_attn_d<128>(Dm, mq, mk, mv, v_f16, m, dense, o, scale_log2, fs, ns, dev_status, st);
-  return launch_attn_d<64>(Dm, mq, mk, mv, v_f16, m, dense, o, scale_log2, fs, ns, dev_status, st);
+  if (Dm.d == 128) return launch_attn_d<128>(Dm, mq, mk, mv, v_f16, m, dense, o, lse, scale_log2, fs, ns, dev_status, st);
+  return launch_attn_d<64>(Dm, mq, mk, mv, v_f16, m, dense, o, lse, scale_log2, fs, ns, dev_status, st);
 }
 
 }  // namespace fva

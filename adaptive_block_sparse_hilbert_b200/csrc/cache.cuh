@@ -1,0 +1,79 @@
+// Paged key/value cache: what its kernels share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "fva_internal.cuh"
+
+namespace fva {
+
+struct CacheDims {
+  int B, Hkv, d, max_blocks, n_pages, dtype, esize;
+};
+constexpr int kMaxCacheBlocks = 16384;  // one CTA's shared memory holds a float64 per block
+
+// Pointers of one cache and one batch of sequences, as the kernels take them.
+template <typename T>
+struct CacheView {
+  T* k;
+  T* v;
+  float* key_mean;
+  float* mass;
+  const int32_t* table;
+  const int32_t* len;
+  int B, Hkv, n_pages, max_blocks;
+};
+
+template <typename T>
+inline CacheView<T> cache_view(const fva_cache* c, const fva_seqs* q) {
+  return {static_cast<T*>(c->k), static_cast<T*>(c->v), c->key_mean, c->mass, q->table,
+          q->len,                q->B,                  c->Hkv,      c->n_pages, q->max_blocks};
+}
+
+// Sequence length, kept inside [0, 64 max_blocks]; a length outside is reported.
+template <typename T>
+__device__ __forceinline__ int seq_len(const CacheView<T>& c, int b, int32_t* dev_status) {
+  const int n = c.len[b];
+  if (n < 0 || n > c.max_blocks * kBlock) {
+    report(dev_status, FVA_DEVERR_BAD_LIST);
+    return n < 0 ? 0 : c.max_blocks * kBlock;
+  }
+  return n;
+}
+
+// Page of a sequence's block; -1, reported, when the table names no page.
+template <typename T>
+__device__ __forceinline__ int page_of(const CacheView<T>& c, int b, int block, int32_t* dev_status) {
+  const int p = c.table[static_cast<int64_t>(b) * c.max_blocks + block];
+  if (p >= 0 && p < c.n_pages) return p;
+  report(dev_status, FVA_DEVERR_BAD_LIST);
+  return -1;
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_f32(float x, float* o) { *o = x; }
+__device__ __forceinline__ void from_f32(float x, __nv_bfloat16* o) { *o = __float2bfloat16(x); }
+__device__ __forceinline__ void from_f32(float x, __half* o) { *o = __float2half_rn(x); }
+
+cudaError_t launch_cache_append(const fva_cache* c, const fva_seqs* q, const void* k_new, const void* v_new,
+                                int64_t token_stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
+                                cudaStream_t st);
+cudaError_t launch_cache_route(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride, double p,
+                               int k_floor, int n_recent, double scale, int32_t* kept, int32_t* n_kept, double* scores,
+                               int32_t* dev_status, cudaStream_t st);
+struct CacheAttnScratch {
+  float* part;    // [2 * CTAs][16][d + 2]: unfinished rows' O, maximum and sum
+  float* scores;  // [B, H, 64 * max_blocks], log2 units; only when weights are accumulated
+  float* lse;     // [B, H] log2 units
+};
+size_t cache_attn_part_floats(int d);
+cudaError_t launch_cache_attn(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride,
+                              const int32_t* kept, const int32_t* n_kept, void* o, float* lse, float scale,
+                              int accumulate, const CacheAttnScratch& ws, int32_t* dev_status, cudaStream_t st);
+cudaError_t launch_cache_evict(const fva_cache* c, const fva_seqs* s, int keep, int n_sink, int n_recent,
+                               const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len,
+                               int32_t* dev_status, cudaStream_t st);
+
+}  // namespace fva

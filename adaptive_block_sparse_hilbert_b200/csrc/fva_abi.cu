@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "cache.cuh"
 #include "fva_internal.cuh"
 
 namespace fva {
@@ -296,13 +297,14 @@ int fva_build_tiles(const fva_shape* s, const fva_mask* mask, int order, void* w
 }
 
 static int attn_common(const fva_shape* s, const void* q, const void* k, const void* v, int v_dtype,
-                       const fva_mask* m, void* o, float scale, bool dense, int64_t first_slot, int64_t n_slots,
-                       bool whole, int32_t* dev_status, fva_stream_t stream) {
+                       const fva_mask* m, void* o, float* lse, float scale, bool dense, int64_t first_slot,
+                       int64_t n_slots, bool whole, int32_t* dev_status, fva_stream_t stream) {
   Dims D;
   if (!s || !q || !k || !v || !o) return FVA_ERR_INVALID_ARG;
   if (!make_dims(s, &D)) return FVA_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return FVA_ERR_ALIGNMENT;
   if (o == q || o == k || o == v) return FVA_ERR_INVALID_ARG;
+  if (lse && !aligned16(lse)) return FVA_ERR_ALIGNMENT;
   if (whole) {
     first_slot = 0;
     n_slots = D.tiles;
@@ -314,7 +316,7 @@ static int attn_common(const fva_shape* s, const void* q, const void* k, const v
     if (D.d != 64 && D.d != 128) return FVA_ERR_UNSUPPORTED_SHAPE;
     if (!dense && (!m || !m->tile_ptr || !m->tile_col || !m->worklist)) return FVA_ERR_INVALID_ARG;
     if (!attn_cta_trace_fits(D.tiles)) return FVA_ERR_CAPACITY;
-    return cuda_status(launch_attn_bf16(D, q, k, v, v_dtype == FVA_F16, m, dense, o, scale, first_slot, n_slots,
+    return cuda_status(launch_attn_bf16(D, q, k, v, v_dtype == FVA_F16, m, dense, o, lse, scale, first_slot, n_slots,
                                         dev_status, stream));
   }
   if (v_dtype != FVA_F32) return FVA_ERR_INVALID_ARG;
@@ -323,24 +325,219 @@ static int attn_common(const fva_shape* s, const void* q, const void* k, const v
   if (!dense && (!m || !m->row_ptr || !m->col_idx)) return FVA_ERR_INVALID_ARG;
   return cuda_status(launch_attn_f32(D, static_cast<const float*>(q), static_cast<const float*>(k),
                                      static_cast<const float*>(v), dense ? nullptr : m->row_ptr,
-                                     dense ? nullptr : m->col_idx, dense, static_cast<float*>(o), scale, stream));
+                                     dense ? nullptr : m->col_idx, dense, static_cast<float*>(o), lse, scale, stream));
 }
 
 int fva_sparse_attn(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev, int v_dtype,
                     const fva_mask* mask, void* o_dev, float scale, int32_t* dev_status, fva_stream_t stream) {
-  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, mask, o_dev, scale, false, 0, 0, true, dev_status, stream);
+  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, mask, o_dev, nullptr, scale, false, 0, 0, true, dev_status, stream);
 }
 
 int fva_sparse_attn_range(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev, int v_dtype,
                           const fva_mask* mask, void* o_dev, float scale, int64_t first_slot, int64_t n_slots,
                           int32_t* dev_status, fva_stream_t stream) {
-  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, mask, o_dev, scale, false, first_slot, n_slots, false,
+  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, mask, o_dev, nullptr, scale, false, first_slot, n_slots, false,
                      dev_status, stream);
 }
 
 int fva_dense_attn(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev, int v_dtype,
                    void* o_dev, float scale, int32_t* dev_status, fva_stream_t stream) {
-  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, nullptr, o_dev, scale, true, 0, 0, true, dev_status, stream);
+  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, nullptr, o_dev, nullptr, scale, true, 0, 0, true, dev_status, stream);
+}
+
+int fva_sparse_attn_lse(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev, int v_dtype,
+                        const fva_mask* mask, void* o_dev, float* lse_dev, float scale, int32_t* dev_status,
+                        fva_stream_t stream) {
+  if (!lse_dev) return FVA_ERR_INVALID_ARG;
+  return attn_common(s, q_dev, k_dev, v_dev, v_dtype, mask, o_dev, lse_dev, scale, false, 0, 0, true, dev_status,
+                     stream);
+}
+
+// Shapes that the gradient takes: the attention's head dims, int32 list offsets, and the
+// ordering kernel's one int32 per tile of a head in shared memory.
+static bool bwd_shape_supported(const Dims& D) {
+  if (D.d != 64 && D.d != 128 && !(D.esize == 4 && D.d == 32)) return false;
+  return D.BH * D.nB * D.nB <= 0x7fffffffLL && D.nPairs * 4 <= 200 * 1024;
+}
+
+static size_t bwd_scratch_layout(const Dims& D, void* ws, BwdScratch* out) {
+  Carver c{static_cast<uint8_t*>(ws), 0};
+  BwdScratch b{};
+  b.delta = c.take<float>(static_cast<size_t>(D.BH * D.N) * 4);
+  b.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
+  b.route_t.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
+  b.route_t.row_cnt = c.take<int32_t>(static_cast<size_t>(D.rows) * 4);
+  b.route_t.head_load = c.take<int64_t>(static_cast<size_t>(D.BH) * 8);
+  b.mask_t.capacity = D.BH * D.nB * D.nB;
+  b.mask_t.tile_capacity = D.BH * D.nPairs * D.nB;
+  b.mask_t.row_ptr = c.take<int32_t>(static_cast<size_t>(D.rows + 1) * 4);
+  b.mask_t.head_kept = c.take<int64_t>(static_cast<size_t>(D.BH) * 8);
+  b.mask_t.tile_ptr = c.take<int32_t>(static_cast<size_t>(D.tiles + 1) * 4);
+  b.mask_t.tile_cost = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
+  b.mask_t.worklist = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
+  b.mask_t.tile_col = c.take<int32_t>(static_cast<size_t>(b.mask_t.tile_capacity) * 4);
+  if (out) *out = b;
+  return c.off;
+}
+
+size_t fva_sparse_attn_bwd_workspace_bytes(const fva_shape* s) {
+  Dims D;
+  if (!make_dims(s, &D) || !bwd_shape_supported(D)) return 0;
+  return bwd_scratch_layout(D, nullptr, nullptr);
+}
+
+int fva_sparse_attn_bwd(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev, const void* o_dev,
+                        const void* d_o_dev, const float* lse_dev, const fva_mask* mask, void* dq_dev, void* dk_dev,
+                        void* dv_dev, float scale, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
+                        fva_stream_t stream) {
+  Dims D;
+  const void* in[5] = {q_dev, k_dev, v_dev, o_dev, d_o_dev};
+  void* out[3] = {dq_dev, dk_dev, dv_dev};
+  if (!s || !lse_dev || !mask || !workspace_dev) return FVA_ERR_INVALID_ARG;
+  for (const void* p : in)
+    if (!p) return FVA_ERR_INVALID_ARG;
+  for (const void* p : out)
+    if (!p) return FVA_ERR_INVALID_ARG;
+  if (!mask->row_ptr || !mask->col_idx || !mask->tile_ptr || !mask->tile_col || !mask->worklist)
+    return FVA_ERR_INVALID_ARG;
+  if (!make_dims(s, &D) || !bwd_shape_supported(D)) return FVA_ERR_UNSUPPORTED_SHAPE;
+  for (int i = 0; i < 3; ++i) {
+    for (const void* p : in)
+      if (p == out[i]) return FVA_ERR_INVALID_ARG;
+    if (out[i] == out[(i + 1) % 3]) return FVA_ERR_INVALID_ARG;
+  }
+  for (const void* p : in)
+    if (!aligned16(p)) return FVA_ERR_ALIGNMENT;
+  for (const void* p : out)
+    if (!aligned16(p)) return FVA_ERR_ALIGNMENT;
+  if (!aligned16(lse_dev) || !aligned16(workspace_dev)) return FVA_ERR_ALIGNMENT;
+  if (workspace_bytes < bwd_scratch_layout(D, nullptr, nullptr)) return FVA_ERR_WORKSPACE;
+  BwdScratch ws;
+  bwd_scratch_layout(D, workspace_dev, &ws);
+  if (!(scale > 0.0f)) scale = 1.0f / sqrtf(static_cast<float>(D.d));
+  const BwdArgs x = {q_dev, k_dev, v_dev, o_dev, d_o_dev, lse_dev, dq_dev, dk_dev, dv_dev, scale};
+  return cuda_status(launch_attn_bwd(D, x, mask, ws, dev_status, stream));
+}
+
+// ---------------------------------------------------------------------------------
+// Paged cache
+// ---------------------------------------------------------------------------------
+static int check_cache(const fva_cache* c, const fva_seqs* q) {
+  if (!c || !q || !c->k || !c->v || !c->key_mean || !q->table || !q->len) return FVA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->Hkv < 1 || q->B < 1 || q->max_blocks < 1) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (c->dtype != FVA_F32 && c->dtype != FVA_BF16 && c->dtype != FVA_F16) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (c->d != 64 && c->d != 128 && !(c->dtype == FVA_F32 && c->d == 32)) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (c->Hkv > 65535 || q->B > 65535 || q->max_blocks > kMaxCacheBlocks) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->key_mean) || !aligned16(c->mass)) return FVA_ERR_ALIGNMENT;
+  return FVA_OK;
+}
+
+// Query rows: H a multiple of Hkv, rows that start on 16 bytes.
+static int check_query(const fva_cache* c, const fva_seqs* q, const void* q_dev, int H, int64_t q_stride) {
+  if (!q_dev) return FVA_ERR_INVALID_ARG;
+  if (H < 1 || H > 65535 || H % c->Hkv != 0) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<int64_t>(q->B) * H > 0x7fffffffLL) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (q_stride < static_cast<int64_t>(H) * c->d) return FVA_ERR_INVALID_ARG;
+  if (!aligned16(q_dev) || q_stride * (c->dtype == FVA_F32 ? 4 : 2) % 16 != 0) return FVA_ERR_ALIGNMENT;
+  return FVA_OK;
+}
+
+int fva_cache_append(const fva_cache* cache, const fva_seqs* seqs, const void* k_new_dev, const void* v_new_dev,
+                     int64_t token_stride, const int32_t* new_ptr_dev, int max_new, int32_t* dev_status,
+                     fva_stream_t stream) {
+  const int rc = check_cache(cache, seqs);
+  if (rc != FVA_OK) return rc;
+  if (!new_ptr_dev || max_new < 0 || max_new > kMaxCacheBlocks * kBlock) return FVA_ERR_INVALID_ARG;
+  if (max_new == 0) return FVA_OK;
+  if (!k_new_dev || !v_new_dev || token_stride < static_cast<int64_t>(cache->Hkv) * cache->d) return FVA_ERR_INVALID_ARG;
+  if (!aligned16(k_new_dev) || !aligned16(v_new_dev) || token_stride * (cache->dtype == FVA_F32 ? 4 : 2) % 16 != 0)
+    return FVA_ERR_ALIGNMENT;
+  return cuda_status(launch_cache_append(cache, seqs, k_new_dev, v_new_dev, token_stride, new_ptr_dev, max_new,
+                                         dev_status, stream));
+}
+
+static bool batch_sizes_ok(const fva_cache* c, int B, int max_blocks) {
+  return c && c->Hkv >= 1 && c->Hkv <= 65535 && c->d >= 1 && B >= 1 && B <= 65535 && max_blocks >= 1 &&
+         max_blocks <= kMaxCacheBlocks;
+}
+
+size_t fva_cache_route_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H) {
+  if (!batch_sizes_ok(cache, B, max_blocks) || H < 1) return 0;
+  return align_up(static_cast<size_t>(B) * H * max_blocks * sizeof(double), 256);
+}
+
+int fva_cache_route(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride, double p,
+                    int k_floor, int n_recent, float scale, int32_t* kept_dev, int32_t* n_kept_dev,
+                    void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream) {
+  int rc = check_cache(cache, seqs);
+  if (rc == FVA_OK) rc = check_query(cache, seqs, q_dev, H, q_stride);
+  if (rc != FVA_OK) return rc;
+  if (!(p > 0.0 && p <= 1.0) || k_floor < 0 || n_recent < 0 || !kept_dev || !n_kept_dev || !workspace_dev)
+    return FVA_ERR_INVALID_ARG;
+  if (workspace_bytes < fva_cache_route_workspace_bytes(cache, seqs->B, seqs->max_blocks, H)) return FVA_ERR_WORKSPACE;
+  if (!aligned16(workspace_dev) || !aligned16(kept_dev) || !aligned16(n_kept_dev)) return FVA_ERR_ALIGNMENT;
+  const double sc = scale > 0.0f ? static_cast<double>(scale) : 1.0 / sqrt(static_cast<double>(cache->d));
+  return cuda_status(launch_cache_route(cache, seqs, q_dev, H, q_stride, p, k_floor, n_recent, sc, kept_dev, n_kept_dev,
+                                        static_cast<double*>(workspace_dev), dev_status, stream));
+}
+
+static size_t cache_attn_layout(const fva_cache* c, int B, int max_blocks, int H, int accumulate, void* ws,
+                                CacheAttnScratch* out) {
+  Carver k{static_cast<uint8_t*>(ws), 0};
+  CacheAttnScratch a{};
+  a.part = k.take<float>(cache_attn_part_floats(c->d) * sizeof(float));
+  if (accumulate) {
+    a.lse = k.take<float>(static_cast<size_t>(B) * H * sizeof(float));
+    a.scores = k.take<float>(static_cast<size_t>(B) * H * max_blocks * kBlock * sizeof(float));
+  }
+  if (out) *out = a;
+  return k.off;
+}
+
+size_t fva_cache_attn_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H, int accumulate) {
+  if (!batch_sizes_ok(cache, B, max_blocks) || H < 1) return 0;
+  return cache_attn_layout(cache, B, max_blocks, H, accumulate, nullptr, nullptr);
+}
+
+int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride,
+                   const int32_t* kept_dev, const int32_t* n_kept_dev, void* o_dev, float* lse_dev, float scale,
+                   int accumulate, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
+                   fva_stream_t stream) {
+  int rc = check_cache(cache, seqs);
+  if (rc == FVA_OK) rc = check_query(cache, seqs, q_dev, H, q_stride);
+  if (rc != FVA_OK) return rc;
+  if ((kept_dev == nullptr) != (n_kept_dev == nullptr) || !o_dev || !workspace_dev || (accumulate && !cache->mass) ||
+      o_dev == q_dev)
+    return FVA_ERR_INVALID_ARG;
+  if (workspace_bytes < cache_attn_layout(cache, seqs->B, seqs->max_blocks, H, accumulate, nullptr, nullptr))
+    return FVA_ERR_WORKSPACE;
+  if (!aligned16(workspace_dev) || !aligned16(kept_dev) || !aligned16(n_kept_dev) || !aligned16(o_dev) || !aligned16(lse_dev))
+    return FVA_ERR_ALIGNMENT;
+  CacheAttnScratch ws;
+  cache_attn_layout(cache, seqs->B, seqs->max_blocks, H, accumulate, workspace_dev, &ws);
+  if (!(scale > 0.0f)) scale = 1.0f / sqrtf(static_cast<float>(cache->d));
+  return cuda_status(launch_cache_attn(cache, seqs, q_dev, H, q_stride, kept_dev, n_kept_dev, o_dev, lse_dev, scale,
+                                       accumulate, ws, dev_status, stream));
+}
+
+size_t fva_cache_evict_workspace_bytes(const fva_cache* cache, int B, int max_blocks) {
+  return batch_sizes_ok(cache, B, max_blocks) ? 256 : 0;
+}
+
+int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int n_sink, int n_recent,
+                    const int32_t* dst_table_dev, int dst_max_blocks, int32_t* kept_dev, int32_t* new_len_dev,
+                    void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream) {
+  const int rc = check_cache(cache, seqs);
+  if (rc != FVA_OK) return rc;
+  if (!cache->mass || !dst_table_dev || !kept_dev || !new_len_dev || !workspace_dev) return FVA_ERR_INVALID_ARG;
+  if (keep < 1 || keep > kMaxCacheBlocks * kBlock || n_sink < 0 || n_recent < 0 ||
+      static_cast<int64_t>(n_sink) + n_recent > keep)
+    return FVA_ERR_INVALID_ARG;
+  if (dst_max_blocks < (keep + kBlock - 1) / kBlock) return FVA_ERR_CAPACITY;
+  if (workspace_bytes < fva_cache_evict_workspace_bytes(cache, seqs->B, seqs->max_blocks)) return FVA_ERR_WORKSPACE;
+  if (!aligned16(workspace_dev)) return FVA_ERR_ALIGNMENT;
+  return cuda_status(launch_cache_evict(cache, seqs, keep, n_sink, n_recent, dst_table_dev, dst_max_blocks, kept_dev,
+                                        new_len_dev, dev_status, stream));
 }
 
 }  // extern "C"

@@ -57,8 +57,9 @@ cudaError_t launch_tiles_from_bits(const Dims& D, const fva_mask* m, int order, 
                                    const int32_t* row_cnt, int write_rows, int32_t* dev_status, cudaStream_t st);
 
 // Sparse: the CTAs of work-list slots [first_slot, first_slot + n_slots); dense: every tile.
+// lse (may be null): float32 [BH, N], the rows' log-sum-exp.
 cudaError_t launch_attn_bf16(const Dims& D, const void* q, const void* k, const void* v, bool v_f16,
-                             const fva_mask* m, bool dense, void* o, float scale, int64_t first_slot,
+                             const fva_mask* m, bool dense, void* o, float* lse, float scale, int64_t first_slot,
                              int64_t n_slots, int32_t* dev_status, cudaStream_t st);
 uint64_t attn_wait_limit_ns();
 uint32_t attn_diag_flags();
@@ -66,8 +67,23 @@ void set_attn_diagnostics(uint64_t wait_limit_ns, uint32_t flags);
 void set_attn_cta_trace(int64_t* trace, int64_t capacity_ctas);
 bool attn_cta_trace_fits(int64_t ctas);
 cudaError_t launch_attn_f32(const Dims& D, const float* q, const float* k, const float* v,
-                            const int32_t* row_ptr, const int32_t* col_idx, bool dense, float* o,
+                            const int32_t* row_ptr, const int32_t* col_idx, bool dense, float* o, float* lse,
                             float scale, cudaStream_t st);
+
+struct BwdArgs {
+  const void *q, *k, *v, *o, *d_o;
+  const float* lse;
+  void *dq, *dk, *dv;
+  float scale;
+};
+struct BwdScratch {
+  float* delta;          // [BH, N] rowsum(dO O)
+  uint32_t* bits;        // [rows, nWords] the mask, by query row
+  RouteScratch route_t;  // bits by key row, their counts, head loads
+  fva_mask mask_t;       // the transposed lists (no col_idx)
+};
+cudaError_t launch_attn_bwd(const Dims& D, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+                            int32_t* dev_status, cudaStream_t st);
 
 // ---------------------------------------------------------------------------------
 // device helpers

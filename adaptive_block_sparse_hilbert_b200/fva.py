@@ -63,6 +63,16 @@ class fva_rlb_move(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("gain_ms", ctypes.c_double)]
 
 
+class fva_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("key_mean", ctypes.c_void_p), ("mass", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class fva_seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32)]
+
+
 class FvaError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {status_string(status)} ({status})")
@@ -76,6 +86,7 @@ def _load():
     P = ctypes.c_void_p
     S = ctypes.POINTER(fva_shape)
     M = ctypes.POINTER(fva_mask)
+    C, Q = ctypes.POINTER(fva_cache), ctypes.POINTER(fva_seqs)
     i32, i64, sz, dbl, flt = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_double, ctypes.c_float
     sig = {
         "fva_status_string": (ctypes.c_char_p, [i32]),
@@ -106,6 +117,16 @@ def _load():
         "fva_sparse_attn": (i32, [S, P, P, P, i32, M, P, flt, P, P]),
         "fva_sparse_attn_range": (i32, [S, P, P, P, i32, M, P, flt, i64, i64, P, P]),
         "fva_dense_attn": (i32, [S, P, P, P, i32, P, flt, P, P]),
+        "fva_sparse_attn_lse": (i32, [S, P, P, P, i32, M, P, P, flt, P, P]),
+        "fva_sparse_attn_bwd_workspace_bytes": (sz, [S]),
+        "fva_sparse_attn_bwd": (i32, [S, P, P, P, P, P, P, M, P, P, P, flt, P, sz, P, P]),
+        "fva_cache_append": (i32, [C, Q, P, P, i64, P, i32, P, P]),
+        "fva_cache_route_workspace_bytes": (sz, [C, i32, i32, i32]),
+        "fva_cache_route": (i32, [C, Q, P, i32, i64, dbl, i32, i32, flt, P, P, P, sz, P, P]),
+        "fva_cache_attn_workspace_bytes": (sz, [C, i32, i32, i32, i32]),
+        "fva_cache_attn": (i32, [C, Q, P, i32, i64, P, P, P, P, flt, i32, P, sz, P, P]),
+        "fva_cache_evict_workspace_bytes": (sz, [C, i32, i32]),
+        "fva_cache_evict": (i32, [C, Q, i32, i32, i32, P, i32, P, P, P, sz, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -120,7 +141,10 @@ EXPORTED = (
     "fva_tile_capacity", "fva_route_workspace_bytes", "fva_tiles_workspace_bytes", "fva_hilbert_perm", "fva_reorder",
     "fva_pool", "fva_route", "fva_build_tiles", "fva_sparse_attn", "fva_dense_attn", "fva_route_noalloc",
     "fva_set_cta_trace", "fva_rlb_plan", "fva_curve_perm", "fva_sasa_budgets", "fva_sasa_workspace_bytes",
-    "fva_sasa_augment", "fva_copy_strided", "fva_sparse_attn_range",
+    "fva_sasa_augment", "fva_copy_strided", "fva_sparse_attn_range", "fva_sparse_attn_lse",
+    "fva_sparse_attn_bwd_workspace_bytes", "fva_sparse_attn_bwd", "fva_cache_append", "fva_cache_route_workspace_bytes",
+    "fva_cache_route", "fva_cache_attn_workspace_bytes", "fva_cache_attn", "fva_cache_evict_workspace_bytes",
+    "fva_cache_evict",
 )
 
 
@@ -356,6 +380,202 @@ def fva_dense_attn(s, q, k, v, o, scale=0.0, dev_status=None, stream=None, v_dty
     vd = _dtype_code(v) if v_dtype is None else int(v_dtype)
     _check("fva_dense_attn", _lib.fva_dense_attn(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), vd, _ptr(o),
                                                  float(scale), _ptr(dev_status), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------ training
+
+def _expect(fn, what, t, shape, dtype, device=None, last_dims=None):
+    """Shape, type, device and contiguity of one tensor argument; `last_dims`: only that many
+    trailing dimensions need be contiguous (the first may have a stride of its own)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {what} has type {t.dtype}, expected {dtype}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{fn}: {what} is on {t.device}, expected {device or 'a CUDA device'}")
+    if last_dims is None:
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {what} is not contiguous")
+    elif t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{fn}: a row of {what} is not contiguous")
+
+
+def _on(device):
+    """The call's launches go to the tensors' device, whichever device is current."""
+    return torch.cuda.device(device)
+
+
+def _stream_on(stream, device):
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+
+
+def _shape_dtype(s):
+    return torch.bfloat16 if s.dtype == FVA_BF16 else torch.float32
+
+
+def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=None, stream=None):
+    """fva_sparse_attn that also writes lse (float32 [B, H, N]), what its gradient needs."""
+    fn, N = "fva_sparse_attn_lse", fva_num_tokens(s)
+    four, dev = (s.B, s.H, N, s.d), q.device
+    for what, t in (("q", q), ("k", k), ("o", o)):
+        _expect(fn, what, t, four, _shape_dtype(s), dev)
+    _expect(fn, "v", v, four, v.dtype if v.dtype in (torch.float16, torch.bfloat16) else _shape_dtype(s), dev)
+    _expect(fn, "lse", lse, four[:3], torch.float32, dev)
+    m = mask.c()
+    with _on(dev):
+        _check(fn, _lib.fva_sparse_attn_lse(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dtype_code(v), ctypes.byref(m),
+                                            _ptr(o), _ptr(lse), float(scale), _ptr(dev_status), _stream_on(stream, dev)))
+
+
+def fva_sparse_attn_bwd_workspace_bytes(s): return _lib.fva_sparse_attn_bwd_workspace_bytes(ctypes.byref(s))
+
+
+def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspace, scale=0.0, dev_status=None,
+                        stream=None):
+    """Gradients of block-sparse attention: everything [B, H, N, d] in Hilbert order and of the
+    shape's type (V too), lse as fva_sparse_attn_lse wrote it."""
+    fn, N = "fva_sparse_attn_bwd", fva_num_tokens(s)
+    four, dev, dt = (s.B, s.H, N, s.d), q.device, _shape_dtype(s)
+    for what, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
+        _expect(fn, what, t, four, dt, dev)
+    _expect(fn, "lse", lse, four[:3], torch.float32, dev)
+    m = mask.c()
+    with _on(dev):
+        _check(fn, _lib.fva_sparse_attn_bwd(
+            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), ctypes.byref(m), _ptr(dq), _ptr(dk),
+            _ptr(dv), float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+            _stream_on(stream, dev)))
+
+
+# ------------------------------------------------------------------------------ serving
+
+@dataclasses.dataclass
+class Cache:
+    """Device buffers of one paged key/value cache (owned by torch; passed to libfva as fva_cache)."""
+
+    k: torch.Tensor         # [n_pages, Hkv, 64, d]
+    v: torch.Tensor
+    key_mean: torch.Tensor  # float32 [n_pages, Hkv, d]
+    mass: torch.Tensor | None = None  # float32 [n_pages, Hkv, 64]
+
+    def __post_init__(self):
+        n, Hkv, _, d = self.k.shape
+        dev = self.k.device
+        if self.k.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError(f"Cache: k has type {self.k.dtype}")
+        _expect("Cache", "k", self.k, (n, Hkv, BLOCK, d), self.k.dtype, dev)
+        _expect("Cache", "v", self.v, (n, Hkv, BLOCK, d), self.k.dtype, dev)
+        _expect("Cache", "key_mean", self.key_mean, (n, Hkv, d), torch.float32, dev)
+        if self.mass is not None:
+            _expect("Cache", "mass", self.mass, (n, Hkv, BLOCK), torch.float32, dev)
+        self._c = fva_cache(self.k.data_ptr(), self.v.data_ptr(), self.key_mean.data_ptr(),
+                            None if self.mass is None else self.mass.data_ptr(), n, Hkv, d, _dtype_code(self.k))
+
+    @staticmethod
+    def allocate(n_pages, Hkv, d, dtype=torch.bfloat16, device="cuda", mass=True) -> "Cache":
+        return Cache(torch.empty((n_pages, Hkv, BLOCK, d), dtype=dtype, device=device),
+                     torch.empty((n_pages, Hkv, BLOCK, d), dtype=dtype, device=device),
+                     torch.empty((n_pages, Hkv, d), dtype=torch.float32, device=device),
+                     torch.zeros((n_pages, Hkv, BLOCK), dtype=torch.float32, device=device) if mass else None)
+
+    def c(self) -> fva_cache:
+        return self._c
+
+
+def _seqs(fn, cache, table, length):
+    dev = cache.k.device
+    B, width = table.shape
+    _expect(fn, "table", table, (B, width), torch.int32, dev)
+    _expect(fn, "length", length, (B,), torch.int32, dev)
+    return fva_seqs(table.data_ptr(), length.data_ptr(), B, width)
+
+
+def fva_cache_append(cache: Cache, table, length, k_new, v_new, new_ptr, max_new, dev_status=None, stream=None):
+    """Append tokens to their sequences; `length` holds the lengths after the append. k_new and
+    v_new are [tokens, Hkv, d]; their rows may be slices of wider ones, with the same stride."""
+    fn, dev = "fva_cache_append", cache.k.device
+    c, q = cache.c(), _seqs(fn, cache, table, length)
+    shape = (k_new.shape[0], c.Hkv, c.d)
+    _expect(fn, "k_new", k_new, shape, cache.k.dtype, dev, 2)
+    _expect(fn, "v_new", v_new, shape, cache.k.dtype, dev, 2)
+    _expect(fn, "new_ptr", new_ptr, (q.B + 1,), torch.int32, dev)
+    if k_new.stride(0) != v_new.stride(0) and shape[0] > 1:
+        raise ValueError(f"{fn}: k_new and v_new have different token strides")
+    stride = max(k_new.stride(0), c.Hkv * c.d) if shape[0] > 1 else c.Hkv * c.d
+    with _on(dev):
+        _check(fn, _lib.fva_cache_append(ctypes.byref(c), ctypes.byref(q), _ptr(k_new), _ptr(v_new), stride,
+                                         _ptr(new_ptr), int(max_new), _ptr(dev_status), _stream_on(stream, dev)))
+
+
+def fva_cache_route_workspace_bytes(cache, B, max_blocks, H):
+    return _lib.fva_cache_route_workspace_bytes(ctypes.byref(cache.c()), int(B), int(max_blocks), int(H))
+
+
+def _query(fn, cache, B, q):
+    c = cache.c()
+    _expect(fn, "q", q, (B, q.shape[1], c.d), cache.k.dtype, cache.k.device, 2)
+    return q.shape[1], q.stride(0) if B > 1 else q.shape[1] * c.d
+
+
+def fva_cache_route(cache: Cache, table, length, q, p, k_floor, n_recent, kept, n_kept, workspace, scale=0.0,
+                    dev_status=None, stream=None):
+    """Blocks that each sequence's query token keeps: kept int32 [B, Hkv, max_blocks] ascending,
+    n_kept int32 [B, Hkv]."""
+    fn, dev = "fva_cache_route", cache.k.device
+    c, sq = cache.c(), _seqs(fn, cache, table, length)
+    H, q_stride = _query(fn, cache, sq.B, q)
+    _expect(fn, "kept", kept, (sq.B, c.Hkv, sq.max_blocks), torch.int32, dev)
+    _expect(fn, "n_kept", n_kept, (sq.B, c.Hkv), torch.int32, dev)
+    with _on(dev):
+        _check(fn, _lib.fva_cache_route(
+            ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, float(p), int(k_floor), int(n_recent), float(scale),
+            _ptr(kept), _ptr(n_kept), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+            _stream_on(stream, dev)))
+
+
+def fva_cache_attn_workspace_bytes(cache, B, max_blocks, H, accumulate):
+    return _lib.fva_cache_attn_workspace_bytes(ctypes.byref(cache.c()), int(B), int(max_blocks), int(H), int(accumulate))
+
+
+def fva_cache_attn(cache: Cache, table, length, q, kept, n_kept, o, workspace, lse=None, scale=0.0, accumulate=False,
+                   dev_status=None, stream=None):
+    """Attention of one query token per sequence over its kept blocks (kept and n_kept None:
+    over every block); `accumulate` adds the weights to cache.mass."""
+    fn, dev = "fva_cache_attn", cache.k.device
+    c, sq = cache.c(), _seqs(fn, cache, table, length)
+    H, q_stride = _query(fn, cache, sq.B, q)
+    if kept is not None:
+        _expect(fn, "kept", kept, (sq.B, c.Hkv, sq.max_blocks), torch.int32, dev)
+    if n_kept is not None:
+        _expect(fn, "n_kept", n_kept, (sq.B, c.Hkv), torch.int32, dev)
+    _expect(fn, "o", o, (sq.B, H, c.d), cache.k.dtype, dev)
+    if lse is not None:
+        _expect(fn, "lse", lse, (sq.B, H), torch.float32, dev)
+    with _on(dev):
+        _check(fn, _lib.fva_cache_attn(
+            ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, _ptr(kept), _ptr(n_kept), _ptr(o), _ptr(lse),
+            float(scale), int(bool(accumulate)), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(dev_status), _stream_on(stream, dev)))
+
+
+def fva_cache_evict_workspace_bytes(cache, B, max_blocks):
+    return _lib.fva_cache_evict_workspace_bytes(ctypes.byref(cache.c()), int(B), int(max_blocks))
+
+
+def fva_cache_evict(cache: Cache, table, length, keep, n_sink, n_recent, dst_table, kept, new_len, workspace,
+                    dev_status=None, stream=None):
+    """Keep the `keep` tokens of the most accumulated weight of every sequence and key head, in
+    order, in the pages of dst_table (int32 [B, >= ceil(keep / 64)])."""
+    fn, dev = "fva_cache_evict", cache.k.device
+    c, sq = cache.c(), _seqs(fn, cache, table, length)
+    _expect(fn, "dst_table", dst_table, (sq.B, dst_table.shape[1]), torch.int32, dev)
+    _expect(fn, "kept", kept, (sq.B, c.Hkv, int(keep)), torch.int32, dev)
+    _expect(fn, "new_len", new_len, (sq.B,), torch.int32, dev)
+    with _on(dev):
+        _check(fn, _lib.fva_cache_evict(
+            ctypes.byref(c), ctypes.byref(sq), int(keep), int(n_sink), int(n_recent), _ptr(dst_table), dst_table.shape[1],
+            _ptr(kept), _ptr(new_len), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+            _stream_on(stream, dev)))
 
 
 def call_raw(name, *args):

@@ -4,6 +4,18 @@ libfva entry point.
 
     layer = SparseAttentionLayer(shape, p=0.9, k_floor=4)
     layer.forward(q_bnhd, k_bnhd, v_bnhd, o_bnhd)   # torch CUDA tensors, raster order
+
+A layer made with train=True keeps what its gradient needs, and CachedAttention serves streams
+token by token from a paged cache:
+
+    layer = SparseAttentionLayer(shape, p=0.9, k_floor=4, train=True)
+    layer.forward(q, k, v, o)
+    layer.backward(do, dq, dk, dv)                  # raster order, of the last forward()
+
+    att = CachedAttention(B, H, Hkv, d, n_pages, max_blocks)
+    att.append(k_prompt, v_prompt, counts)          # [tokens, Hkv, d], tokens per sequence
+    att.attend(q, o)                                # [B, H, d]
+    att.evict(keep=4096, n_sink=4, n_recent=256)
 """
 from __future__ import annotations
 
@@ -14,7 +26,8 @@ from . import fva
 
 class SparseAttentionLayer:
     def __init__(self, shape: fva.fva_shape, p: float, k_floor: int, order: int = fva.FVA_ORDER_HEAD_LPT,
-                 device: str = "cuda", v_fp16: bool = True, curve: int = fva.FVA_CURVE_HILBERT):
+                 device: str = "cuda", v_fp16: bool = True, curve: int = fva.FVA_CURVE_HILBERT,
+                 train: bool = False):
         self.shape = shape
         self.p = float(p)
         self.k_floor = int(k_floor)
@@ -41,6 +54,14 @@ class SparseAttentionLayer:
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
         self.curve = int(curve)
+        self.train = bool(train)
+        if self.train:
+            # the gradient's products need V and dO in one 16-bit type, so a layer whose forward
+            # reads V as fp16 keeps it as bf16 too
+            self.vb = torch.empty(bhnd, dtype=dt, device=device) if self.v_fp16 else self.vh
+            self.lse = torch.empty(bhnd[:3], dtype=torch.float32, device=device)
+            self.doh, self.dqh, self.dkh, self.dvh = (torch.empty(bhnd, dtype=dt, device=device) for _ in range(4))
+            self.bwd_workspace = torch.empty(fva.fva_sparse_attn_bwd_workspace_bytes(s), dtype=torch.uint8, device=device)
         fva.fva_curve_perm(s, self.curve, self.perm, self.inv, self.dev_status)
 
     def reorder_inputs(self, q, k, v, stream=None):
@@ -48,12 +69,19 @@ class SparseAttentionLayer:
         fva.fva_reorder(s, q, self.qh, self.pooled_q, self.perm, fva.FVA_FWD, stream)
         fva.fva_reorder(s, k, self.kh, self.pooled_k, self.perm, fva.FVA_FWD, stream)
         fva.fva_reorder(s, v, self.vh, None, self.perm, fva.FVA_FWD_F16 if self.v_fp16 else fva.FVA_FWD, stream)
+        if self.train and self.v_fp16:
+            fva.fva_reorder(s, v, self.vb, None, self.perm, fva.FVA_FWD, stream)
 
     def route(self, stream=None):
         fva.fva_route(self.shape, None, None, self.pooled_q, self.pooled_k, self.p, self.k_floor, self.mask,
                       self.workspace, self.order, self.dev_status, stream)
 
     def attend(self, stream=None, scale: float = 0.0):
+        if self.train:
+            self.scale = scale
+            fva.fva_sparse_attn_lse(self.shape, self.qh, self.kh, self.vh, self.mask, self.oh, self.lse, scale,
+                                    self.dev_status, stream)
+            return
         fva.fva_sparse_attn(self.shape, self.qh, self.kh, self.vh, self.mask, self.oh, scale, self.dev_status, stream)
 
     def restore_output(self, o_out, stream=None):
@@ -65,6 +93,120 @@ class SparseAttentionLayer:
         self.attend(stream)
         self.restore_output(o_out, stream)
         return o_out
+
+    def backward(self, do, dq, dk, dv, stream=None):
+        """Gradients of the last forward() (train=True) for the output gradient `do`; all
+        [B, N, H, d] in raster order. The routed mask is a constant of the gradient."""
+        if not self.train:
+            raise RuntimeError("SparseAttentionLayer.backward: the layer was made without train=True")
+        s = self.shape
+        fva.fva_reorder(s, do, self.doh, None, self.perm, fva.FVA_FWD, stream)
+        fva.fva_sparse_attn_bwd(s, self.qh, self.kh, self.vb, self.oh, self.doh, self.lse, self.mask, self.dqh, self.dkh,
+                                self.dvh, self.bwd_workspace, self.scale, self.dev_status, stream)
+        for grad, out in ((self.dqh, dq), (self.dkh, dk), (self.dvh, dv)):
+            fva.fva_reorder(s, grad, out, None, self.perm, fva.FVA_INV, stream)
+        return dq, dk, dv
+
+
+class CachedAttention:
+    """Attention of B streams over a paged key/value cache, one query token per stream and
+    call: append() stores new keys and values, attend() lets every query choose its blocks by
+    Top-p with a Top-k floor and attends over them, evict() cuts the streams to a budget of
+    tokens by accumulated attention weight. Pages are handed out and taken back on the host;
+    every call enqueues on `stream` (default: the current one), so use one stream, or order them.
+
+    append() and evict() change the page table and lengths on the host and copy them to the
+    device; attend() touches only device state and may be captured into a CUDA graph and
+    replayed between them.
+    """
+
+    def __init__(self, B: int, H: int, Hkv: int, d: int, n_pages: int, max_blocks: int, dtype=torch.bfloat16,
+                 p: float = 0.9, k_floor: int = 4, n_recent: int = 1, accumulate: bool = True, device: str = "cuda"):
+        self.B, self.H, self.max_blocks = int(B), int(H), int(max_blocks)
+        self.p, self.k_floor, self.n_recent, self.accumulate = float(p), int(k_floor), int(n_recent), bool(accumulate)
+        self.cache = fva.Cache.allocate(n_pages, Hkv, d, dtype, device, mass=True)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.zeros((B, max_blocks), **i32)
+        self.length = torch.zeros(B, **i32)
+        self.kept = torch.empty((B, Hkv, max_blocks), **i32)
+        self.n_kept = torch.empty((B, Hkv), **i32)
+        self.lse = torch.empty((B, H), dtype=torch.float32, device=device)
+        self.dev_status = torch.zeros(1, **i32)
+
+        def ws(n):
+            return torch.empty(max(16, n), dtype=torch.uint8, device=device)
+        self.route_ws = ws(fva.fva_cache_route_workspace_bytes(self.cache, B, max_blocks, H))
+        self.attn_ws = ws(fva.fva_cache_attn_workspace_bytes(self.cache, B, max_blocks, H, self.accumulate))
+        self.evict_ws = ws(fva.fva_cache_evict_workspace_bytes(self.cache, B, max_blocks))
+        self.free = list(range(n_pages))[::-1]
+        self.pages = [[] for _ in range(B)]   # host copies of the table's rows and the lengths
+        self.lengths = [0] * B
+
+    def _publish(self, stream):
+        rows = torch.zeros((self.B, self.max_blocks), dtype=torch.int32)
+        for b, pages in enumerate(self.pages):
+            rows[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
+        with torch.cuda.device(self.table.device), torch.cuda.stream(stream):
+            self.table.copy_(rows)
+            self.length.copy_(torch.tensor(self.lengths, dtype=torch.int32))
+
+    def _stream(self, stream):
+        return torch.cuda.current_stream(self.table.device) if stream is None else stream
+
+    def append(self, k_new, v_new, counts, stream=None):
+        """k_new, v_new [sum(counts), Hkv, d]: counts[b] new tokens for stream b."""
+        st = self._stream(stream)
+        counts = [int(n) for n in counts]
+        if len(counts) != self.B or min(counts) < 0 or sum(counts) != k_new.shape[0]:
+            raise ValueError(f"CachedAttention.append: {counts} does not share out {k_new.shape[0]} tokens")
+        need = [-(-(n + c) // fva.BLOCK) - len(p) for n, c, p in zip(self.lengths, counts, self.pages)]
+        if any(len(p) + n > self.max_blocks for p, n in zip(self.pages, need)):
+            raise ValueError("CachedAttention.append: a stream would outgrow max_blocks")
+        if sum(need) > len(self.free):
+            raise RuntimeError(f"CachedAttention.append: {sum(need)} pages needed, {len(self.free)} free")
+        for b, n in enumerate(need):
+            self.pages[b] += [self.free.pop() for _ in range(n)]
+            self.lengths[b] += counts[b]
+        self._publish(st)
+        ptr = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+        with torch.cuda.device(self.table.device), torch.cuda.stream(st):
+            new_ptr = ptr.to(self.table.device)
+            fva.fva_cache_append(self.cache, self.table, self.length, k_new, v_new, new_ptr, max(counts), self.dev_status,
+                                 st)
+
+    def attend(self, q, o, stream=None, scale: float = 0.0):
+        """o [B, H, d] = attention of the query tokens q [B, H, d]; the choice is left in
+        kept / n_kept, the softmax's log-sum-exp in lse."""
+        fva.fva_cache_route(self.cache, self.table, self.length, q, self.p, self.k_floor, self.n_recent, self.kept,
+                            self.n_kept, self.route_ws, scale, self.dev_status, stream)
+        fva.fva_cache_attn(self.cache, self.table, self.length, q, self.kept, self.n_kept, o, self.attn_ws, self.lse,
+                           scale, self.accumulate, self.dev_status, stream)
+        return o
+
+    def evict(self, keep: int, n_sink: int = 4, n_recent: int = 64, stream=None):
+        """Cut every stream to at most `keep` tokens; returns the kept tokens' old positions
+        (int32 [B, Hkv, keep], -1 behind them). Their old pages are free afterwards."""
+        st = self._stream(stream)
+        room = -(-int(keep) // fva.BLOCK)
+        after = [min(n, int(keep)) for n in self.lengths]
+        need = [-(-n // fva.BLOCK) for n in after]
+        if sum(need) > len(self.free):
+            raise RuntimeError(f"CachedAttention.evict: {sum(need)} pages needed, {len(self.free)} free")
+        fresh = [[self.free.pop() for _ in range(n)] for n in need]
+        rows = torch.full((self.B, room), -1, dtype=torch.int32)
+        for b, pages in enumerate(fresh):
+            rows[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
+        with torch.cuda.device(self.table.device), torch.cuda.stream(st):
+            dst = rows.to(self.table.device)
+            kept = torch.empty((self.B, self.cache.k.shape[1], int(keep)), dtype=torch.int32, device=dst.device)
+            new_len = torch.empty_like(self.length)
+            fva.fva_cache_evict(self.cache, self.table, self.length, keep, n_sink, n_recent, dst, kept, new_len,
+                                self.evict_ws, self.dev_status, st)
+        for b, pages in enumerate(fresh):
+            self.free += self.pages[b][::-1]
+            self.pages[b], self.lengths[b] = pages, after[b]
+        self._publish(st)
+        return kept
 
 
 def ramp_sizes(H: int, steady: int = 4):

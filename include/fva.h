@@ -293,6 +293,142 @@ FVA_API int fva_dense_attn(const fva_shape* s, const void* q_dev, const void* k_
                            int v_dtype, void* o_dev, float scale, int32_t* dev_status, fva_stream_t stream);
 
 /*
+ * Training: the forward that keeps what its gradient needs, and the gradient.
+ *
+ * fva_sparse_attn_lse is fva_sparse_attn that also writes lse_dev, float32 [B, H, N]: the
+ * natural logarithm of each query row's softmax denominator, ln sum_j exp(scale * q_i . k_j)
+ * over the valid keys of its kept blocks; -infinity for a row that keeps none.
+ *
+ * fva_sparse_attn_bwd: with P_ij = exp(scale * q_i . k_j - lse_i) on kept blocks, 0 elsewhere,
+ *   dP = dO V^T,  D_i = sum_c dO_ic O_ic,  dS_ij = P_ij (dP_ij - D_i),
+ *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
+ * All of q, k, v, o, d_o, dq, dk, dv are [B, H, N, d] in Hilbert order, dtype s->dtype (V too:
+ * a bf16 layer gives its V as bf16 here even when its forward read an fp16 V); lse as above.
+ *   FVA_BF16 (tensor cores, d in {64, 128}): fp32 accumulation; P and dS are rounded to bf16
+ *     for their products, the gradients to bf16 once.
+ *   FVA_F32 (CUDA cores, d in {32, 64, 128}): fp32 throughout.
+ * A row that keeps no block has dQ = 0; a key block that no row keeps has dK = dV = 0. Sums
+ * run in a fixed order (no atomics): equal inputs give equal bits.
+ * Reads mask->row_ptr, col_idx, tile_ptr, tile_col and worklist, of a mask that fva_route,
+ * fva_sasa_augment or fva_build_tiles filled; the transposed lists are built in the workspace
+ * (fva_sparse_attn_bwd_workspace_bytes, 16-byte aligned; calls that may overlap need one each,
+ * captured graphs that may run at once among them). The gradients must not overlap each other
+ * or any input. scale <= 0 selects 1/sqrt(d), and has to be the forward's.
+ * Limits: B*H*nB*nB <= 2^31 - 1, nPairs <= 51200.
+ */
+FVA_API int fva_sparse_attn_lse(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev,
+                                int v_dtype, const fva_mask* mask, void* o_dev, float* lse_dev, float scale,
+                                int32_t* dev_status, fva_stream_t stream);
+/* 0 when the shape is outside the limits above. */
+FVA_API size_t fva_sparse_attn_bwd_workspace_bytes(const fva_shape* s);
+FVA_API int fva_sparse_attn_bwd(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev,
+                                const void* o_dev, const void* d_o_dev, const float* lse_dev, const fva_mask* mask,
+                                void* dq_dev, void* dk_dev, void* dv_dev, float scale, void* workspace_dev,
+                                size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream);
+
+/*
+ * Serving: a paged key/value cache, and attention of one query token per sequence over the
+ * cache blocks that the token selects for itself.
+ *
+ * A page holds one block (64 tokens) of one sequence for every key head:
+ *   k, v      [n_pages, Hkv, 64, d] of dtype (FVA_BF16, FVA_F16 or FVA_F32)
+ *   key_mean  float32 [n_pages, Hkv, d]: the mean of the page's valid keys (written by
+ *             fva_cache_append and fva_cache_evict, read by fva_cache_route)
+ *   mass      float32 [n_pages, Hkv, 64]: accumulated attention weight of every token;
+ *             may be NULL where no call accumulates or evicts
+ * d in {64, 128}, for FVA_F32 {32, 64, 128}; Hkv <= 65535; n_pages <= 2^31 - 1.
+ * A batch of sequences:
+ *   table int32 [B, max_blocks]: token t of sequence b is in page table[b][t / 64], slot t % 64;
+ *   len   int32 [B]: tokens of each sequence, 0 <= len[b] <= 64 * max_blocks (0: an empty one).
+ * Table entries behind a sequence's last block are not read. Slots behind len[b] in its last
+ * page may hold anything, NaN included. A page id outside [0, n_pages), or a length outside
+ * its range, sets FVA_DEVERR_BAD_LIST in dev_status; the page is then skipped, the length
+ * clamped. 1 <= B <= 65535, 1 <= max_blocks <= 16384 (2^20 tokens).
+ */
+typedef struct fva_cache {
+  void* k;
+  void* v;
+  float* key_mean;
+  float* mass;
+  int32_t n_pages, Hkv, d, dtype;
+} fva_cache;
+
+typedef struct fva_seqs {
+  const int32_t* table;
+  const int32_t* len;
+  int32_t B, max_blocks;
+} fva_seqs;
+
+/*
+ * Append: the tokens new_ptr[b] .. new_ptr[b+1] - 1 of k_new / v_new become the last tokens of
+ * sequence b, whose length AFTER the append is seqs->len[b]; the touched pages' key_mean (the
+ * sum of the page's valid keys in float64, divided, rounded once) is rewritten, and the new
+ * tokens' mass, if the cache has one, set to 0.
+ *   k_new, v_new: rows [Hkv, d] of the cache's dtype, token_stride elements apart (>= Hkv*d;
+ *     token_stride * element size a multiple of 16): slices of a fused projection's output fit;
+ *   new_ptr_dev: int32 [B + 1], ascending from 0; max_new >= the largest count (a sequence with
+ *     more, or with more than its length, sets FVA_DEVERR_BAD_LIST and is left unchanged).
+ * Two sequences of one call may not share a page that the call writes.
+ */
+FVA_API int fva_cache_append(const fva_cache* cache, const fva_seqs* seqs, const void* k_new_dev,
+                             const void* v_new_dev, int64_t token_stride, const int32_t* new_ptr_dev, int max_new,
+                             int32_t* dev_status, fva_stream_t stream);
+
+/*
+ * Routing of single queries: Top-p with a Top-k floor, as fva_route does for query blocks, for
+ * one query token per sequence. q [B, H, d] (rows q_stride elements apart, >= H*d, q_stride *
+ * element size a multiple of 16) of the cache's dtype; the H / Hkv query heads of a key head
+ * select together:
+ *   s_hb = scale * q_h . key_mean[b]  (float64),   P_b = mean over the group's heads of softmax_b(s_hb);
+ *   blocks by P descending, ties to the lower index; the shortest prefix whose mass reaches p
+ *   (p = 1: all blocks) and that has at least min(k_floor, blocks) entries is kept, and the last
+ *   n_recent blocks of the sequence whatever their score.
+ * Cumulative masses are summed exactly in 2^-52 fixed point, as in fva_route.
+ * kept_dev: int32 [B, Hkv, max_blocks], the kept blocks ascending, -1 behind them; n_kept_dev:
+ * int32 [B, Hkv]. scale <= 0 selects 1/sqrt(d) in float64. H a multiple of Hkv, H <= 65535.
+ * A NaN in a group's scores leaves no order: the group keeps every block.
+ */
+FVA_API size_t fva_cache_route_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H);
+FVA_API int fva_cache_route(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride,
+                            double p, int k_floor, int n_recent, float scale, int32_t* kept_dev, int32_t* n_kept_dev,
+                            void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream);
+
+/*
+ * Attention of single queries over the kept blocks of their sequences (kept_dev / n_kept_dev as
+ * fva_cache_route writes them, or both NULL: every block):
+ *   o_h = sum_j softmax_j(scale * q_h . k_j) v_j   over the valid tokens j of the kept blocks.
+ * o [B, H, d] contiguous, of the cache's dtype; lse_dev, optional: float32 [B, H], the natural
+ * logarithm of the softmax denominator. An empty sequence or list gives o = 0, lse = -infinity.
+ * accumulate != 0 adds every token's attention weight, summed over the query heads of its key
+ * head, to cache->mass (sequences of one call that share pages add atomically: the sum is then
+ * right but its rounding order is not fixed; otherwise equal inputs give equal bits).
+ * An entry outside the sequence's blocks sets FVA_DEVERR_BAD_LIST and is skipped.
+ * Every softmax statistic and sum is float32; scale <= 0 selects 1/sqrt(d).
+ */
+FVA_API size_t fva_cache_attn_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H, int accumulate);
+FVA_API int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride,
+                           const int32_t* kept_dev, const int32_t* n_kept_dev, void* o_dev, float* lse_dev, float scale,
+                           int accumulate, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
+                           fva_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: each sequence and key head keeps `keep` tokens
+ * (all of them when it has no more): its first n_sink, its last n_recent, and of the others
+ * those of the largest mass, the earlier token on ties (NaN counts as the lowest). The kept
+ * tokens' keys, values and masses are copied, in their order, into the pages of dst_table
+ * (int32 [B, dst_max_blocks], dst_max_blocks >= ceil(keep / 64)), whose key_mean is written;
+ * the source pages are left as they were, and so are the slots behind the last token.
+ * kept_dev: int32 [B, Hkv, keep], the kept tokens' old positions, -1 behind them; new_len_dev:
+ * int32 [B], min(len, keep). n_sink + n_recent <= keep, 1 <= keep <= 2^20. A destination page
+ * must not be a source page of the call (of its own sequence: FVA_DEVERR_BAD_LIST, and the
+ * page is not written) nor be named twice.
+ */
+FVA_API size_t fva_cache_evict_workspace_bytes(const fva_cache* cache, int B, int max_blocks);
+FVA_API int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int n_sink, int n_recent,
+                            const int32_t* dst_table_dev, int dst_max_blocks, int32_t* kept_dev, int32_t* new_len_dev,
+                            void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream);
+
+/*
  * Routing without a caller-provided workspace. The pages have no counterpart of this
  * entry point; it exists for callers that cannot allocate device memory: a plugin inside
  * a host application whose allocator owns all device memory, a service that forbids
