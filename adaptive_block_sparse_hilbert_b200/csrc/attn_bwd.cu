@@ -1,5 +1,5 @@
-// Gradient of block-sparse attention: the parts that every element type shares (transposed
-// block lists, D = rowsum(dO O)) and the CUDA-core gradient kernel.
+// Gradient of block-sparse attention: the parts that both element types share (transposed
+// block lists, row statistics) and the CUDA-core kernel for fp32.
 //
 // With P = exp(scale Q K^T - lse) on the kept blocks:
 //   dP = dO V^T,  dS = P (dP - D),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
@@ -52,24 +52,50 @@ __global__ void __launch_bounds__(256) count_bits_kernel(const uint32_t* __restr
 }
 
 // ---------------------------------------------------------------------------------
-// D_i = sum_c dO_ic O_ic: one warp per row
+// Row statistics: -lse in log2 units and -D, D_i = sum_c dO_ic O_ic
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float x, float* o) { *o = x; }
-__device__ __forceinline__ void from_f32(float x, __nv_bfloat16* o) { *o = __float2bfloat16(x); }
-
-template <typename T>
-__global__ void __launch_bounds__(256) row_dot_kernel(const T* __restrict__ o, const T* __restrict__ d_o, int64_t rows,
-                                                      int d, float* __restrict__ delta) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (r >= rows) return;
+// d * sizeof(T) / 16 lanes per row, 16 bytes each; a row without keys (lse = -inf) and the rows
+// past N of the last block get -infinity and 0, so that their P is 0.
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float) {
+  const float* x = reinterpret_cast<const float*>(&a);
+  const float* y = reinterpret_cast<const float*>(&b);
+  return fmaf(x[0], y[0], fmaf(x[1], y[1], fmaf(x[2], y[2], x[3] * y[3])));
+}
+__device__ __forceinline__ float dot16(const uint4& a, const uint4& b, __nv_bfloat16) {
+  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&a);
+  const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&b);
   float s = 0.0f;
-  for (int c = lane; c < d; c += 32) s = fmaf(to_f32(o[r * d + c]), to_f32(d_o[r * d + c]), s);
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  if (lane == 0) delta[r] = s;
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = __bfloat1622float2(x[i]), v = __bfloat1622float2(y[i]);
+    s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+  }
+  return s;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) row_stats_kernel(const T* __restrict__ o, const T* __restrict__ d_o,
+                                                        const float* __restrict__ lse, int64_t rows, int N, int nB,
+                                                        float* __restrict__ stats) {
+  constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16;  // 8, 16 or 32
+  const int64_t r = (blockIdx.x * 256ll + threadIdx.x) / kLanes;  // row of the padded [BH, nB * 64]
+  const int l = threadIdx.x % kLanes;
+  const int64_t bh = r / (static_cast<int64_t>(nB) * kBlock);
+  const int64_t n = r - bh * nB * kBlock;
+  const bool in = r < rows && n < N;
+  float s = 0.0f;
+  if (in) {
+    const int64_t at = (bh * N + n) * kLanes + l;
+    s = dot16(reinterpret_cast<const uint4*>(o)[at], reinterpret_cast<const uint4*>(d_o)[at], T());
+  }
+#pragma unroll
+  for (int k = kLanes / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (l == 0 && r < rows) {
+    const float x = in ? lse[bh * N + n] : -INFINITY;
+    float* out = stats + (r / kBlock) * 128 + r % kBlock;
+    out[0] = x == -INFINITY ? -INFINITY : -1.4426950408889634f * x;
+    out[64] = -s;
+  }
 }
 
 // ---------------------------------------------------------------------------------
@@ -81,14 +107,14 @@ __global__ void __launch_bounds__(256) row_dot_kernel(const T* __restrict__ o, c
 //                                                                     out1 = dV = P^T dO
 // Both form X = a0 b0^T and Y = a1 b1^T (scores and dP, transposed when KV), 4 x 4 values a
 // thread, then accumulate out0 += dS b0 (and out1 += P b1) from the 64 x 64 tiles.
-template <typename T, int D, bool KV>
-__global__ void __launch_bounds__(256) attn_bwd_kernel(const T* __restrict__ a0, const T* __restrict__ a1,
-                                                       const T* __restrict__ b0, const T* __restrict__ b1,
-                                                       const float* __restrict__ lse, const float* __restrict__ delta,
-                                                       const int32_t* __restrict__ tile_ptr,
-                                                       const int32_t* __restrict__ tile_col, T* __restrict__ out0,
-                                                       T* __restrict__ out1, int N, int nB, int nPairs, float scale,
-                                                       int32_t* dev_status) {
+template <int D, bool KV>
+__global__ void __launch_bounds__(256) attn_bwd_f32_kernel(const float* __restrict__ a0, const float* __restrict__ a1,
+                                                           const float* __restrict__ b0, const float* __restrict__ b1,
+                                                           const float* __restrict__ stats,
+                                                           const int32_t* __restrict__ tile_ptr,
+                                                           const int32_t* __restrict__ tile_col,
+                                                           float* __restrict__ out0, float* __restrict__ out1, int N,
+                                                           int nB, int nPairs, float scale, int32_t* dev_status) {
   constexpr int LD = D + 4, LP = kBlock + 1, NC = D / 16;
   extern __shared__ __align__(16) float smem_bwd[];
   float* sA0 = smem_bwd;
@@ -105,21 +131,20 @@ __global__ void __launch_bounds__(256) attn_bwd_kernel(const T* __restrict__ a0,
   const int64_t base = bh * N;
   const int64_t tile = bh * nPairs + (a >> 1);
   const int half = a & 1;
+  const float scale_log2 = scale * 1.4426950408889634f;
 
-  auto load = [&](float* dst, const T* src, int block) {
+  auto load = [&](float* dst, const float* src, int block) {
     for (int i = tid; i < kBlock * D; i += 256) {
       const int r = i / D, c = i % D;
       const int n = block * kBlock + r;
-      dst[r * LD + c] = n < N ? to_f32(src[(base + n) * D + c]) : 0.0f;
+      dst[r * LD + c] = n < N ? src[(base + n) * D + c] : 0.0f;
     }
   };
   auto load_rows = [&](int block) {
     if (tid < kBlock) {
-      const int n = block * kBlock + tid;
-      // a row without keys (lse = -inf) and a row past N contribute nothing
-      const float l = n < N ? lse[base + n] : INFINITY;
-      sL[tid] = l == -INFINITY ? INFINITY : l;
-      sD[tid] = n < N ? delta[base + n] : 0.0f;
+      const float* st = stats + (bh * nB + block) * 128 + tid;
+      sL[tid] = st[0];
+      sD[tid] = st[64];
     }
   };
   load(sA0, a0, a);
@@ -175,9 +200,9 @@ __global__ void __launch_bounds__(256) attn_bwd_kernel(const T* __restrict__ a0,
         const int r = tr + 16 * i, s = tc + 16 * j;
         const int qi = KV ? s : r, key = (KV ? a : blk) * kBlock + (KV ? r : s);
         // keys past N hold zero scores, not -inf: their weight is forced to 0
-        const float p = key < N ? expf(x[i][j] * scale - sL[qi]) : 0.0f;
+        const float p = key < N ? exp2f(fmaf(x[i][j], scale_log2, sL[qi])) : 0.0f;
         if (KV) sP[r * LP + s] = p;
-        sDS[r * LP + s] = p == 0.0f ? 0.0f : p * (y[i][j] - sD[qi]);
+        sDS[r * LP + s] = p * (y[i][j] + sD[qi]);
       }
     }
     __syncthreads();
@@ -206,36 +231,45 @@ __global__ void __launch_bounds__(256) attn_bwd_kernel(const T* __restrict__ a0,
     if (n >= N) continue;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      from_f32(acc0[i][j] * scale, out0 + (base + n) * D + tc + 16 * j);
-      if (KV) from_f32(acc1[i][j], out1 + (base + n) * D + tc + 16 * j);
+      out0[(base + n) * D + tc + 16 * j] = acc0[i][j] * scale;
+      if (KV) out1[(base + n) * D + tc + 16 * j] = acc1[i][j];
     }
   }
 }
 
-template <typename T, int D, bool KV>
-static cudaError_t launch_bwd_t(const Dims& Dm, const void* a0, const void* a1, const void* b0, const void* b1,
-                                const float* lse, const float* delta, const int32_t* tile_ptr, const int32_t* tile_col,
-                                void* out0, void* out1, float scale, int32_t* dev_status, cudaStream_t st) {
+template <int D, bool KV>
+static cudaError_t launch_f32_t(const Dims& Dm, const void* a0, const void* a1, const void* b0, const void* b1,
+                                const float* stats, const fva_mask* m, void* out0, void* out1, float scale,
+                                int32_t* dev_status, cudaStream_t st) {
   const size_t smem = sizeof(float) * (4 * kBlock * (D + 4) + 2 * kBlock * (kBlock + 1) + 2 * kBlock);
-  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_kernel<T, D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_f32_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(Dm.nB), static_cast<unsigned>(Dm.BH));
-  attn_bwd_kernel<T, D, KV><<<grid, 256, smem, st>>>(
-      static_cast<const T*>(a0), static_cast<const T*>(a1), static_cast<const T*>(b0), static_cast<const T*>(b1), lse,
-      delta, tile_ptr, tile_col, static_cast<T*>(out0), static_cast<T*>(out1), static_cast<int>(Dm.N),
-      static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), scale, dev_status);
+  attn_bwd_f32_kernel<D, KV><<<grid, 256, smem, st>>>(
+      static_cast<const float*>(a0), static_cast<const float*>(a1), static_cast<const float*>(b0),
+      static_cast<const float*>(b1), stats, m->tile_ptr, m->tile_col, static_cast<float*>(out0),
+      static_cast<float*>(out1), static_cast<int>(Dm.N), static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), scale,
+      dev_status);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-static cudaError_t launch_bwd_d(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+template <int D>
+static cudaError_t launch_f32_d(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
                                 int32_t* dev_status, cudaStream_t st) {
-  cudaError_t e = launch_bwd_t<T, D, true>(Dm, x.k, x.v, x.q, x.d_o, x.lse, ws.delta, ws.mask_t.tile_ptr,
-                                           ws.mask_t.tile_col, x.dk, x.dv, x.scale, dev_status, st);
+  const cudaError_t e = launch_f32_t<D, true>(Dm, x.k, x.v, x.q, x.d_o, ws.stats, &ws.mask_t, x.dk, x.dv, x.scale,
+                                              dev_status, st);
   if (e != cudaSuccess) return e;
-  return launch_bwd_t<T, D, false>(Dm, x.q, x.d_o, x.k, x.v, x.lse, ws.delta, m->tile_ptr, m->tile_col, x.dq, nullptr,
-                                   x.scale, dev_status, st);
+  return launch_f32_t<D, false>(Dm, x.q, x.d_o, x.k, x.v, ws.stats, m, x.dq, nullptr, x.scale, dev_status, st);
+}
+
+template <typename T, int D>
+static cudaError_t launch_stats(const Dims& Dm, const BwdArgs& x, float* stats, cudaStream_t st) {
+  const int64_t rows = Dm.rows * kBlock, per_cta = 256 * 16 / (D * static_cast<int>(sizeof(T)));
+  row_stats_kernel<T, D><<<static_cast<unsigned>((rows + per_cta - 1) / per_cta), 256, 0, st>>>(
+      static_cast<const T*>(x.o), static_cast<const T*>(x.d_o), x.lse, rows, static_cast<int>(Dm.N),
+      static_cast<int>(Dm.nB), stats);
+  return cudaGetLastError();
 }
 
 // The transposed mask's tile lists (tiles of two key blocks over the union of the query
@@ -258,25 +292,21 @@ cudaError_t launch_attn_bwd(const Dims& Dm, const BwdArgs& x, const fva_mask* m,
                             int32_t* dev_status, cudaStream_t st) {
   cudaError_t e = launch_transposed_lists(Dm, m, ws, dev_status, st);
   if (e != cudaSuccess) return e;
-  const int64_t rows = Dm.BH * Dm.N;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (Dm.esize == 2)
-    row_dot_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x.o),
-                                                        static_cast<const __nv_bfloat16*>(x.d_o), rows,
-                                                        static_cast<int>(Dm.d), ws.delta);
-  else
-    row_dot_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(x.o), static_cast<const float*>(x.d_o), rows,
-                                                static_cast<int>(Dm.d), ws.delta);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   if (Dm.esize == 2) {
-    if (Dm.d == 128) return launch_bwd_d<__nv_bfloat16, 128>(Dm, x, m, ws, dev_status, st);
-    return launch_bwd_d<__nv_bfloat16, 64>(Dm, x, m, ws, dev_status, st);
+    e = Dm.d == 128 ? launch_stats<__nv_bfloat16, 128>(Dm, x, ws.stats, st)
+                    : launch_stats<__nv_bfloat16, 64>(Dm, x, ws.stats, st);
+    return e != cudaSuccess ? e : launch_attn_bwd_tc(Dm, x, m, &ws.mask_t, ws.stats, dev_status, st);
   }
   switch (Dm.d) {
-    case 32: return launch_bwd_d<float, 32>(Dm, x, m, ws, dev_status, st);
-    case 64: return launch_bwd_d<float, 64>(Dm, x, m, ws, dev_status, st);
-    default: return launch_bwd_d<float, 128>(Dm, x, m, ws, dev_status, st);
+    case 32:
+      e = launch_stats<float, 32>(Dm, x, ws.stats, st);
+      return e != cudaSuccess ? e : launch_f32_d<32>(Dm, x, m, ws, dev_status, st);
+    case 64:
+      e = launch_stats<float, 64>(Dm, x, ws.stats, st);
+      return e != cudaSuccess ? e : launch_f32_d<64>(Dm, x, m, ws, dev_status, st);
+    default:
+      e = launch_stats<float, 128>(Dm, x, ws.stats, st);
+      return e != cudaSuccess ? e : launch_f32_d<128>(Dm, x, m, ws, dev_status, st);
   }
 }
 

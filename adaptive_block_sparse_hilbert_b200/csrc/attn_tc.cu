@@ -40,13 +40,6 @@ constexpr int kBN = 64;   // keys per step (one key block)
 constexpr uint32_t kTmemCols = 256;
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
 
-// Bounded wait taken by a whole warp: the result is the same on every lane, so the
-// warp stays converged for the .sync.aligned TMEM instructions that follow.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  const bool ok = mbar_wait(bar, parity, abort, limit_ns);
-  return __all_sync(0xffffffffu, ok);
-}
-
 template <int D>
 struct AttnCfg {
   static constexpr int kChunks = D / 64;                    // 128-byte swizzle rows per d
@@ -477,8 +470,7 @@ static EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// 3-D map over a [B*H, N, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
-static bool make_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16) {
+bool make_bhnd_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
@@ -524,8 +516,8 @@ cudaError_t launch_attn_bf16(const Dims& Dm, const void* q, const void* k, const
                              const fva_mask* m, bool dense, void* o, float* lse, float scale, int64_t first_slot, int64_t n_slots,
                              int32_t* dev_status, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
-  if (!make_map(&mq, q, Dm.BH, Dm.N, Dm.d, false) || !make_map(&mk, k, Dm.BH, Dm.N, Dm.d, false) ||
-      !make_map(&mv, v, Dm.BH, Dm.N, Dm.d, v_f16))
+  if (!make_bhnd_map(&mq, q, Dm.BH, Dm.N, Dm.d, false) || !make_bhnd_map(&mk, k, Dm.BH, Dm.N, Dm.d, false) ||
+      !make_bhnd_map(&mv, v, Dm.BH, Dm.N, Dm.d, v_f16))
     return cudaErrorInvalidValue;
   const float scale_log2 = scale * 1.4426950408889634f;
   const int fs = static_cast<int>(first_slot), ns = static_cast<int>(n_slots);

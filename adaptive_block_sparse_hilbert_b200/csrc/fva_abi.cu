@@ -363,7 +363,7 @@ static bool bwd_shape_supported(const Dims& D) {
 static size_t bwd_scratch_layout(const Dims& D, void* ws, BwdScratch* out) {
   Carver c{static_cast<uint8_t*>(ws), 0};
   BwdScratch b{};
-  b.delta = c.take<float>(static_cast<size_t>(D.BH * D.N) * 4);
+  b.stats = c.take<float>(static_cast<size_t>(D.rows) * 2 * kBlock * 4);
   b.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
   b.route_t.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
   b.route_t.row_cnt = c.take<int32_t>(static_cast<size_t>(D.rows) * 4);

@@ -77,13 +77,17 @@ struct BwdArgs {
   float scale;
 };
 struct BwdScratch {
-  float* delta;          // [BH, N] rowsum(dO O)
+  float* stats;          // [BH, nB, 2, 64] -lse in log2 units and -rowsum(dO O) of every row
   uint32_t* bits;        // [rows, nWords] the mask, by query row
   RouteScratch route_t;  // bits by key row, their counts, head loads
   fva_mask mask_t;       // the transposed lists (no col_idx)
 };
 cudaError_t launch_attn_bwd(const Dims& D, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
                             int32_t* dev_status, cudaStream_t st);
+cudaError_t launch_attn_bwd_tc(const Dims& D, const BwdArgs& x, const fva_mask* m, const fva_mask* m_t,
+                               const float* stats, int32_t* dev_status, cudaStream_t st);
+// 3-D TMA map over a [B*H, N, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
+bool make_bhnd_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16);
 
 // ---------------------------------------------------------------------------------
 // device helpers
@@ -144,6 +148,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Bounded wait taken by a whole warp: the result is the same on every lane, so the
+// warp stays converged for the .sync.aligned TMEM instructions that follow.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  const bool ok = mbar_wait(bar, parity, abort, limit_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // ---- TMA (tile mode, no multicast) ------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -155,6 +166,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // ---- tcgen05 ----------------------------------------------------------------------------
@@ -242,6 +261,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// Load 32 columns from each of two places, one wait for both.
+#define FVA_RP8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                      "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld32_pair(uint32_t ta, uint32_t (&a)[32], uint32_t tb, uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : FVA_RP8(a, 0), FVA_RP8(a, 8), FVA_RP8(a, 16), FVA_RP8(a, 24), FVA_RP8(b, 0), FVA_RP8(b, 8), FVA_RP8(b, 16),
+        FVA_RP8(b, 24)
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
 // Load 64 consecutive 32-bit TMEM columns of this thread's lane and wait for them.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
@@ -265,6 +301,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       FVA_W8(0), FVA_W8(8), FVA_W8(16), FVA_W8(24)
       : "memory");
 }
+
+// Store 16 columns without waiting; tmem_st_wait() completes this thread's stores.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      FVA_W8(0), FVA_W8(8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -304,6 +350,11 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

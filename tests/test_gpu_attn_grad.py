@@ -235,3 +235,38 @@ def test_backward_needs_a_training_layer():
     x = torch.empty(1, 64, 1, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(RuntimeError):
         layer.backward(x, x, x, x)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_wait_that_runs_out_is_reported(d):
+    """With the first loads withheld and a 20 ms limit the gradient kernels report a timeout and
+    leave the device usable; the next call is right."""
+    c = Case(1, 2, 3, 12, 17, d, "bf16", "random")
+    c.fva.fva_set_diagnostics(20_000_000, c.fva.FVA_DIAG_WITHHOLD_Q)
+    try:
+        c.backward()
+        assert int(c.st.item()) == c.fva.FVA_DEVERR_TIMEOUT
+    finally:
+        c.fva.fva_set_diagnostics(0, 0)
+    c.st.zero_()
+    c.check(c.backward())
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+def test_bad_list_entries_are_reported(d, dtype):
+    """Tile entries and work-list entries that name nothing are reported, not followed."""
+    c = Case(1, 2, 3, 12, 17, d, dtype, "random")
+    good = c.mask.tile_col[5].clone()
+    c.mask.tile_col[5] = 4 * 4000 + 3
+    c.backward()
+    assert int(c.st.item()) == c.fva.FVA_DEVERR_BAD_LIST
+    c.mask.tile_col[5] = good
+    c.st.zero_()
+    if dtype == "bf16":
+        good = c.mask.worklist[1].clone()
+        c.mask.worklist[1] = 4000
+        c.backward()
+        assert int(c.st.item()) == c.fva.FVA_DEVERR_BAD_LIST
+        c.mask.worklist[1] = good
+        c.st.zero_()
+    c.check(c.backward())
