@@ -9,11 +9,15 @@
 // the second products (their relative error, 2^-9 on average, is the size of the gradients'
 // own rounding); sums stay in fp32 in TMEM. One owner per output row: no atomics.
 //
-//   * Warp 8 issues TMA loads into a ring of stages, warp 9 issues tcgen05.mma; warps 0-7 form
-//     P and dS, each thread one row (TMEM lane) and half of a step's 64 columns. S and dP sit
-//     in 2 (d = 128) or 3 (d = 64) TMEM buffers, so the tensor cores run the next step's first
-//     products while the warps work; P and dS overwrite them as packed bf16 and are the A
-//     operands, from TMEM, of the second products.
+//   * Warp 16 issues TMA loads into two rings of stages, warp 17 the products S, warp 18 dP and
+//     the second products. (One thread's waits and commits for all three took longer than the
+//     products: 1130 cycles a step where the dQ kernel's take 800. dP and the second products
+//     stay in one thread because products execute in the order of issue: dP needs no wait for
+//     its buffer's last readers.) Warps 0-15 form P and dS: two groups of eight take alternate
+//     steps, each thread one row (TMEM lane) and half of the step's 64 columns.
+//   * S runs ahead: its buffers are free again once the warps have read them, so the exponentials
+//     of a step overlap the products of the one before. P and dS (packed bf16) share the
+//     columns of the dP buffer they came from and are A operands from TMEM.
 //   * M = 128, N = 64 products with A in shared memory read 6 KB per 32 tensor cycles, above
 //     the 128 B a cycle that shared memory gives. The query kernel therefore keeps Q and dO
 //     in TMEM (columns: dQ d, Q d/2, dO d/2, buffers: 512 in all). The key kernel has no room
@@ -29,7 +33,7 @@
 
 namespace fva {
 
-constexpr int kBwdThreads = 320;
+constexpr int kBwdThreads = 608;
 constexpr uint32_t kBwdTmemCols = 512;
 
 template <int D, bool KV>
@@ -37,25 +41,64 @@ struct BwdCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kChunks * 64 * 128;                  // 64 rows x D bf16
   static constexpr int kOwn = KV ? 2 * kChunks * 128 * 128 : 0;     // K and V of the owned rows
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = D == 128 ? (KV ? 4 : 6) : 8;
-  static constexpr int kStats = KV ? kStages * 512 : 0;
-  static constexpr int kBufs = D == 128 ? 2 : 3;
-  static constexpr uint32_t kBufCol = 2 * D;  // buffer i: S at kBufCol + 128 i, dP 64 columns on
-  static constexpr int kSmemData = kOwn + kStages * kStage + kStats;
+  // ring 0 holds Q or K (read by the first product of a step and by its second ones), ring 1
+  // dO or V, which are needed later or for less long
+  static constexpr int kS0 = D == 128 ? (KV ? 5 : 6) : 8;
+  static constexpr int kS1 = D == 128 ? (KV ? 4 : 5) : 8;
+  static constexpr int kStats = KV ? kS0 * 512 : 0;  // statistics travel with Q
+  static constexpr int kBufs = D == 128 ? 2 : 3;     // S and dP buffers, 64 columns each
+  static constexpr int kLag = kBufs - 1;
+  static constexpr uint32_t kSCol = 2 * D, kDPCol = 2 * D + 64 * kBufs;
+  static constexpr int kSmemData = kOwn + (kS0 + kS1) * kTile + kStats;
 };
 
 template <int D, bool KV>
 struct __align__(8) BwdBars {
+  using Cfg = BwdCfg<D, KV>;
   uint64_t own_full;
-  uint64_t full[BwdCfg<D, KV>::kStages];
-  uint64_t empty[BwdCfg<D, KV>::kStages];
-  uint64_t s_full[BwdCfg<D, KV>::kBufs];
-  uint64_t p_full[BwdCfg<D, KV>::kBufs];
+  uint64_t full0[Cfg::kS0], empty0[Cfg::kS0];
+  uint64_t full1[Cfg::kS1], empty1[Cfg::kS1];
+  uint64_t s_full[Cfg::kBufs];   // S is in the buffer
+  uint64_t s_free[Cfg::kBufs];   // the warps have read it
+  uint64_t dp_full[Cfg::kBufs];  // dP is in the buffer
+  uint64_t p_full[Cfg::kBufs];   // P and dS have replaced it
   uint64_t out_full;
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
+};
+
+// Position in a ring: index and parity of the pass, stepped without divisions.
+template <int kSize>
+struct RingPos {
+  int i = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kSize) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Entries of a tile's list, 32 at a time in a warp's lanes, the next 32 on their way: a
+// per-step load's latency stays off the warp's path. Called by whole warps, j ascending, no 32
+// consecutive steps left out.
+struct ListReader {
+  const int32_t* list;
+  int n, batch, cur, next;
+  __device__ __forceinline__ ListReader(const int32_t* l, int count, int lane) : list(l), n(count), batch(0) {
+    cur = lane < n ? list[lane] : 0;
+    next = 32 + lane < n ? list[32 + lane] : 0;
+  }
+  __device__ __forceinline__ int get(int j, int lane) {
+    if ((j >> 5) != batch) {
+      batch = j >> 5;
+      cur = next;
+      const int at = 32 * (batch + 1) + lane;
+      next = at < n ? list[at] : 0;
+    }
+    return __shfl_sync(0xffffffffu, cur, j & 31);
+  }
 };
 
 template <int D, bool KV>
@@ -79,11 +122,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* s_own = smem;
-  uint8_t* s_ring = smem + Cfg::kOwn;
-  uint8_t* s_stats = s_ring + Cfg::kStages * Cfg::kStage;
+  uint8_t* s_ring0 = smem + Cfg::kOwn;
+  uint8_t* s_ring1 = s_ring0 + Cfg::kS0 * Cfg::kTile;
+  uint8_t* s_stats = s_ring1 + Cfg::kS1 * Cfg::kTile;
   BwdBars<D, KV>& bar = *reinterpret_cast<BwdBars<D, KV>*>(smem + Cfg::kSmemData);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (through a shuffle: the compiler then knows that the warp takes each role as a whole)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int tile = worklist[blockIdx.x];
   const bool tile_ok = tile >= 0 && tile < ntiles;
   if (!tile_ok) {
@@ -94,24 +139,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int list_base = tile_ptr[tile];
   const int n_iter = tile_ok ? tile_ptr[tile + 1] - list_base : 0;
 
-  if (threadIdx.x == 256) {
+  if (threadIdx.x == 512) {
     tma_prefetch_desc(&tm0);
     tma_prefetch_desc(&tm1);
     mbar_init(&bar.own_full, 1);
-    for (int s = 0; s < Cfg::kStages; ++s) {
-      mbar_init(&bar.full[s], 1);
-      mbar_init(&bar.empty[s], 1);
+    for (int s = 0; s < Cfg::kS0; ++s) {
+      mbar_init(&bar.full0[s], 1);
+      mbar_init(&bar.empty0[s], 1);
+    }
+    for (int s = 0; s < Cfg::kS1; ++s) {
+      mbar_init(&bar.full1[s], 1);
+      mbar_init(&bar.empty1[s], 1);
     }
     for (int i = 0; i < Cfg::kBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 256);
+      mbar_init(&bar.s_free[i], 8);
+      mbar_init(&bar.dp_full[i], 1);
+      mbar_init(&bar.p_full[i], 8);
     }
     mbar_init(&bar.out_full, 1);
-    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.drain[0], 1);
+    mbar_init(&bar.drain[1], 1);
     bar.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(&bar.tmem_base, kBwdTmemCols);
     tmem_relinquish();
   }
@@ -120,90 +172,106 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
   volatile int* abort_flag = &bar.abort;
-  const int row = (warp & 3) * 32 + lane;  // warps 0-7: row of the tile, and column half
+  const int row = (warp & 3) * 32 + lane;  // warps 0-15: row of the tile; warp / 4: a quarter of the work
+  const int part = warp >> 2;
   const int grow = t * 128 + row;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   if (!KV) {
-    // the owned rows become A operands: warps 0-3 store Q, warps 4-7 dO
-    if (warp < 8) {
-      const uint4* src = reinterpret_cast<const uint4*>((warp < 4 ? own0 : own1) + (static_cast<int64_t>(bh) * N + grow) * D);
+    // the owned rows become A operands: Q in parts 0 and 1, dO in 2 and 3, 64 channels each
+    if (warp < 16 && (D == 128 || (part & 1) == 0)) {
+      const uint4* src = reinterpret_cast<const uint4*>((part < 2 ? own0 : own1) + (static_cast<int64_t>(bh) * N + grow) * D) +
+                         (part & 1) * 8;
+      uint32_t r[32];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 x = grow < N ? src[c * 8 + i] : make_uint4(0u, 0u, 0u, 0u);
-          r[4 * i] = x.x;
-          r[4 * i + 1] = x.y;
-          r[4 * i + 2] = x.z;
-          r[4 * i + 3] = x.w;
-        }
-        tmem_st32(lane_base + D + (warp < 4 ? 0 : D / 2) + c * 32, r);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = grow < N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        r[4 * i] = x.x;
+        r[4 * i + 1] = x.y;
+        r[4 * i + 2] = x.z;
+        r[4 * i + 3] = x.w;
       }
+      tmem_st32(lane_base + D + (part >> 1) * (D / 2) + (part & 1) * 32, r);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
   }
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int uses[Cfg::kStages];
-      for (int s = 0; s < Cfg::kStages; ++s) uses[s] = 0;
-      const bool withhold = diag_flags & FVA_DIAG_WITHHOLD_Q;
-      if (KV && !withhold && n_iter > 0) {
-        mbar_arrive_expect_tx(&bar.own_full, Cfg::kOwn);
-        for (int c = 0; c < Cfg::kChunks; ++c)
-          for (int hf = 0; hf < 2; ++hf) {
-            const int at = c * (128 * 128) + hf * (64 * 128);
-            tma_load_3d(s_own + at, &tmo0, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
-            tma_load_3d(s_own + Cfg::kOwn / 2 + at, &tmo1, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
-          }
-      }
-      for (int j = 0; j < n_iter; ++j) {
-        const int blk = tile_col[list_base + j] >> 2;
-        if (blk < 0 || blk >= nB) {
-          report(dev_status, FVA_DEVERR_BAD_LIST);
-          *abort_flag = 1;
-          break;
+    const bool leader = elect_one();
+    const bool withhold = diag_flags & FVA_DIAG_WITHHOLD_Q;
+    ListReader entries(tile_col + list_base, n_iter, lane);
+    if (KV && !withhold && n_iter > 0 && leader) {
+      mbar_arrive_expect_tx(&bar.own_full, Cfg::kOwn);
+      for (int c = 0; c < Cfg::kChunks; ++c)
+        for (int hf = 0; hf < 2; ++hf) {
+          const int at = c * (128 * 128) + hf * (64 * 128);
+          tma_load_3d(s_own + at, &tmo0, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
+          tma_load_3d(s_own + Cfg::kOwn / 2 + at, &tmo1, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
         }
-        const int s = j % Cfg::kStages;
-        if (j >= Cfg::kStages &&
-            !mbar_wait(&bar.empty[s], ((j / Cfg::kStages) - 1) & 1, abort_flag, wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        if (!KV && withhold) break;  // nothing ever arrives: the waits behind it run out
-        mbar_arrive_expect_tx(&bar.full[s], Cfg::kStage + (KV ? 512 : 0));
-        uint8_t* dst = s_ring + s * Cfg::kStage;
-        for (int c = 0; c < Cfg::kChunks; ++c) {
-          tma_load_3d(dst + c * (64 * 128), &tm0, &bar.full[s], c * 64, blk * 64, bh);
-          tma_load_3d(dst + Cfg::kTile + c * (64 * 128), &tm1, &bar.full[s], c * 64, blk * 64, bh);
-        }
-        if (KV) bulk_load(s_stats + s * 512, stats + (static_cast<int64_t>(bh) * nB + blk) * 128, 512, &bar.full[s]);
-        ++uses[s];
-      }
-      if (!ok) {
-        report(dev_status, FVA_DEVERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      if (*abort_flag) {  // wait (bounded) for the last load into every buffer
-        volatile int never = 0;
-        if (KV && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
-        for (int s = 0; s < Cfg::kStages; ++s)
-          if (uses[s] > 0) mbar_wait(&bar.full[s], (uses[s] - 1) & 1, &never, 100000000ull);
-      }
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_iter > 0) {
+    RingPos<Cfg::kS0> r0;
+    RingPos<Cfg::kS1> r1;
+    bool ok = true;
+    int n0 = 0, n1 = 0;  // loads issued into each ring
+    for (int j = 0; j < n_iter; ++j) {
+      const int blk = entries.get(j, lane) >> 2;
+      if (blk < 0 || blk >= nB) {
+        report(dev_status, FVA_DEVERR_BAD_LIST);
+        *abort_flag = 1;
+        break;
+      }
+      if (!KV && withhold) break;  // nothing ever arrives: the waits behind it run out
+      // a ring's first pass finds its stages empty: the parity before the first phase passes
+      if (!warp_wait_spin(&bar.empty0[r0.i], r0.phase ^ 1, abort_flag, wait_limit_ns)) {
+        ok = false;
+        break;
+      }
+      if (leader) {
+        mbar_arrive_expect_tx(&bar.full0[r0.i], Cfg::kTile + (KV ? 512 : 0));
+#pragma unroll
+        for (int c = 0; c < Cfg::kChunks; ++c)
+          tma_load_3d(s_ring0 + r0.i * Cfg::kTile + c * (64 * 128), &tm0, &bar.full0[r0.i], c * 64, blk * 64, bh);
+        if (KV)
+          bulk_load(s_stats + r0.i * 512, stats + (static_cast<int64_t>(bh) * nB + blk) * 128, 512, &bar.full0[r0.i]);
+      }
+      ++n0;
+      if (!warp_wait_spin(&bar.empty1[r1.i], r1.phase ^ 1, abort_flag, wait_limit_ns)) {
+        ok = false;
+        break;
+      }
+      if (leader) {
+        mbar_arrive_expect_tx(&bar.full1[r1.i], Cfg::kTile);
+#pragma unroll
+        for (int c = 0; c < Cfg::kChunks; ++c)
+          tma_load_3d(s_ring1 + r1.i * Cfg::kTile + c * (64 * 128), &tm1, &bar.full1[r1.i], c * 64, blk * 64, bh);
+      }
+      ++n1;
+      r0.next();
+      r1.next();
+    }
+    if (!ok) {
+      report(dev_status, FVA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    if (*abort_flag) {  // wait (bounded) for the last load into every stage
+      volatile int never = 0;
+      if (KV && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
+      for (int j = n0 > Cfg::kS0 ? n0 - Cfg::kS0 : 0; j < n0; ++j)
+        mbar_wait(&bar.full0[j % Cfg::kS0], (j / Cfg::kS0) & 1, &never, 100000000ull);
+      for (int j = n1 > Cfg::kS1 ? n1 - Cfg::kS1 : 0; j < n1; ++j)
+        mbar_wait(&bar.full1[j % Cfg::kS1], (j / Cfg::kS1) & 1, &never, 100000000ull);
+    }
+  } else if (warp >= 17) {
+    // ------------------------------------------------------------------ products
+    // An elected lane, not `lane == 0`: the compiler keeps the descriptors in uniform registers
+    // then. An M = 128, N = 64, K = 16 product issues every 34 (A in TMEM) or 48 cycles (A in
+    // shared memory: its bandwidth) instead of every 57 to 61.
+    if (n_iter > 0 && elect_one()) {
       constexpr uint32_t idesc_first = idesc_f16kind_f32(128, 64, 0, 0, kFmtBF16);
       constexpr uint32_t idesc_second = idesc_f16kind_f32(128, D, 0, 1, kFmtBF16);
-      bool ok = KV ? mbar_wait(&bar.own_full, 0, abort_flag, wait_limit_ns) : true;
-      bool issued = false;
-      constexpr int kLag = Cfg::kBufs - 1;
       // x(buffer) = own (A) * streamed^T, over the D channels
       auto first = [&](uint32_t d_col, uint32_t own_smem, uint32_t own_col, uint32_t b_base) {
 #pragma unroll
@@ -217,59 +285,77 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mma_ts(tmem + d_col, tmem + own_col + kk * 8, bdesc, idesc_first, kk > 0);
         }
       };
-      // out += x (A, packed bf16 in the buffer) * streamed, over the block's 64 rows. The two
-      // column halves of x were stored 32 columns apart (each warp inside its own columns).
+      // out += x (A, packed bf16 in the dP buffer) * streamed, over the block's 64 rows. The
+      // two column halves of x were stored 32 columns apart (each warp inside its own columns).
       auto second = [&](uint32_t out_col, uint32_t x_col, uint32_t b_base, bool add) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_ts(tmem + out_col, tmem + x_col + (kk >> 1) * 32 + (kk & 1) * 8,
                  sdesc_sw128(b_base + kk * 2048, 64 * 128, 1024), idesc_second, add || kk > 0);
       };
-      auto finish = [&](int i) -> bool {
-        const int sb = i % Cfg::kBufs, s = i % Cfg::kStages;
-        if (!mbar_wait(&bar.p_full[sb], (i / Cfg::kBufs) & 1, abort_flag, wait_limit_ns)) return false;
-        tc_fence_after();
-        const uint32_t b0 = smem_u32(s_ring + s * Cfg::kStage);
-        const uint32_t col = Cfg::kBufCol + sb * 128;
-        if (KV) second(D, col, b0 + Cfg::kTile, i > 0);  // dV += P^T dO
-        second(0, col + 64, b0, i > 0);                  // dK += dS^T Q, or dQ += dS K
-        tc_commit(&bar.empty[s]);
-        return true;
-      };
-      if (ok) tc_fence_after();
-      for (int j = 0; j < n_iter && ok; ++j) {
-        const int s = j % Cfg::kStages, sb = j % Cfg::kBufs;
-        if (!mbar_wait(&bar.full[s], (j / Cfg::kStages) & 1, abort_flag, wait_limit_ns)) {
-          ok = false;
-          break;
+      bool issued = false;
+      bool ok = KV ? mbar_wait(&bar.own_full, 0, abort_flag, wait_limit_ns) : true;
+      if (warp == 17) {
+        RingPos<Cfg::kBufs> buf;
+        RingPos<Cfg::kS0> r;
+        for (int j = 0; j < n_iter && ok; ++j) {
+          ok = mbar_wait_spin(&bar.s_free[buf.i], buf.phase ^ 1, abort_flag, wait_limit_ns) &&
+               mbar_wait_spin(&bar.full0[r.i], r.phase, abort_flag, wait_limit_ns);
+          if (!ok) break;
+          tc_fence_after();
+          first(Cfg::kSCol + buf.i * 64, smem_u32(s_own), D, smem_u32(s_ring0) + r.i * Cfg::kTile);
+          tc_commit(&bar.s_full[buf.i]);
+          issued = true;
+          buf.next();
+          r.next();
         }
-        tc_fence_after();
-        // the products are executed in the order of issue, so the buffer's last reader, step
-        // j - kBufs, is done with it when these write
-        const uint32_t b0 = smem_u32(s_ring + s * Cfg::kStage);
-        const uint32_t col = Cfg::kBufCol + sb * 128;
-        first(col, smem_u32(s_own), D, b0);
-        first(col + 64, smem_u32(s_own) + Cfg::kOwn / 2, D + D / 2, b0 + Cfg::kTile);
-        issued = true;
-        tc_commit(&bar.s_full[sb]);
-        if (j >= kLag && !finish(j - kLag)) ok = false;
-      }
-      for (int i = n_iter > kLag ? n_iter - kLag : 0; i < n_iter && ok; ++i) ok = finish(i);
-      if (ok) {
-        tc_commit(&bar.out_full);
       } else {
+        RingPos<Cfg::kBufs> db, pb;  // buffers of the next dP and of the next second products
+        RingPos<Cfg::kS0> q0;
+        RingPos<Cfg::kS1> r1, q1;
+        // turn j: dP(j), then the second products of step j - kLag
+        for (int j = 0; j < n_iter + Cfg::kLag && ok; ++j) {
+          if (j < n_iter) {
+            ok = mbar_wait_spin(&bar.full1[r1.i], r1.phase, abort_flag, wait_limit_ns);
+            if (!ok) break;
+            tc_fence_after();
+            first(Cfg::kDPCol + db.i * 64, smem_u32(s_own) + Cfg::kOwn / 2, D + D / 2,
+                  smem_u32(s_ring1) + r1.i * Cfg::kTile);
+            tc_commit(&bar.dp_full[db.i]);
+            if (!KV) tc_commit(&bar.empty1[r1.i]);
+            issued = true;
+            db.next();
+            r1.next();
+          }
+          if (j >= Cfg::kLag) {
+            ok = mbar_wait_spin(&bar.p_full[pb.i], pb.phase, abort_flag, wait_limit_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t x = Cfg::kDPCol + pb.i * 64;
+            if (KV) second(D, x + 16, smem_u32(s_ring1) + q1.i * Cfg::kTile, j > Cfg::kLag);  // dV += P^T dO
+            second(0, x, smem_u32(s_ring0) + q0.i * Cfg::kTile, j > Cfg::kLag);  // dK += dS^T Q, or dQ += dS K
+            tc_commit(&bar.empty0[q0.i]);
+            if (KV) tc_commit(&bar.empty1[q1.i]);
+            pb.next();
+            q0.next();
+            q1.next();
+          }
+        }
+        if (ok) tc_commit(&bar.out_full);
+      }
+      if (!ok) {
         report(dev_status, FVA_DEVERR_TIMEOUT);
         *abort_flag = 1;
         if (issued) {
           volatile int never = 0;
-          tc_commit(&bar.drain);
-          mbar_wait(&bar.drain, 0, &never, 100000000ull);
+          tc_commit(&bar.drain[warp - 17]);
+          mbar_wait(&bar.drain[warp - 17], 0, &never, 100000000ull);
         }
       }
     }
   } else {
     // ------------------------------------------------------------------ P and dS
-    const int half = (warp & 3) >> 1, ch = warp >> 2;
+    const int half = (warp & 3) >> 1, ch = part & 1, group = part >> 1;
     float nl_row = 0.0f, nd_row = 0.0f;  // KV = false: this row's -lse2 and -D
     if (!KV) {
       const bool in = 2 * t + (row >> 6) < nB;
@@ -278,65 +364,95 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       nd_row = in ? st[64] : 0.0f;
     }
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    ListReader entries(tile_col + list_base, n_iter, lane);
     bool ok = true;
-    for (int j = 0; j < n_iter; ++j) {
-      const int entry = tile_col[list_base + j];
+    RingPos<Cfg::kBufs> buf;
+    RingPos<Cfg::kS0> stage;
+    if (group == 1) {
+      buf.next();
+      stage.next();
+    }
+    for (int j = group; j < n_iter; j += 2) {
+      const int entry = entries.get(j, lane);
       const int blk = entry >> 2;
-      const int sb = j % Cfg::kBufs;
       // (KV: these threads read the stage's statistics too, which S only implies have landed)
-      if (!warp_wait(&bar.s_full[sb], (j / Cfg::kBufs) & 1, abort_flag, wait_limit_ns) ||
-          (KV && !warp_wait(&bar.full[j % Cfg::kStages], (j / Cfg::kStages) & 1, abort_flag, wait_limit_ns))) {
+      if (!warp_wait_spin(&bar.s_full[buf.i], buf.phase, abort_flag, wait_limit_ns) ||
+          (KV && !warp_wait_spin(&bar.full0[stage.i], stage.phase, abort_flag, wait_limit_ns))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t col = lane_base + Cfg::kBufCol + sb * 128 + ch * 32;
-      uint32_t pp[16], pd[16];
-      if ((entry >> half) & 1) {
-        uint32_t x[32], y[32];
-        tmem_ld32_pair(col, x, col + 64, y);
-        const ulonglong2* nl4 = nullptr;
-        const ulonglong2* nd4 = nullptr;
-        if (KV) {
-          nl4 = reinterpret_cast<const ulonglong2*>(s_stats + (j % Cfg::kStages) * 512 + ch * 128);
-          nd4 = reinterpret_cast<const ulonglong2*>(s_stats + (j % Cfg::kStages) * 512 + 256 + ch * 128);
+      const uint32_t s_col = lane_base + Cfg::kSCol + buf.i * 64 + ch * 32;
+      const uint32_t dp_col = lane_base + Cfg::kDPCol + buf.i * 64 + ch * 32;
+      const bool keep = (entry >> half) & 1;
+      float p[32];
+      if (keep) {
+        uint32_t x[32];
+        tmem_ld32(s_col, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.s_free[buf.i]);
+        const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(s_stats + stage.i * 512 + ch * 128);
+        const uint64_t nlr = f2_pack(nl_row, nl_row);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 nl = KV ? nl4[c / 4] : make_ulonglong2(nlr, nlr);
+          const float2 a = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, nl.x));
+          const float2 b = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2, nl.y));
+          p[c] = ex2_approx(a.x);
+          p[c + 1] = ex2_approx(a.y);
+          p[c + 2] = ex2_approx(b.x);
+          p[c + 3] = ex2_approx(b.y);
         }
-        const uint64_t nlr = f2_pack(nl_row, nl_row), ndr = f2_pack(nd_row, nd_row);
+        if (!KV && blk == nB - 1) {  // keys past N: zero rows, not -inf scores
+          const int nvalid = N - blk * 64 - ch * 32;
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          ulonglong2 nl, nd;
-          if (KV) {
-            nl = nl4[c / 2];
-            nd = nd4[c / 2];
-          } else {
-            nl = make_ulonglong2(nlr, nlr);
-            nd = make_ulonglong2(ndr, ndr);
-          }
+          for (int c = 0; c < 32; ++c)
+            if (c >= nvalid) p[c] = 0.0f;
+        }
+      } else if (lane == 0) {
+        mbar_arrive(&bar.s_free[buf.i]);
+      }
+      if (!warp_wait_spin(&bar.dp_full[buf.i], buf.phase, abort_flag, wait_limit_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t w[16];
+      if (keep) {
+        uint32_t y[32];
+        tmem_ld32(dp_col, y);
+        if (KV) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = 2 * (c + i);
-            const float2 a = f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, i ? nl.y : nl.x));
-            float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
-            if (!KV && blk == nB - 1) {  // keys past N: zero rows, not -inf scores
-              const int nvalid = N - blk * 64 - ch * 32;
-              if (e >= nvalid) p0 = 0.0f;
-              if (e + 1 >= nvalid) p1 = 0.0f;
-            }
-            const uint64_t g = f2_add(f2_pack(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), i ? nd.y : nd.x);
-            const float2 ds = f2_unpack(f2_mul(f2_pack(p0, p1), g));
-            if (KV) pp[c + i] = pack_bf16x2(p0, p1);
-            pd[c + i] = pack_bf16x2(ds.x, ds.y);
-          }
+          for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+          tmem_st16(dp_col + 16, w);
+        }
+        const ulonglong2* nd4 = reinterpret_cast<const ulonglong2*>(s_stats + stage.i * 512 + 256 + ch * 128);
+        const uint64_t ndr = f2_pack(nd_row, nd_row);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 nd = KV ? nd4[c / 4] : make_ulonglong2(ndr, ndr);
+          const float2 a = f2_unpack(f2_mul(f2_pack(p[c], p[c + 1]),
+                                            f2_add(f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), nd.x)));
+          const float2 b = f2_unpack(f2_mul(f2_pack(p[c + 2], p[c + 3]),
+                                            f2_add(f2_pack(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), nd.y)));
+          w[c / 2] = pack_bf16x2(a.x, a.y);
+          w[c / 2 + 1] = pack_bf16x2(b.x, b.y);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) pp[c] = pd[c] = 0u;
+        for (int c = 0; c < 16; ++c) w[c] = 0u;
+        if (KV) tmem_st16(dp_col + 16, w);
       }
-      if (KV) tmem_st16(col, pp);
-      tmem_st16(col + 64, pd);
+      tmem_st16(dp_col, w);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bar.p_full[sb]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[buf.i]);
+      buf.next();
+      buf.next();
+      stage.next();
+      stage.next();
     }
     // ------------------------------------------------------------------ epilogue
     if (ok && n_iter > 0 && !warp_wait(&bar.out_full, 0, abort_flag, wait_limit_ns)) ok = false;
@@ -345,27 +461,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       *abort_flag = 1;
     } else if (tile_ok) {
       tc_fence_after();
-      // KV: warps 0-3 write dK, warps 4-7 dV; else the halves of dQ
-      constexpr int kCols = KV ? D : D / 2;
-      const float f = KV && ch == 1 ? 1.0f : scale;
-      __nv_bfloat16* dst = (KV && ch == 1 ? out1 : out0) + (static_cast<int64_t>(bh) * N + grow) * D + (KV ? 0 : ch * kCols);
+      // the outputs' columns (KV: dK, then dV) in pieces of 32, a quarter of them a part
+      constexpr int kPieces = (KV ? 2 * D : D) / 32;
 #pragma unroll
-      for (int cc = 0; cc < kCols / 32; ++cc) {
+      for (int pc = part; pc < kPieces; pc += 4) {
+        const bool second = KV && pc >= D / 32;
+        const float f = second ? 1.0f : scale;
         uint32_t o[32];
         if (n_iter > 0) {
-          tmem_ld32(lane_base + (KV ? ch * D : ch * kCols) + cc * 32, o);
+          tmem_ld32(lane_base + pc * 32, o);
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
         if (grow < N) {
+          uint4* dst = reinterpret_cast<uint4*>((second ? out1 : out0) + (static_cast<int64_t>(bh) * N + grow) * D +
+                                                (second ? pc * 32 - D : pc * 32));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               w[i] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * i]) * f, __uint_as_float(o[8 * q + 2 * i + 1]) * f);
-            reinterpret_cast<uint4*>(dst)[cc * 4 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
@@ -374,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, kBwdTmemCols);
   }
