@@ -19,9 +19,11 @@
 //     of a step overlap the products of the one before. P and dS (packed bf16) share the
 //     columns of the dP buffer they came from and are A operands from TMEM.
 //   * M = 128, N = 64 products with A in shared memory read 6 KB per 32 tensor cycles, above
-//     the 128 B a cycle that shared memory gives. The query kernel therefore keeps Q and dO
-//     in TMEM (columns: dQ d, Q d/2, dO d/2, buffers: 512 in all). The key kernel has no room
-//     for both K and V there beside dK and dV.
+//     the 128 B a cycle that shared memory gives, so the owned operands (A) go to TMEM where
+//     its 512 columns have room (outputs, owned operands, S buffers, dP buffers):
+//       dQ     d = 128: 128 + Q 64 + dO 64 + 2 x 64 + 2 x 64    d = 64: 64 + 32 + 32 + 3 x 64 + 3 x 64
+//       dK, dV d = 128: 256 (K, V in smem) + 2 x 64 + 2 x 64    d = 64: 128 + 32 + 32 + 2 x 64 + 3 x 64
+//     (dK, dV at d = 128 with K in TMEM and one S buffer: 5.3 ms where this takes 5.2.)
 //   * The statistics of a 64-row block, -lse2 and -D, are one 512-byte piece (see
 //     row_stats_kernel): the key kernel streams it with Q and dO. Rows without keys and rows
 //     past N have -lse2 = -infinity, so their P is 0.
@@ -40,15 +42,21 @@ template <int D, bool KV>
 struct BwdCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kChunks * 64 * 128;                  // 64 rows x D bf16
-  static constexpr int kOwn = KV ? 2 * kChunks * 128 * 128 : 0;     // K and V of the owned rows
+  static constexpr bool kOwnSmem = KV && D == 128;                  // K and V stay in shared memory
+  static constexpr int kOwnTile = kChunks * 128 * 128;
+  static constexpr int kOwn = kOwnSmem ? 2 * kOwnTile : 0;
   // ring 0 holds Q or K (read by the first product of a step and by its second ones), ring 1
   // dO or V, which are needed later or for less long
   static constexpr int kS0 = D == 128 ? (KV ? 5 : 6) : 8;
   static constexpr int kS1 = D == 128 ? (KV ? 4 : 5) : 8;
   static constexpr int kStats = KV ? kS0 * 512 : 0;  // statistics travel with Q
-  static constexpr int kBufs = D == 128 ? 2 : 3;     // S and dP buffers, 64 columns each
-  static constexpr int kLag = kBufs - 1;
-  static constexpr uint32_t kSCol = 2 * D, kDPCol = 2 * D + 64 * kBufs;
+  // S and dP buffers, 64 columns each
+  static constexpr int kSBufs = D == 128 || KV ? 2 : 3;
+  static constexpr int kDPBufs = D == 128 ? 2 : 3;
+  static constexpr int kLag = kDPBufs - 1;
+  static constexpr uint32_t kOwn0Col = (KV ? 2 : 1) * D, kOwn1Col = kOwn0Col + D / 2;
+  static constexpr uint32_t kSCol = kOwnSmem ? kOwn0Col : kOwn1Col + D / 2, kDPCol = kSCol + 64 * kSBufs;
+  static_assert(kDPCol + 64 * kDPBufs <= kBwdTmemCols, "TMEM columns");
   static constexpr int kSmemData = kOwn + (kS0 + kS1) * kTile + kStats;
 };
 
@@ -58,10 +66,10 @@ struct __align__(8) BwdBars {
   uint64_t own_full;
   uint64_t full0[Cfg::kS0], empty0[Cfg::kS0];
   uint64_t full1[Cfg::kS1], empty1[Cfg::kS1];
-  uint64_t s_full[Cfg::kBufs];   // S is in the buffer
-  uint64_t s_free[Cfg::kBufs];   // the warps have read it
-  uint64_t dp_full[Cfg::kBufs];  // dP is in the buffer
-  uint64_t p_full[Cfg::kBufs];   // P and dS have replaced it
+  uint64_t s_full[Cfg::kSBufs];    // S is in the buffer
+  uint64_t s_free[Cfg::kSBufs];    // the warps have read it
+  uint64_t dp_full[Cfg::kDPBufs];  // dP is in the buffer
+  uint64_t p_full[Cfg::kDPBufs];   // P and dS have replaced it
   uint64_t out_full;
   uint64_t drain[2];
   uint32_t tmem_base;
@@ -106,8 +114,8 @@ constexpr size_t bwd_smem_bytes() {
   return 1024 /*alignment slack*/ + BwdCfg<D, KV>::kSmemData + sizeof(BwdBars<D, KV>);
 }
 
-// own0, own1: Q and dO (KV = false, read by the threads) -- maps of the streamed pair in
-// tm0 / tm1, of the owned pair (KV) in tmo0 / tmo1.
+// own0, own1: the owned pair, Q and dO or K and V, tmo0, tmo1 maps of them; tm0,
+// tm1: maps of the streamed pair.
 template <int D, bool KV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmo0, const __grid_constant__ CUtensorMap tmo1,
@@ -151,9 +159,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&bar.full1[s], 1);
       mbar_init(&bar.empty1[s], 1);
     }
-    for (int i = 0; i < Cfg::kBufs; ++i) {
+    for (int i = 0; i < Cfg::kSBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.s_free[i], 8);
+    }
+    for (int i = 0; i < Cfg::kDPBufs; ++i) {
       mbar_init(&bar.dp_full[i], 1);
       mbar_init(&bar.p_full[i], 8);
     }
@@ -176,39 +186,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int part = warp >> 2;
   const int grow = t * 128 + row;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  if (!KV) {
-    // the owned rows become A operands: Q in parts 0 and 1, dO in 2 and 3, 64 channels each
-    if (warp < 16 && (D == 128 || (part & 1) == 0)) {
-      const uint4* src = reinterpret_cast<const uint4*>((part < 2 ? own0 : own1) + (static_cast<int64_t>(bh) * N + grow) * D) +
-                         (part & 1) * 8;
-      uint32_t r[32];
+  // the owned rows become A operands in TMEM: own0 by parts 0 and 1, own1 by 2 and 3, 64 channels each
+  if (!Cfg::kOwnSmem && warp < 16 && (D == 128 || (part & 1) == 0)) {
+    const uint4* src = reinterpret_cast<const uint4*>((part < 2 ? own0 : own1) + (static_cast<int64_t>(bh) * N + grow) * D) +
+                       (part & 1) * 8;
+    uint32_t r[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = grow < N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        r[4 * i] = x.x;
-        r[4 * i + 1] = x.y;
-        r[4 * i + 2] = x.z;
-        r[4 * i + 3] = x.w;
-      }
-      tmem_st32(lane_base + D + (part >> 1) * (D / 2) + (part & 1) * 32, r);
+    for (int i = 0; i < 8; ++i) {
+      const uint4 x = grow < N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      r[4 * i] = x.x;
+      r[4 * i + 1] = x.y;
+      r[4 * i + 2] = x.z;
+      r[4 * i + 3] = x.w;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    tmem_st32(lane_base + (part < 2 ? Cfg::kOwn0Col : Cfg::kOwn1Col) + (part & 1) * 32, r);
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
 
   if (warp == 16) {
     // ------------------------------------------------------------------ TMA producer
     const bool leader = elect_one();
     const bool withhold = diag_flags & FVA_DIAG_WITHHOLD_Q;
     ListReader entries(tile_col + list_base, n_iter, lane);
-    if (KV && !withhold && n_iter > 0 && leader) {
+    if (Cfg::kOwnSmem && !withhold && n_iter > 0 && leader) {
       mbar_arrive_expect_tx(&bar.own_full, Cfg::kOwn);
       for (int c = 0; c < Cfg::kChunks; ++c)
         for (int hf = 0; hf < 2; ++hf) {
           const int at = c * (128 * 128) + hf * (64 * 128);
           tma_load_3d(s_own + at, &tmo0, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
-          tma_load_3d(s_own + Cfg::kOwn / 2 + at, &tmo1, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
+          tma_load_3d(s_own + Cfg::kOwnTile + at, &tmo1, &bar.own_full, c * 64, t * 128 + hf * 64, bh);
         }
     }
     RingPos<Cfg::kS0> r0;
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         *abort_flag = 1;
         break;
       }
-      if (!KV && withhold) break;  // nothing ever arrives: the waits behind it run out
+      if (withhold) break;  // nothing ever arrives: the waits behind it run out
       // a ring's first pass finds its stages empty: the parity before the first phase passes
       if (!warp_wait_spin(&bar.empty0[r0.i], r0.phase ^ 1, abort_flag, wait_limit_ns)) {
         ok = false;
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     if (*abort_flag) {  // wait (bounded) for the last load into every stage
       volatile int never = 0;
-      if (KV && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
+      if (Cfg::kOwnSmem && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
       for (int j = n0 > Cfg::kS0 ? n0 - Cfg::kS0 : 0; j < n0; ++j)
         mbar_wait(&bar.full0[j % Cfg::kS0], (j / Cfg::kS0) & 1, &never, 100000000ull);
       for (int j = n1 > Cfg::kS1 ? n1 - Cfg::kS1 : 0; j < n1; ++j)
@@ -272,14 +280,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (n_iter > 0 && elect_one()) {
       constexpr uint32_t idesc_first = idesc_f16kind_f32(128, 64, 0, 0, kFmtBF16);
       constexpr uint32_t idesc_second = idesc_f16kind_f32(128, D, 0, 1, kFmtBF16);
-      // x(buffer) = own (A) * streamed^T, over the D channels
-      auto first = [&](uint32_t d_col, uint32_t own_smem, uint32_t own_col, uint32_t b_base) {
+      // x(buffer) = own (A) * streamed^T, over the D channels; A in TMEM or shared memory
+      auto first = [&](uint32_t d_col, uint32_t own_col, uint32_t own_smem, uint32_t b_base) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int c = kk >> 2;
           const uint32_t ko = (kk & 3) * 32;
           const uint64_t bdesc = sdesc_sw128(b_base + c * (64 * 128) + ko, 16, 1024);
-          if (KV)
+          if (Cfg::kOwnSmem)
             mma_ss(tmem + d_col, sdesc_sw128(own_smem + c * (128 * 128) + ko, 16, 1024), bdesc, idesc_first, kk > 0);
           else
             mma_ts(tmem + d_col, tmem + own_col + kk * 8, bdesc, idesc_first, kk > 0);
@@ -294,23 +302,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  sdesc_sw128(b_base + kk * 2048, 64 * 128, 1024), idesc_second, add || kk > 0);
       };
       bool issued = false;
-      bool ok = KV ? mbar_wait(&bar.own_full, 0, abort_flag, wait_limit_ns) : true;
+      bool ok = Cfg::kOwnSmem ? mbar_wait(&bar.own_full, 0, abort_flag, wait_limit_ns) : true;
       if (warp == 17) {
-        RingPos<Cfg::kBufs> buf;
+        RingPos<Cfg::kSBufs> buf;
         RingPos<Cfg::kS0> r;
         for (int j = 0; j < n_iter && ok; ++j) {
-          ok = mbar_wait_spin(&bar.s_free[buf.i], buf.phase ^ 1, abort_flag, wait_limit_ns) &&
-               mbar_wait_spin(&bar.full0[r.i], r.phase, abort_flag, wait_limit_ns);
+          ok = mbar_wait_spin(&bar.full0[r.i], r.phase, abort_flag, wait_limit_ns);
+          ok = ok && mbar_wait_spin(&bar.s_free[buf.i], buf.phase ^ 1, abort_flag, wait_limit_ns);
           if (!ok) break;
           tc_fence_after();
-          first(Cfg::kSCol + buf.i * 64, smem_u32(s_own), D, smem_u32(s_ring0) + r.i * Cfg::kTile);
+          first(Cfg::kSCol + buf.i * 64, Cfg::kOwn0Col, smem_u32(s_own), smem_u32(s_ring0) + r.i * Cfg::kTile);
           tc_commit(&bar.s_full[buf.i]);
           issued = true;
           buf.next();
           r.next();
         }
       } else {
-        RingPos<Cfg::kBufs> db, pb;  // buffers of the next dP and of the next second products
+        RingPos<Cfg::kDPBufs> db, pb;  // buffers of the next dP and of the next second products
         RingPos<Cfg::kS0> q0;
         RingPos<Cfg::kS1> r1, q1;
         // turn j: dP(j), then the second products of step j - kLag
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ok = mbar_wait_spin(&bar.full1[r1.i], r1.phase, abort_flag, wait_limit_ns);
             if (!ok) break;
             tc_fence_after();
-            first(Cfg::kDPCol + db.i * 64, smem_u32(s_own) + Cfg::kOwn / 2, D + D / 2,
+            first(Cfg::kDPCol + db.i * 64, Cfg::kOwn1Col, smem_u32(s_own) + Cfg::kOwnTile,
                   smem_u32(s_ring1) + r1.i * Cfg::kTile);
             tc_commit(&bar.dp_full[db.i]);
             if (!KV) tc_commit(&bar.empty1[r1.i]);
@@ -366,24 +374,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
     ListReader entries(tile_col + list_base, n_iter, lane);
     bool ok = true;
-    RingPos<Cfg::kBufs> buf;
+    RingPos<Cfg::kSBufs> sb;
+    RingPos<Cfg::kDPBufs> db;
     RingPos<Cfg::kS0> stage;
     if (group == 1) {
-      buf.next();
+      sb.next();
+      db.next();
       stage.next();
     }
     for (int j = group; j < n_iter; j += 2) {
       const int entry = entries.get(j, lane);
       const int blk = entry >> 2;
       // (KV: these threads read the stage's statistics too, which S only implies have landed)
-      if (!warp_wait_spin(&bar.s_full[buf.i], buf.phase, abort_flag, wait_limit_ns) ||
+      if (!warp_wait_spin(&bar.s_full[sb.i], sb.phase, abort_flag, wait_limit_ns) ||
           (KV && !warp_wait_spin(&bar.full0[stage.i], stage.phase, abort_flag, wait_limit_ns))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t s_col = lane_base + Cfg::kSCol + buf.i * 64 + ch * 32;
-      const uint32_t dp_col = lane_base + Cfg::kDPCol + buf.i * 64 + ch * 32;
+      const uint32_t s_col = lane_base + Cfg::kSCol + sb.i * 64 + ch * 32;
+      const uint32_t dp_col = lane_base + Cfg::kDPCol + db.i * 64 + ch * 32;
       const bool keep = (entry >> half) & 1;
       float p[32];
       if (keep) {
@@ -391,7 +401,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld32(s_col, x);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.s_free[buf.i]);
+        if (lane == 0) mbar_arrive(&bar.s_free[sb.i]);
         const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(s_stats + stage.i * 512 + ch * 128);
         const uint64_t nlr = f2_pack(nl_row, nl_row);
 #pragma unroll
@@ -411,9 +421,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (c >= nvalid) p[c] = 0.0f;
         }
       } else if (lane == 0) {
-        mbar_arrive(&bar.s_free[buf.i]);
+        mbar_arrive(&bar.s_free[sb.i]);
       }
-      if (!warp_wait_spin(&bar.dp_full[buf.i], buf.phase, abort_flag, wait_limit_ns)) {
+      if (!warp_wait_spin(&bar.dp_full[db.i], db.phase, abort_flag, wait_limit_ns)) {
         ok = false;
         break;
       }
@@ -448,9 +458,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[buf.i]);
-      buf.next();
-      buf.next();
+      if (lane == 0) mbar_arrive(&bar.p_full[db.i]);
+      sb.next();
+      sb.next();
+      db.next();
+      db.next();
       stage.next();
       stage.next();
     }
@@ -508,8 +520,8 @@ static cudaError_t launch_tc_t(const Dims& Dm, const BwdArgs& x, const CUtensorM
   if (e != cudaSuccess) return e;
   using bf = __nv_bfloat16;
   attn_bwd_tc_kernel<D, KV><<<static_cast<unsigned>(Dm.tiles), kBwdThreads, smem, st>>>(
-      KV ? mk : mq, KV ? mv : mdo, KV ? mq : mk, KV ? mdo : mv, static_cast<const bf*>(x.q),
-      static_cast<const bf*>(x.d_o), stats, static_cast<bf*>(KV ? x.dk : x.dq), static_cast<bf*>(KV ? x.dv : nullptr),
+      KV ? mk : mq, KV ? mv : mdo, KV ? mq : mk, KV ? mdo : mv, static_cast<const bf*>(KV ? x.k : x.q),
+      static_cast<const bf*>(KV ? x.v : x.d_o), stats, static_cast<bf*>(KV ? x.dk : x.dq), static_cast<bf*>(KV ? x.dv : nullptr),
       m->tile_ptr, m->tile_col, m->worklist, static_cast<int>(Dm.tiles), static_cast<int>(Dm.N),
       static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), x.scale, x.scale * 1.4426950408889634f,
       attn_wait_limit_ns(), attn_diag_flags(), dev_status);
