@@ -531,8 +531,8 @@ static cudaError_t launch_tc_t(const Dims& Dm, const BwdArgs& x, const CUtensorM
 cudaError_t launch_attn_bwd_tc(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const fva_mask* m_t,
                                const float* stats, int32_t* dev_status, cudaStream_t st) {
   CUtensorMap mq, mk, mv, mdo;
-  if (!make_bhnd_map(&mq, x.q, Dm.BH, Dm.N, Dm.d, false) || !make_bhnd_map(&mk, x.k, Dm.BH, Dm.N, Dm.d, false) ||
-      !make_bhnd_map(&mv, x.v, Dm.BH, Dm.N, Dm.d, false) || !make_bhnd_map(&mdo, x.d_o, Dm.BH, Dm.N, Dm.d, false))
+  if (!make_rows_map(&mq, x.q, Dm.BH, Dm.N, Dm.d, false) || !make_rows_map(&mk, x.k, Dm.BH, Dm.N, Dm.d, false) ||
+      !make_rows_map(&mv, x.v, Dm.BH, Dm.N, Dm.d, false) || !make_rows_map(&mdo, x.d_o, Dm.BH, Dm.N, Dm.d, false))
     return cudaErrorInvalidValue;
   cudaError_t e;
   if (Dm.d == 128) {

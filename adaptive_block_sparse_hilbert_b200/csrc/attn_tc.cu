@@ -470,7 +470,7 @@ static EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-bool make_bhnd_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16) {
+bool make_rows_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
@@ -516,8 +516,8 @@ cudaError_t launch_attn_bf16(const Dims& Dm, const void* q, const void* k, const
                              const fva_mask* m, bool dense, void* o, float* lse, float scale, int64_t first_slot, int64_t n_slots,
                              int32_t* dev_status, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
-  if (!make_bhnd_map(&mq, q, Dm.BH, Dm.N, Dm.d, false) || !make_bhnd_map(&mk, k, Dm.BH, Dm.N, Dm.d, false) ||
-      !make_bhnd_map(&mv, v, Dm.BH, Dm.N, Dm.d, v_f16))
+  if (!make_rows_map(&mq, q, Dm.BH, Dm.N, Dm.d, false) || !make_rows_map(&mk, k, Dm.BH, Dm.N, Dm.d, false) ||
+      !make_rows_map(&mv, v, Dm.BH, Dm.N, Dm.d, v_f16))
     return cudaErrorInvalidValue;
   const float scale_log2 = scale * 1.4426950408889634f;
   const int fs = static_cast<int>(first_slot), ns = static_cast<int>(n_slots);

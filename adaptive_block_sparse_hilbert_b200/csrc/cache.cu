@@ -1,32 +1,70 @@
 // Paged key/value cache: append, routing of single queries, eviction by accumulated weight.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "cache.cuh"
 
 namespace fva {
 
-// Mean of a page's first n keys, one thread per channel: the sum in float64 in token order
-// (exact for 16-bit keys of a usual range, so it does not depend on how the tokens came),
-// divided, rounded once.
-template <typename T>
-__device__ __forceinline__ void write_mean(const T* page_k, int n, int d, float* mean) {
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    double s = 0.0;
-    for (int r = 0; r < n; ++r) s += static_cast<double>(to_f32(page_k[r * d + c]));
-    mean[c] = static_cast<float>(s / n);
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------------
+// Rows of a page: copy and mean (append, eviction)
+// ---------------------------------------------------------------------------------
+// A CTA of 256 threads holds the 64 rows of one (page, key head), 16 bytes a thread and row:
+// thread = (row lane, 16-byte piece), rows row lane, row lane + kLanes, ... All of a thread's
+// loads are issued before its first store, so a CTA has up to 32 KB in flight.
+constexpr int kPageThreads = 256;
+
+template <typename T, int D>
+struct PageRows {
+  static constexpr int kPieces = D * static_cast<int>(sizeof(T)) / 16;
+  static constexpr int kLanes = kPageThreads / kPieces;
+  static constexpr int kRows = kBlock / kLanes;
+  static constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // values of a piece
+};
+
+// key_mean of the page from its rows' keys in registers (rows >= n are not counted): sums in
+// float64 (exact for 16-bit keys of a usual range), divided, rounded once. A row's place in
+// the sum depends on the row alone, so the mean does not depend on how the tokens came.
+template <typename T, int D>
+__device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D>::kRows], int n, float* mean) {
+  using P = PageRows<T, D>;
+  __shared__ double sums[P::kLanes][D];
+  const int lane = threadIdx.x / P::kPieces, piece = threadIdx.x % P::kPieces;
+  double s[P::kPer];
+#pragma unroll
+  for (int i = 0; i < P::kPer; ++i) s[i] = 0.0;
+#pragma unroll
+  for (int r = 0; r < P::kRows; ++r) {
+    const T* x = reinterpret_cast<const T*>(&k[r]);
+    if (lane + r * P::kLanes < n) {
+#pragma unroll
+      for (int i = 0; i < P::kPer; ++i) s[i] += static_cast<double>(to_f32(x[i]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P::kPer; ++i) sums[lane][piece * P::kPer + i] = s[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += kPageThreads) {
+    double t = 0.0;
+#pragma unroll
+    for (int l = 0; l < P::kLanes; ++l) t += sums[l][c];
+    mean[c] = static_cast<float>(t / n);
   }
 }
 
 // ---------------------------------------------------------------------------------
 // Append
 // ---------------------------------------------------------------------------------
-// One CTA per (touched block, key head, sequence): its share of the new rows is copied in
-// 16-byte pieces, then the page's mean is taken from the page itself.
-template <typename T>
-__global__ void __launch_bounds__(128) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
-                                                     const T* __restrict__ v_new, int64_t token_stride, int d,
-                                                     const int32_t* __restrict__ new_ptr, int max_new,
-                                                     int32_t* dev_status) {
+// One CTA per (touched block, key head, sequence). Bound by the copy: 16 prompts of 1 to 4001
+// tokens, 8 key heads, d = 128.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPageThreads) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
+                                                              const T* __restrict__ v_new, int64_t token_stride,
+                                                              const int32_t* __restrict__ new_ptr, int max_new,
+                                                              int32_t* dev_status) {
+  using P = PageRows<T, D>;
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = seq_len(c, b, dev_status);
   const int from = new_ptr[b], n_new = new_ptr[b + 1] - from;
@@ -34,384 +72,735 @@ __global__ void __launch_bounds__(128) append_kernel(CacheView<T> c, const T* __
     if (n_new != 0 && threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
     return;
   }
-  const int first = len - n_new;                     // position of the first new token
+  const int first = len - n_new;  // position of the first new token
   const int block = first / kBlock + blockIdx.x;
   if (block * kBlock >= len) return;
   const int page = page_of(c, b, block, dev_status);
   if (page < 0) return;
   const int r0 = max(first - block * kBlock, 0), r1 = min(len - block * kBlock, kBlock);
   const int64_t base = (static_cast<int64_t>(page) * c.Hkv + h) * kBlock;
-  const int vecs = d * static_cast<int>(sizeof(T)) / 16;  // 16-byte pieces of a row
-  for (int i = threadIdx.x; i < (r1 - r0) * vecs; i += blockDim.x) {
-    const int r = r0 + i / vecs, p = i % vecs;
-    const int64_t src = (static_cast<int64_t>(from) + block * kBlock + r - first) * token_stride + static_cast<int64_t>(h) * d;
-    reinterpret_cast<uint4*>(c.k + (base + r) * d)[p] = reinterpret_cast<const uint4*>(k_new + src)[p];
-    reinterpret_cast<uint4*>(c.v + (base + r) * d)[p] = reinterpret_cast<const uint4*>(v_new + src)[p];
+  const int lane = threadIdx.x / P::kPieces, piece = threadIdx.x % P::kPieces;
+  uint4 k[P::kRows], v[P::kRows];
+#pragma unroll
+  for (int i = 0; i < P::kRows; ++i) {
+    const int r = lane + i * P::kLanes;
+    const int64_t src = (static_cast<int64_t>(from) + block * kBlock + r - first) * token_stride + static_cast<int64_t>(h) * D;
+    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < r0) {
+      k[i] = reinterpret_cast<const uint4*>(c.k + (base + r) * D)[piece];  // older, for the mean
+    } else if (r < r1) {
+      k[i] = reinterpret_cast<const uint4*>(k_new + src)[piece];
+      v[i] = reinterpret_cast<const uint4*>(v_new + src)[piece];
+    }
   }
-  if (c.mass)
-    for (int r = r0 + threadIdx.x; r < r1; r += blockDim.x) c.mass[base + r] = 0.0f;
-  __syncthreads();
-  write_mean(c.k + base * d, r1, d, c.key_mean + (static_cast<int64_t>(page) * c.Hkv + h) * d);
+#pragma unroll
+  for (int i = 0; i < P::kRows; ++i) {
+    const int r = lane + i * P::kLanes;
+    if (r >= r0 && r < r1) {
+      reinterpret_cast<uint4*>(c.k + (base + r) * D)[piece] = k[i];
+      reinterpret_cast<uint4*>(c.v + (base + r) * D)[piece] = v[i];
+      if (c.mass && piece == 0) c.mass[base + r] = 0.0f;
+    }
+  }
+  write_mean<T, D>(k, r1, c.key_mean + (static_cast<int64_t>(page) * c.Hkv + h) * D);
 }
 
 // ---------------------------------------------------------------------------------
 // Routing
 // ---------------------------------------------------------------------------------
-// Block scores: one warp per block, lanes over the channels, one query head after another.
-template <typename T>
-__global__ void __launch_bounds__(128) cache_scores_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
-                                                           int H, int d, double scale, double* __restrict__ scores,
-                                                           int32_t* dev_status) {
-  const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-  const int block = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int len = seq_len(c, b, dev_status);
-  if (block * kBlock >= len) return;
-  const int page = page_of(c, b, block, dev_status);
-  const int G = H / c.Hkv;
-  const float* mean = c.key_mean + (static_cast<int64_t>(page < 0 ? 0 : page) * c.Hkv + h) * d;
-  for (int g = 0; g < G; ++g) {
-    const T* qh = q + b * q_stride + static_cast<int64_t>(h * G + g) * d;
-    double s = 0.0;
-    if (page >= 0)
-      for (int i = lane; i < d; i += 32) s = fma(static_cast<double>(to_f32(qh[i])), static_cast<double>(mean[i]), s);
-    s = warp_sum_d(s) * scale;
-    if (page < 0) s = -INFINITY;  // a block without a page is never chosen for its score
-    if (lane == 0) scores[(static_cast<int64_t>(b) * H + h * G + g) * c.max_blocks + block] = s;
-  }
-}
-
+// A cluster of CTAs per (key head, sequence), each with a contiguous share of the blocks:
+// scores in float64 (a share of the softmax next to the p border decides), the heads' maxima
+// and sums joined over the cluster, then every block's share P_b, gathered in the shared
+// memory of the cluster's first CTA, which selects.
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRankMost = 512;    // this many blocks are ranked against one another
+constexpr int kDigitBits = 11, kDigitBins = 1 << kDigitBits;
 constexpr double kMassUnit = 4503599627370496.0;  // 2^52: fixed-point unit of a block's share
+constexpr int kHeadsAtOnce = 8;   // query heads of one pass over the means
+
+struct RouteShared {
+  double red[kRouteWarps];
+  double top[kHeadsAtOnce], sum[kHeadsAtOnce];  // this CTA's maximum and sum of each head
+  double cand_p[kRankMost];
+  unsigned long long cand_mass[kRankMost];
+  int cand_at[kRankMost];
+  unsigned long long warp_mass[kRouteWarps];
+  int warp_cnt[kRouteWarps];
+  unsigned long long prefix, mass_above;
+  int cnt_above, in_bin, n_cand, bad;
+  // a bin's fixed-point mass in three 18-bit parts (16384 of them fit 32 bits: plain atomics)
+  // and its count
+  unsigned int bin[4][kDigitBins];
+};
 
 __device__ __forceinline__ double block_reduce(double v, bool take_max, double* sm) {
   v = take_max ? warp_max_d(v) : warp_sum_d(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int n = blockDim.x >> 5;
   double r = sm[0];
-  for (int i = 1; i < n; ++i) r = take_max ? fmax(r, sm[i]) : r + sm[i];
+  for (int i = 1; i < kRouteWarps; ++i) r = take_max ? fmax(r, sm[i]) : r + sm[i];
   return r;
 }
 
-// One CTA per (key head, sequence). Shares P_b in shared memory; the threshold is found
-// digit by digit (8 bits of the float64 pattern, which orders non-negative values): a digit's
-// bins hold their blocks' count and fixed-point mass, and the walk stops in the bin in which
-// the prefix first has both the mass and the count it needs. Integer sums: any order of the
-// atomics gives the same bins.
-__global__ void __launch_bounds__(512) cache_select_kernel(const double* __restrict__ scores, int H, int Hkv,
-                                                           int max_blocks, const int32_t* __restrict__ len_dev, double p,
-                                                           int k_floor, int n_recent, int32_t* __restrict__ kept,
-                                                           int32_t* __restrict__ n_kept) {
-  extern __shared__ __align__(16) double prob[];  // [max_blocks]
-  __shared__ double red[16];
-  __shared__ unsigned long long bin_mass[256];
-  __shared__ int bin_cnt[256];
-  __shared__ unsigned long long s_prefix, s_mass_above;
-  __shared__ int s_cnt_above, s_done, warp_cnt[16], s_nan;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int len = min(max(len_dev[b], 0), max_blocks * kBlock);
-  const int nB = (len + kBlock - 1) / kBlock;
-  int32_t* out = kept + (static_cast<int64_t>(b) * Hkv + h) * max_blocks;
-  const int G = H / Hkv;
+__device__ __forceinline__ unsigned long long fixed_mass(double p) {
+  return static_cast<unsigned long long>(__double2ll_rn(p * kMassUnit));
+}
 
-  if (tid == 0) s_nan = 0;
-  for (int i = tid; i < nB; i += nt) prob[i] = 0.0;
-  for (int g = 0; g < G; ++g) {
-    const double* s = scores + (static_cast<int64_t>(b) * H + h * G + g) * max_blocks;
-    double m = -INFINITY;
-    bool bad = false;
-    for (int i = tid; i < nB; i += nt) {
-      m = fmax(m, s[i]);
-      bad |= isnan(s[i]);
+// Sums v[i] over the warp for N values at once (N a power of two): lane l ends with value
+// l % N. Each halving step keeps half of the values, so N - 1 + log2(32 / N) exchanges do what
+// 5 N would.
+template <int N>
+__device__ __forceinline__ double warp_sum_many(double (&v)[N], int lane) {
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1) {
+    const bool up = lane & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const double send = up ? v[i] : v[i + n];
+      const double keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
     }
-    m = block_reduce(m, true, red);
-    double z = 0.0;
-    for (int i = tid; i < nB; i += nt) z += exp(s[i] - m);
-    z = block_reduce(z, false, red);
-    if (bad || !(z > 0.0) || isinf(z)) s_nan = 1;
-    for (int i = tid; i < nB; i += nt) prob[i] += exp(s[i] - m) / (z * G);
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// Scores of `ng` heads for the blocks [lo, hi): a warp takes eight blocks at a time, their means
+// all on their way before the first is used; lanes over the channels.
+template <typename T, int D, int NG>
+__device__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, int h, int lo, int hi, double scale,
+                             double* scores, int32_t* dev_status) {
+  constexpr int V = D / 32, kAtOnce = 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double qd[NG][V];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < V; ++i) qd[g][i] = g < ng ? static_cast<double>(to_f32(q[g * D + lane * V + i])) : 0.0;
+  for (int base = lo + warp * kAtOnce; base < hi; base += kRouteWarps * kAtOnce) {
+    int page = lane < kAtOnce && base + lane < hi ? page_of(c, b, base + lane, dev_status) : -1;
+    float m[kAtOnce][V];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int pg = __shfl_sync(0xffffffffu, page, k);
+      const float* mean = c.key_mean + (static_cast<int64_t>(pg < 0 ? 0 : pg) * c.Hkv + h) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(mean);
+        m[k][0] = x.x, m[k][1] = x.y, m[k][2] = x.z, m[k][3] = x.w;
+      } else if constexpr (V == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(mean);
+        m[k][0] = x.x, m[k][1] = x.y;
+      } else {
+        m[k][0] = mean[0];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (base + k >= hi) break;
+      double s[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        s[g] = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[g] = fma(qd[g][i], static_cast<double>(m[k][i]), s[g]);
+      }
+      double x = warp_sum_many<NG>(s, lane) * scale;
+      // a block without a page is never chosen for its score
+      if (__shfl_sync(0xffffffffu, page, k) < 0) x = -INFINITY;
+      if (lane < ng) scores[static_cast<int64_t>(lane) * c.max_blocks + base + k] = x;
+    }
+  }
+}
+
+// The selection, by the cluster's first CTA. Block i is kept when the blocks before it (larger
+// share, or equal and a lower index) lack the mass or the count the prefix needs. Up to 512
+// blocks are ranked against one another; of more, the bins of an 11-bit digit of the float64
+// pattern (which orders non-negative values) find the one in which the prefix ends, digit by
+// digit, until its blocks can be ranked. The sums are of integers: any order gives the same.
+// On return a kept block's share is +infinity or above the returned pattern.
+__device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int nB, double p, int k_floor) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned long long need_mass = static_cast<unsigned long long>(ceil(p * kMassUnit));
+  const int need_cnt = min(k_floor, nB);
+  int shift = 64;
+  if (tid == 0) {
+    sm.prefix = 0;
+    sm.mass_above = 0;
+    sm.cnt_above = 0;
+    sm.in_bin = nB;
+    sm.n_cand = 0;
   }
   __syncthreads();
-
-  unsigned long long threshold = 0;  // blocks with a larger pattern are kept, `ties` of the equal ones
-  int ties = 0;
-  const bool all = p >= 1.0 || s_nan || nB == 0;
-  if (!all) {
-    const unsigned long long need_mass = static_cast<unsigned long long>(ceil(p * kMassUnit));
-    const int need_cnt = min(k_floor, nB);
-    if (tid == 0) {
-      s_prefix = 0;
-      s_mass_above = 0;
-      s_cnt_above = 0;
-    }
-    for (int shift = 56; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += nt) {
-        bin_mass[i] = 0;
-        bin_cnt[i] = 0;
+  while (sm.in_bin > kRankMost && shift > 0) {
+    const int up = shift, width = shift >= kDigitBits ? kDigitBits : shift;
+    shift -= width;
+    for (int i = tid; i < kDigitBins; i += kRouteThreads) sm.bin[0][i] = sm.bin[1][i] = sm.bin[2][i] = sm.bin[3][i] = 0u;
+    __syncthreads();
+    const unsigned long long prefix = sm.prefix;
+    for (int base = 0; base < nB; base += kRouteThreads) {
+      const int i = base + tid;
+      const unsigned long long bits = i < nB ? __double_as_longlong(prob[i]) : 0ull;
+      const bool in = i < nB && (up == 64 || (bits >> up) == (prefix >> up));
+      const int d = in ? static_cast<int>((bits >> shift) & (kDigitBins - 1) & ((1 << width) - 1)) : -1;
+      int same;
+      __match_all_sync(0xffffffffu, d, &same);
+      const unsigned long long m = in ? fixed_mass(prob[i]) : 0ull;
+      unsigned int part[4] = {static_cast<unsigned int>(m & 0x3ffff), static_cast<unsigned int>((m >> 18) & 0x3ffff),
+                              static_cast<unsigned int>(m >> 36), in ? 1u : 0u};
+      if (same) {  // one digit in the whole warp (blocks of equal shares): one addition for it
+#pragma unroll
+        for (int k = 0; k < 4; ++k) part[k] = __reduce_add_sync(0xffffffffu, part[k]);
       }
-      __syncthreads();
-      const unsigned long long prefix = s_prefix;
-      for (int i = tid; i < nB; i += nt) {
-        const unsigned long long bits = __double_as_longlong(prob[i]);
-        if (shift == 56 || (bits >> (shift + 8)) == (prefix >> (shift + 8))) {
-          const int bin = static_cast<int>((bits >> shift) & 255);
-          atomicAdd(&bin_mass[bin], static_cast<unsigned long long>(rint(prob[i] * kMassUnit)));
-          atomicAdd(&bin_cnt[bin], 1);
-        }
+      if (d >= 0 && (!same || lane == 0)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (part[k]) atomicAdd(&sm.bin[k][d], part[k]);
       }
-      __syncthreads();
-      if (tid == 0) {
-        unsigned long long mass = s_mass_above;
-        int cnt = s_cnt_above, bin = 255, last = -1;
-        for (; bin >= 0; --bin) {
-          if (bin_cnt[bin] == 0) continue;
-          last = bin;
-          if (mass + bin_mass[bin] >= need_mass && cnt + bin_cnt[bin] >= need_cnt) break;
-          mass += bin_mass[bin];
-          cnt += bin_cnt[bin];
-        }
-        if (bin < 0) {  // rounding left the total below p: the smallest block ends the prefix
-          bin = last;
-          mass -= bin_mass[bin];
-          cnt -= bin_cnt[bin];
-        }
-        s_prefix = prefix | (static_cast<unsigned long long>(bin) << shift);
-        s_mass_above = mass;
-        s_cnt_above = cnt;
-        s_done = bin_cnt[bin];
+    }
+    __syncthreads();
+    // bins from the highest down: four a thread, then a scan over the threads
+    constexpr int kPer = kDigitBins / kRouteThreads;
+    unsigned long long m[kPer], tm = 0;
+    int n[kPer], tn = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int d = kDigitBins - 1 - (tid * kPer + k);
+      m[k] = sm.bin[0][d] + (static_cast<unsigned long long>(sm.bin[1][d]) << 18) +
+             (static_cast<unsigned long long>(sm.bin[2][d]) << 36);
+      n[k] = static_cast<int>(sm.bin[3][d]);
+      tm += m[k];
+      tn += n[k];
+    }
+    unsigned long long im = tm;
+    int in = tn;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long a = __shfl_up_sync(0xffffffffu, im, o);
+      const int e = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) {
+        im += a;
+        in += e;
       }
-      __syncthreads();
     }
-    threshold = s_prefix;
-    const double v = __longlong_as_double(threshold);
-    const unsigned long long one = static_cast<unsigned long long>(rint(v * kMassUnit));
-    ties = max(need_cnt - s_cnt_above, 1);
-    if (s_mass_above < need_mass) {
-      const unsigned long long lack = need_mass - s_mass_above;
-      const unsigned long long n = one ? (lack + one - 1) / one : static_cast<unsigned long long>(s_done);
-      if (n > static_cast<unsigned long long>(ties)) ties = n > static_cast<unsigned long long>(nB) ? nB : static_cast<int>(n);
+    if (lane == 31) {
+      sm.warp_mass[warp] = im;
+      sm.warp_cnt[warp] = in;
     }
+    __syncthreads();
+    unsigned long long mass = sm.mass_above + im - tm, total = sm.mass_above;
+    int cnt = sm.cnt_above + in - tn;
+    const int in_bin = sm.in_bin, cnt_before = sm.cnt_above;
+    for (int w = 0; w < kRouteWarps; ++w) {
+      if (w < warp) {
+        mass += sm.warp_mass[w];
+        cnt += sm.warp_cnt[w];
+      }
+      total += sm.warp_mass[w];
+    }
+    __syncthreads();
+    // the bin in which the prefix first has both; where rounding leaves the total below p, the
+    // lowest one that holds a block
+    const bool short_of = total < need_mass;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const bool before = mass < need_mass || cnt < need_cnt;
+      const bool after = mass + m[k] < need_mass || cnt + n[k] < need_cnt;
+      const bool here = n[k] > 0 && before && (!after || (short_of && cnt + n[k] == cnt_before + in_bin));
+      if (here) {
+        const int d = kDigitBins - 1 - (tid * kPer + k);
+        sm.prefix = prefix | (static_cast<unsigned long long>(d) << shift);
+        sm.mass_above = mass;
+        sm.cnt_above = cnt;
+        sm.in_bin = n[k];
+      }
+      mass += m[k];
+      cnt += n[k];
+    }
+    __syncthreads();
   }
-  // emission in block order, 512 blocks at a time
-  int written = 0, tied = 0;
-  for (int base = 0; base < nB; base += nt) {
+  const unsigned long long prefix = sm.prefix;
+  if (sm.in_bin <= kRankMost) {
+    for (int i = tid; i < nB; i += kRouteThreads) {
+      const unsigned long long bits = __double_as_longlong(prob[i]);
+      if (shift == 64 || (bits >> shift) == (prefix >> shift)) {
+        const int at = atomicAdd(&sm.n_cand, 1);
+        sm.cand_p[at] = prob[i];
+        sm.cand_mass[at] = fixed_mass(prob[i]);
+        sm.cand_at[at] = i;
+      }
+    }
+    __syncthreads();
+    const int n = sm.n_cand;
+    if (tid < n) {
+      const double mine = sm.cand_p[tid];
+      const int at = sm.cand_at[tid];
+      unsigned long long mass = sm.mass_above;
+      int cnt = sm.cnt_above;
+      for (int j = 0; j < n; ++j) {
+        const double o = sm.cand_p[j];
+        const bool first = o > mine || (o == mine && sm.cand_at[j] < at);
+        mass += first ? sm.cand_mass[j] : 0ull;
+        cnt += first;
+      }
+      prob[at] = mass < need_mass || cnt < need_cnt ? INFINITY : -1.0;
+    }
+    __syncthreads();
+    // what is left above the candidates' bin: patterns from the next prefix on
+    if (shift == 64) return 0x7fefffffffffffffull;
+    return (((prefix >> shift) + 1) << shift) - 1;
+  }
+  // more than 512 blocks of one and the same share: the first ones of them, by index
+  const unsigned long long one = fixed_mass(__longlong_as_double(prefix));
+  long long ties = max(need_cnt - sm.cnt_above, 1);
+  if (sm.mass_above < need_mass) {
+    const unsigned long long lack = need_mass - sm.mass_above;
+    const unsigned long long n = one ? (lack + one - 1) / one : static_cast<unsigned long long>(sm.in_bin);
+    if (n > static_cast<unsigned long long>(ties)) ties = n > static_cast<unsigned long long>(nB) ? nB : static_cast<long long>(n);
+  }
+  int before = 0;  // equal ones at lower indices
+  for (int base = 0; base < nB; base += kRouteThreads) {
     const int i = base + tid;
-    const unsigned long long bits = i < nB ? __double_as_longlong(prob[i]) : 0ull;
-    const bool eq = !all && i < nB && bits == threshold;
-    // rank among the equal ones
-    const unsigned eqm = __ballot_sync(0xffffffffu, eq);
+    const bool eq = i < nB && static_cast<unsigned long long>(__double_as_longlong(prob[i])) == prefix;
+    const unsigned mask = __ballot_sync(0xffffffffu, eq);
     __syncthreads();
-    if (lane == 0) warp_cnt[warp] = __popc(eqm);
+    if (lane == 0) sm.warp_cnt[warp] = __popc(mask);
     __syncthreads();
-    int before = tied + __popc(eqm & ((1u << lane) - 1u)), total = 0;
-    for (int w = 0; w < (nt >> 5); ++w) {
-      if (w < warp) before += warp_cnt[w];
-      total += warp_cnt[w];
+    int at = before + __popc(mask & ((1u << lane) - 1u));
+    for (int w = 0; w < kRouteWarps; ++w) {
+      if (w < warp) at += sm.warp_cnt[w];
+      before += sm.warp_cnt[w];
     }
-    tied += total;
-    const bool keep = i < nB && (all || bits > threshold || (eq && before < ties) || i >= nB - n_recent);
-    const unsigned km = __ballot_sync(0xffffffffu, keep);
-    __syncthreads();
-    if (lane == 0) warp_cnt[warp] = __popc(km);
-    __syncthreads();
-    int at = written + __popc(km & ((1u << lane) - 1u));
-    total = 0;
-    for (int w = 0; w < (nt >> 5); ++w) {
-      if (w < warp) at += warp_cnt[w];
-      total += warp_cnt[w];
-    }
-    if (keep) out[at] = i;
-    written += total;
+    if (eq) prob[i] = at < ties ? INFINITY : -1.0;
   }
-  for (int i = written + tid; i < max_blocks; i += nt) out[i] = -1;
-  if (tid == 0) n_kept[static_cast<int64_t>(b) * Hkv + h] = written;
+  __syncthreads();
+  return prefix;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
+                                                              int H, double scale, double p, int k_floor, int n_recent,
+                                                              double* __restrict__ scores, int32_t* __restrict__ kept,
+                                                              int32_t* __restrict__ n_kept, int32_t* dev_status) {
+  extern __shared__ __align__(16) double prob[];  // [max_blocks], used in the cluster's first CTA
+  __shared__ RouteShared sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = seq_len(c, b, dev_status);
+  const int nB = (len + kBlock - 1) / kBlock, G = H / c.Hkv;
+  const int per = (nB + C - 1) / C, lo = min(rank * per, nB), hi = min(lo + per, nB);
+  double* const gathered = cluster.map_shared_rank(prob, 0);
+  if (tid == 0) sm.bad = 0;
+
+  for (int g0 = 0; g0 < G; g0 += kHeadsAtOnce) {
+    const int ng = min(G - g0, kHeadsAtOnce);
+    const T* qg = q + b * q_stride + static_cast<int64_t>(h * G + g0) * D;
+    double* sg = scores + (static_cast<int64_t>(b) * H + h * G + g0) * c.max_blocks;
+    if (ng == 1) block_scores<T, D, 1>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
+    else if (ng == 2) block_scores<T, D, 2>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
+    else if (ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
+    else block_scores<T, D, 8>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
+    __syncthreads();
+    for (int g = 0; g < ng; ++g) {
+      const double* s = sg + static_cast<int64_t>(g) * c.max_blocks;
+      double m = -INFINITY;
+      bool nan = false;
+      for (int i = lo + tid; i < hi; i += kRouteThreads) {
+        m = fmax(m, s[i]);
+        nan |= isnan(s[i]);
+      }
+      if (nan) sm.bad = 1;
+      m = block_reduce(m, true, sm.red);
+      double z = 0.0;
+      for (int i = lo + tid; i < hi; i += kRouteThreads) z += exp(s[i] - m);
+      z = block_reduce(z, false, sm.red);
+      if (tid == 0) {
+        sm.top[g] = m;
+        sm.sum[g] = z;
+      }
+    }
+    cluster.sync();
+    double top[kHeadsAtOnce], inv[kHeadsAtOnce];
+#pragma unroll
+    for (int g = 0; g < kHeadsAtOnce; ++g) {
+      top[g] = -INFINITY;
+      double z = 0.0;
+      if (g < ng) {
+        for (int r = 0; r < C; ++r) top[g] = fmax(top[g], cluster.map_shared_rank(sm.top, r)[g]);
+        for (int r = 0; r < C; ++r) {
+          const double t = cluster.map_shared_rank(sm.top, r)[g];
+          if (t > -INFINITY || nB == 0) z += cluster.map_shared_rank(sm.sum, r)[g] * exp(t - top[g]);
+        }
+        if (!(z > 0.0) || isinf(z)) sm.bad = 1;  // no finite score, or a NaN
+      }
+      inv[g] = 1.0 / (z * G);
+    }
+    // a block's share is a function of its scores alone (the cluster-wide maximum and sum), so
+    // blocks of equal scores have equal shares whichever CTA holds them
+    for (int i = lo + tid; i < hi; i += kRouteThreads) {
+      double x = g0 > 0 ? gathered[i] : 0.0;
+#pragma unroll
+      for (int g = 0; g < kHeadsAtOnce; ++g)
+        if (g < ng) x += exp(sg[static_cast<int64_t>(g) * c.max_blocks + i] - top[g]) * inv[g];
+      gathered[i] = x;
+    }
+    cluster.sync();  // the next heads overwrite the maxima; at the end, the shares are complete
+  }
+  bool bad = false;
+  for (int r = 0; r < C; ++r) bad |= *cluster.map_shared_rank(&sm.bad, r) != 0;
+  cluster.sync();  // nobody leaves while its shared memory is read
+  if (rank != 0) return;
+
+  const bool all = p >= 1.0 || bad || nB == 0;
+  const unsigned long long above = all ? 0ull : select_blocks(sm, prob, nB, p, k_floor);
+  // emission in block order, a contiguous piece a warp
+  int32_t* out = kept + (static_cast<int64_t>(b) * c.Hkv + h) * c.max_blocks;
+  const int piece = ((nB + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32, w0 = warp * piece;
+  auto keep = [&](int i) -> bool {
+    if (i >= nB) return false;
+    const double x = prob[i];
+    return all || i >= nB - n_recent || (x >= 0.0 && static_cast<unsigned long long>(__double_as_longlong(x)) > above);
+  };
+  int n = 0;
+  for (int i = w0; i < w0 + piece && i < nB; i += 32) n += __popc(__ballot_sync(0xffffffffu, keep(i + lane)));
+  __syncthreads();
+  if (lane == 0) sm.warp_cnt[warp] = n;
+  __syncthreads();
+  int at = 0, total = 0;
+  for (int w = 0; w < kRouteWarps; ++w) {
+    if (w < warp) at += sm.warp_cnt[w];
+    total += sm.warp_cnt[w];
+  }
+  for (int i = w0; i < w0 + piece && i < nB; i += 32) {
+    const bool k = keep(i + lane);
+    const unsigned mask = __ballot_sync(0xffffffffu, k);
+    if (k) out[at + __popc(mask & ((1u << lane) - 1u))] = i + lane;
+    at += __popc(mask);
+  }
+  for (int i = total + tid; i < c.max_blocks; i += kRouteThreads) out[i] = -1;
+  if (tid == 0) n_kept[static_cast<int64_t>(b) * c.Hkv + h] = total;
 }
 
 // ---------------------------------------------------------------------------------
 // Eviction
 // ---------------------------------------------------------------------------------
 // Order-preserving pattern of a weight: larger weight, larger pattern; -0 as 0, NaN lowest.
+constexpr uint32_t kZeroMass = 0x80000000u;
 __device__ __forceinline__ uint32_t mass_key(float x) {
   if (isnan(x)) return 0u;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA per (key head, sequence): radix selection of the threshold over the middle tokens,
-// then the kept positions in order.
+// A cluster of CTAs per (key head, sequence), each with a contiguous share of the tokens. The
+// threshold among the middle tokens is found in three digits (11, 11, 10 bits) from the
+// cluster-wide histograms; then the shares' counts place every share's kept tokens. The
+// patterns stay in shared memory between the passes while a share fits (`hold` tokens).
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictWarps = kEvictThreads / 32;
+
 template <typename T>
-__global__ void __launch_bounds__(1024) evict_select_kernel(CacheView<T> c, int keep, int n_sink, int n_recent,
-                                                            int32_t* __restrict__ kept, int32_t* __restrict__ new_len,
-                                                            int32_t* dev_status) {
-  __shared__ int bins[256];
+__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T> c, int keep, int n_sink, int n_recent,
+                                                                     int hold, int32_t* __restrict__ kept,
+                                                                     int32_t* __restrict__ new_len,
+                                                                     int32_t* dev_status) {
+  extern __shared__ uint32_t held[];  // [hold]
+  __shared__ uint32_t bins[2048];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need, warp_cnt[32];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int s_need, warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = seq_len(c, b, dev_status);
   int32_t* out = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep;
-  if (h == 0 && tid == 0) new_len[b] = min(len, keep);
-  auto key = [&](int t) -> uint32_t {
+  if (h == 0 && rank == 0 && tid == 0) new_len[b] = min(len, keep);
+  if (len <= keep) {
+    for (int i = rank * kEvictThreads + tid; i < keep; i += C * kEvictThreads) out[i] = i < len ? i : -1;
+    return;
+  }
+  // shares end on block borders, so a warp's 32 tokens lie in one page
+  const int per = ((len + C - 1) / C + kBlock - 1) / kBlock * kBlock, t0 = min(rank * per, len), t1 = min(t0 + per, len);
+  const bool fits = per <= hold;
+  auto load_key = [&](int t) -> uint32_t {
     const int page = page_of(c, b, t / kBlock, dev_status);
     return page < 0 ? 0u : mass_key(c.mass[(static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock]);
   };
-  if (len <= keep) {
-    for (int i = tid; i < keep; i += nt) out[i] = i < len ? i : -1;
-    return;
+  if (fits) {
+    for (int t = t0 + tid; t < t1; t += kEvictThreads) held[t - t0] = load_key(t);
+    __syncthreads();
   }
-  const int lo = n_sink, hi = len - n_recent;
-  int need = keep - n_sink - n_recent;  // of the tokens lo .. hi - 1, of which there are more
+  auto key = [&](int t) -> uint32_t { return fits ? held[t - t0] : load_key(t); };
+  const int lo = n_sink, hi = len - n_recent;  // the middle, of which `need` tokens stay
+  int need = keep - n_sink - n_recent;
+  const bool some = need > 0;
   uint32_t prefix = 0;
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += nt) bins[i] = 0;
+  int shift = 32;
+  for (int pass = 0; pass < 3 && some; ++pass) {
+    const int up = shift, width = pass < 2 ? 11 : 10;
+    shift -= width;
+    for (int i = tid; i < 2048; i += kEvictThreads) bins[i] = 0u;
     __syncthreads();
-    for (int t = lo + tid; t < hi; t += nt) {
+    uint32_t zeros = 0;  // tokens that were never attended to, often many: counted aside
+    for (int t = max(t0, lo) + tid; t < min(t1, hi); t += kEvictThreads) {
       const uint32_t u = key(t);
-      if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&bins[(u >> shift) & 255], 1);
+      if (pass > 0 && (u >> up) != (prefix >> up)) continue;
+      if (u == kZeroMass)
+        ++zeros;
+      else
+        atomicAdd(&bins[(u >> shift) & ((1u << width) - 1u)], 1u);
     }
-    __syncthreads();
-    if (tid == 0) {
-      int bin = 255, left = need;
-      while (bin > 0 && bins[bin] < left) left -= bins[bin--];
-      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-      s_need = left;
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros) atomicAdd(&bins[(kZeroMass >> shift) & ((1u << width) - 1u)], zeros);
+    cluster.sync();
+    // two bins a thread, from the highest down; every CTA finds the same one
+    uint32_t n0 = 0, n1 = 0;
+    const int d0 = 2047 - 2 * tid;
+    for (int r = 0; r < C; ++r) {
+      const uint32_t* o = cluster.map_shared_rank(bins, r);
+      n0 += o[d0];
+      n1 += o[d0 - 1];
     }
+    int inc = static_cast<int>(n0 + n1);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_a[warp] = inc;
     __syncthreads();
+    int before = inc - static_cast<int>(n0 + n1);
+    for (int w = 0; w < warp; ++w) before += warp_a[w];
+    if (before < need && need <= before + static_cast<int>(n0 + n1)) {
+      const bool first = need <= before + static_cast<int>(n0);
+      s_prefix = prefix | (static_cast<uint32_t>(first ? d0 : d0 - 1) << shift);
+      s_need = need - before - (first ? 0 : static_cast<int>(n0));
+    }
+    cluster.sync();  // the bins have been read everywhere
     prefix = s_prefix;
     need = s_need;
   }
-  // keys above the threshold, `need` of the equal ones (the earliest), the ends
-  const bool some = keep > n_sink + n_recent;
-  int written = 0, tied = 0;
-  for (int base = 0; base < len; base += nt) {
-    const int t = base + tid;
-    const bool middle = t >= lo && t < hi;
-    const uint32_t u = middle && some ? key(t) : 0u;
-    const bool eq = middle && some && u == prefix;
-    const unsigned eqm = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) warp_cnt[warp] = __popc(eqm);
-    __syncthreads();
-    int before = tied + __popc(eqm & ((1u << lane) - 1u)), total = 0;
-    for (int w = 0; w < (nt >> 5); ++w) {
-      if (w < warp) before += warp_cnt[w];
-      total += warp_cnt[w];
-    }
-    tied += total;
-    const bool take = t < len && (!middle || (some && (u > prefix || (eq && before < need))));
-    const unsigned km = __ballot_sync(0xffffffffu, take);
-    __syncthreads();
-    if (lane == 0) warp_cnt[warp] = __popc(km);
-    __syncthreads();
-    int at = written + __popc(km & ((1u << lane) - 1u));
-    total = 0;
-    for (int w = 0; w < (nt >> 5); ++w) {
-      if (w < warp) at += warp_cnt[w];
-      total += warp_cnt[w];
-    }
-    if (take) out[at] = t;
-    written += total;
+  // keys above the threshold and both ends stay, and the first `need` of the equal ones
+  const int piece = (per / kEvictWarps + 31) / 32 * 32, w0 = t0 + warp * piece, w1 = min(w0 + piece, t1);
+  auto classify = [&](int t, bool& above, bool& equal) {
+    const bool in = t < w1, middle = t >= lo && t < hi;
+    const uint32_t u = in && middle && some ? key(t) : 0u;
+    above = in && (!middle || (some && u > prefix));
+    equal = in && middle && some && u == prefix;
+  };
+  int na = 0, ne = 0;
+  for (int base = w0; base < w1; base += 32) {
+    bool a, e;
+    classify(base + lane, a, e);
+    na += __popc(__ballot_sync(0xffffffffu, a));
+    ne += __popc(__ballot_sync(0xffffffffu, e));
   }
+  if (lane == 0) {
+    warp_a[warp] = na;
+    warp_e[warp] = ne;
+  }
+  __syncthreads();
+  int above = 0, equal = 0;
+  if (tid == 0) {
+    for (int w = 0; w < kEvictWarps; ++w) {
+      above += warp_a[w];
+      equal += warp_e[w];
+    }
+    mine[0] = above;
+    mine[1] = equal;
+  }
+  cluster.sync();
+  above = equal = 0;
+  for (int r = 0; r < rank; ++r) {
+    above += cluster.map_shared_rank(mine, r)[0];
+    equal += cluster.map_shared_rank(mine, r)[1];
+  }
+  for (int w = 0; w < warp; ++w) {
+    above += warp_a[w];
+    equal += warp_e[w];
+  }
+  for (int base = w0; base < w1; base += 32) {
+    bool a, e;
+    classify(base + lane, a, e);
+    const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
+    const unsigned below = (1u << lane) - 1u;
+    const int rank_e = equal + __popc(em & below);
+    if (a || (e && rank_e < need)) out[above + __popc(am & below) + min(rank_e, need)] = base + lane;
+    above += __popc(am);
+    equal += __popc(em);
+  }
+  cluster.sync();  // nobody leaves while its counts are read
 }
 
 // One CTA per (destination block, key head, sequence): gathers its 64 kept tokens.
-template <typename T>
-__global__ void __launch_bounds__(128) evict_copy_kernel(CacheView<T> c, int d, int keep,
-                                                         const int32_t* __restrict__ dst_table, int dst_blocks,
-                                                         const int32_t* __restrict__ kept, int32_t* dev_status) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c, int keep,
+                                                                  const int32_t* __restrict__ dst_table, int dst_blocks,
+                                                                  const int32_t* __restrict__ kept,
+                                                                  int32_t* dev_status) {
+  using P = PageRows<T, D>;
   const int b = blockIdx.z, h = blockIdx.y, block = blockIdx.x;
   const int len = seq_len(c, b, nullptr);
   const int n = min(min(len, keep) - block * kBlock, kBlock);
   if (n <= 0) return;
+  const int lane = threadIdx.x / P::kPieces, piece = threadIdx.x % P::kPieces;
+  const int32_t* src_at = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep + block * kBlock;
   const int dst = dst_table[static_cast<int64_t>(b) * dst_blocks + block];
+  uint4 k[P::kRows], v[P::kRows];
+  float mass[P::kRows];
+#pragma unroll
+  for (int i = 0; i < P::kRows; ++i) {
+    const int r = lane + i * P::kLanes;
+    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    mass[i] = 0.0f;
+    if (r < n) {
+      const int t = src_at[r];
+      const int page = page_of(c, b, t / kBlock, dev_status);
+      if (page >= 0) {
+        const int64_t from = (static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock;
+        k[i] = reinterpret_cast<const uint4*>(c.k + from * D)[piece];
+        v[i] = reinterpret_cast<const uint4*>(c.v + from * D)[piece];
+        if (piece == 0) mass[i] = c.mass[from];
+      }
+    }
+  }
   bool clash = false;
-  for (int i = threadIdx.x; i * kBlock < len; i += blockDim.x)
+  for (int i = threadIdx.x; i * kBlock < len; i += kPageThreads)
     clash |= c.table[static_cast<int64_t>(b) * c.max_blocks + i] == dst;
   if (__syncthreads_or(clash) || dst < 0 || dst >= c.n_pages) {
     if (threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
     return;
   }
-  const int32_t* src_at = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep + block * kBlock;
   const int64_t to = (static_cast<int64_t>(dst) * c.Hkv + h) * kBlock;
-  const int vecs = d * static_cast<int>(sizeof(T)) / 16;
-  for (int i = threadIdx.x; i < n * vecs; i += blockDim.x) {
-    const int r = i / vecs, p = i % vecs, t = src_at[r];
-    const int page = page_of(c, b, t / kBlock, dev_status);
-    const int64_t from = (static_cast<int64_t>(page < 0 ? dst : page) * c.Hkv + h) * kBlock + (page < 0 ? r : t % kBlock);
-    reinterpret_cast<uint4*>(c.k + (to + r) * d)[p] = reinterpret_cast<const uint4*>(c.k + from * d)[p];
-    reinterpret_cast<uint4*>(c.v + (to + r) * d)[p] = reinterpret_cast<const uint4*>(c.v + from * d)[p];
-    if (p == 0) c.mass[to + r] = c.mass[from];
+#pragma unroll
+  for (int i = 0; i < P::kRows; ++i) {
+    const int r = lane + i * P::kLanes;
+    if (r < n) {
+      reinterpret_cast<uint4*>(c.k + (to + r) * D)[piece] = k[i];
+      reinterpret_cast<uint4*>(c.v + (to + r) * D)[piece] = v[i];
+      if (piece == 0) c.mass[to + r] = mass[i];
+    }
   }
-  __syncthreads();
-  write_mean(c.k + to * d, n, d, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * d);
+  write_mean<T, D>(k, n, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * D);
 }
 
 // ---------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------
-template <typename T>
-static cudaError_t append_t(const fva_cache* c, const fva_seqs* s, const void* k_new, const void* v_new, int64_t stride,
-                            const int32_t* new_ptr, int max_new, int32_t* dev_status, cudaStream_t st) {
-  // a sequence's new tokens touch at most this many blocks
-  const dim3 grid(static_cast<unsigned>((max_new + kBlock - 2) / kBlock + 1), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B));
-  append_kernel<T><<<grid, 128, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(k_new), static_cast<const T*>(v_new),
-                                         stride, c->d, new_ptr, max_new, dev_status);
-  return cudaGetLastError();
+// CTAs of a unit's cluster: doubled while the units leave SMs idle and every CTA keeps at
+// least `least` items, up to 8 (portable).
+static int cluster_size(int64_t units, int64_t items, int64_t least) {
+  int n = 1;
+  while (n < 8 && units * n * 2 <= 148 && items / (2 * n) >= least) n *= 2;
+  return n;
 }
+
+template <typename... Args>
+static cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int threads, int cluster, size_t smem,
+                                  cudaStream_t st, Args... args) {
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+struct AppendCall {
+  const fva_cache* c;
+  const fva_seqs* s;
+  const void *k_new, *v_new;
+  int64_t stride;
+  const int32_t* new_ptr;
+  int max_new;
+  int32_t* dev_status;
+  cudaStream_t st;
+  template <typename T, int D>
+  cudaError_t operator()() const {
+    // a sequence's new tokens touch at most this many blocks
+    const dim3 grid(static_cast<unsigned>((max_new + kBlock - 2) / kBlock + 1), static_cast<unsigned>(c->Hkv),
+                    static_cast<unsigned>(s->B));
+    append_kernel<T, D><<<grid, kPageThreads, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(k_new),
+                                                       static_cast<const T*>(v_new), stride, new_ptr, max_new, dev_status);
+    return cudaGetLastError();
+  }
+};
 
 cudaError_t launch_cache_append(const fva_cache* c, const fva_seqs* s, const void* k_new, const void* v_new,
                                 int64_t stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
                                 cudaStream_t st) {
-  if (c->dtype == FVA_BF16) return append_t<__nv_bfloat16>(c, s, k_new, v_new, stride, new_ptr, max_new, dev_status, st);
-  if (c->dtype == FVA_F16) return append_t<__half>(c, s, k_new, v_new, stride, new_ptr, max_new, dev_status, st);
-  return append_t<float>(c, s, k_new, v_new, stride, new_ptr, max_new, dev_status, st);
+  return by_cache_type(c, AppendCall{c, s, k_new, v_new, stride, new_ptr, max_new, dev_status, st});
 }
 
-template <typename T>
-static cudaError_t scores_t(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride, double scale,
-                            double* scores, int32_t* dev_status, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((s->max_blocks + 3) / 4), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B));
-  cache_scores_kernel<T><<<grid, 128, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, c->d, scale,
-                                               scores, dev_status);
-  return cudaGetLastError();
-}
+struct RouteCall {
+  const fva_cache* c;
+  const fva_seqs* s;
+  const void* q;
+  int H;
+  int64_t q_stride;
+  double p, scale;
+  int k_floor, n_recent;
+  int32_t *kept, *n_kept;
+  double* scores;
+  int32_t* dev_status;
+  cudaStream_t st;
+  template <typename T, int D>
+  cudaError_t operator()() const {
+    const int C = cluster_size(static_cast<int64_t>(s->B) * c->Hkv, s->max_blocks, 64);
+    return launch_cluster(route_kernel<T, D>,
+                          dim3(static_cast<unsigned>(C), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
+                          kRouteThreads, C, static_cast<size_t>(s->max_blocks) * sizeof(double), st, cache_view<T>(c, s),
+                          static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, scores, kept, n_kept,
+                          dev_status);
+  }
+};
 
 cudaError_t launch_cache_route(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride, double p,
                                int k_floor, int n_recent, double scale, int32_t* kept, int32_t* n_kept, double* scores,
                                int32_t* dev_status, cudaStream_t st) {
-  cudaError_t e = c->dtype == FVA_BF16  ? scores_t<__nv_bfloat16>(c, s, q, H, q_stride, scale, scores, dev_status, st)
-                  : c->dtype == FVA_F16 ? scores_t<__half>(c, s, q, H, q_stride, scale, scores, dev_status, st)
-                                        : scores_t<float>(c, s, q, H, q_stride, scale, scores, dev_status, st);
-  if (e != cudaSuccess) return e;
-  const size_t smem = static_cast<size_t>(s->max_blocks) * sizeof(double);
-  e = cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  cache_select_kernel<<<dim3(static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)), 512, smem, st>>>(
-      scores, H, c->Hkv, s->max_blocks, s->len, p, k_floor, n_recent, kept, n_kept);
-  return cudaGetLastError();
+  return by_cache_type(c, RouteCall{c, s, q, H, q_stride, p, scale, k_floor, n_recent, kept, n_kept, scores, dev_status, st});
 }
 
-template <typename T>
-static cudaError_t evict_t(const fva_cache* c, const fva_seqs* s, int keep, int n_sink, int n_recent,
-                           const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len,
-                           int32_t* dev_status, cudaStream_t st) {
-  const CacheView<T> v = cache_view<T>(c, s);
-  const unsigned Hkv = static_cast<unsigned>(c->Hkv), B = static_cast<unsigned>(s->B);
-  evict_select_kernel<T><<<dim3(Hkv, B), 1024, 0, st>>>(v, keep, n_sink, n_recent, kept, new_len, dev_status);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  evict_copy_kernel<T><<<dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B), 128, 0, st>>>(
-      v, c->d, keep, dst_table, dst_blocks, kept, dev_status);
-  return cudaGetLastError();
-}
+struct EvictCall {
+  const fva_cache* c;
+  const fva_seqs* s;
+  int keep, n_sink, n_recent;
+  const int32_t* dst_table;
+  int dst_blocks;
+  int32_t *kept, *new_len, *dev_status;
+  cudaStream_t st;
+  template <typename T, int D>
+  cudaError_t operator()() const {
+    const CacheView<T> v = cache_view<T>(c, s);
+    const unsigned Hkv = static_cast<unsigned>(c->Hkv), B = static_cast<unsigned>(s->B);
+    const int tokens = s->max_blocks * kBlock, C = cluster_size(static_cast<int64_t>(B) * Hkv, tokens, 4096);
+    const int per = ((tokens + C - 1) / C + kBlock - 1) / kBlock * kBlock, most = 200 * 1024 / 4;
+    const int hold = per <= most ? per : 0;
+    cudaError_t e = launch_cluster(evict_select_kernel<T>, dim3(static_cast<unsigned>(C), Hkv, B), kEvictThreads, C,
+                                   static_cast<size_t>(hold) * 4, st, v, keep, n_sink, n_recent, hold, kept, new_len,
+                                   dev_status);
+    if (e != cudaSuccess) return e;
+    evict_copy_kernel<T, D><<<dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B), kPageThreads, 0, st>>>(
+        v, keep, dst_table, dst_blocks, kept, dev_status);
+    return cudaGetLastError();
+  }
+};
 
 cudaError_t launch_cache_evict(const fva_cache* c, const fva_seqs* s, int keep, int n_sink, int n_recent,
                                const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len,
                                int32_t* dev_status, cudaStream_t st) {
-  if (c->dtype == FVA_BF16)
-    return evict_t<__nv_bfloat16>(c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, dev_status, st);
-  if (c->dtype == FVA_F16)
-    return evict_t<__half>(c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, dev_status, st);
-  return evict_t<float>(c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, dev_status, st);
+  return by_cache_type(c, EvictCall{c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, dev_status, st});
 }
 
 }  // namespace fva

@@ -7,10 +7,8 @@
 
 namespace fva {
 
-struct CacheDims {
-  int B, Hkv, d, max_blocks, n_pages, dtype, esize;
-};
 constexpr int kMaxCacheBlocks = 16384;  // one CTA's shared memory holds a float64 per block
+constexpr int kMaxCacheGroup = 128;     // query heads per key head
 
 // Pointers of one cache and one batch of sequences, as the kernels take them.
 template <typename T>
@@ -57,6 +55,16 @@ __device__ __forceinline__ void from_f32(float x, float* o) { *o = x; }
 __device__ __forceinline__ void from_f32(float x, __nv_bfloat16* o) { *o = __float2bfloat16(x); }
 __device__ __forceinline__ void from_f32(float x, __half* o) { *o = __float2half_rn(x); }
 
+// Calls f with the element type and the head dim as template arguments.
+template <typename F>
+inline cudaError_t by_cache_type(const fva_cache* c, const F& f) {
+  if (c->dtype == FVA_BF16)
+    return c->d == 128 ? f.template operator()<__nv_bfloat16, 128>() : f.template operator()<__nv_bfloat16, 64>();
+  if (c->dtype == FVA_F16) return c->d == 128 ? f.template operator()<__half, 128>() : f.template operator()<__half, 64>();
+  if (c->d == 128) return f.template operator()<float, 128>();
+  return c->d == 64 ? f.template operator()<float, 64>() : f.template operator()<float, 32>();
+}
+
 cudaError_t launch_cache_append(const fva_cache* c, const fva_seqs* q, const void* k_new, const void* v_new,
                                 int64_t token_stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
                                 cudaStream_t st);
@@ -64,9 +72,11 @@ cudaError_t launch_cache_route(const fva_cache* c, const fva_seqs* s, const void
                                int k_floor, int n_recent, double scale, int32_t* kept, int32_t* n_kept, double* scores,
                                int32_t* dev_status, cudaStream_t st);
 struct CacheAttnScratch {
-  float* part;    // [2 * CTAs][16][d + 2]: unfinished rows' O, maximum and sum
-  float* scores;  // [B, H, 64 * max_blocks], log2 units; only when weights are accumulated
-  float* lse;     // [B, H] log2 units
+  float* part;     // [2 * shares][16][d + 2]: unfinished rows' O, maximum and sum
+  int64_t* start;  // [units] first block of a unit among all units' blocks
+  int64_t* per;    // blocks of a share
+  float* scores;   // [B, H, 64 * max_blocks], log2 units; only when weights are accumulated
+  float* lse;      // [B, H] log2 units, likewise
 };
 size_t cache_attn_part_floats(int d);
 cudaError_t launch_cache_attn(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride,

@@ -435,7 +435,7 @@ static int check_cache(const fva_cache* c, const fva_seqs* q) {
 // Query rows: H a multiple of Hkv, rows that start on 16 bytes.
 static int check_query(const fva_cache* c, const fva_seqs* q, const void* q_dev, int H, int64_t q_stride) {
   if (!q_dev) return FVA_ERR_INVALID_ARG;
-  if (H < 1 || H > 65535 || H % c->Hkv != 0) return FVA_ERR_UNSUPPORTED_SHAPE;
+  if (H < 1 || H > 65535 || H % c->Hkv != 0 || H / c->Hkv > kMaxCacheGroup) return FVA_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<int64_t>(q->B) * H > 0x7fffffffLL) return FVA_ERR_UNSUPPORTED_SHAPE;
   if (q_stride < static_cast<int64_t>(H) * c->d) return FVA_ERR_INVALID_ARG;
   if (!aligned16(q_dev) || q_stride * (c->dtype == FVA_F32 ? 4 : 2) % 16 != 0) return FVA_ERR_ALIGNMENT;
@@ -486,6 +486,8 @@ static size_t cache_attn_layout(const fva_cache* c, int B, int max_blocks, int H
   Carver k{static_cast<uint8_t*>(ws), 0};
   CacheAttnScratch a{};
   a.part = k.take<float>(cache_attn_part_floats(c->d) * sizeof(float));
+  a.per = k.take<int64_t>(sizeof(int64_t));
+  a.start = k.take<int64_t>(static_cast<size_t>(B) * H * sizeof(int64_t));  // at most a unit per query head
   if (accumulate) {
     a.lse = k.take<float>(static_cast<size_t>(B) * H * sizeof(float));
     a.scores = k.take<float>(static_cast<size_t>(B) * H * max_blocks * kBlock * sizeof(float));

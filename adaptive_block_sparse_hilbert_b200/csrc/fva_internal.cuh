@@ -86,8 +86,8 @@ cudaError_t launch_attn_bwd(const Dims& D, const BwdArgs& x, const fva_mask* m, 
                             int32_t* dev_status, cudaStream_t st);
 cudaError_t launch_attn_bwd_tc(const Dims& D, const BwdArgs& x, const fva_mask* m, const fva_mask* m_t,
                                const float* stats, int32_t* dev_status, cudaStream_t st);
-// 3-D TMA map over a [B*H, N, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
-bool make_bhnd_map(CUtensorMap* map, const void* base, int64_t BH, int64_t N, int64_t d, bool f16);
+// 3-D TMA map over an [n, rows, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
+bool make_rows_map(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t d, bool f16);
 
 // ---------------------------------------------------------------------------------
 // device helpers

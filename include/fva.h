@@ -385,8 +385,9 @@ FVA_API int fva_cache_append(const fva_cache* cache, const fva_seqs* seqs, const
  *   n_recent blocks of the sequence whatever their score.
  * Cumulative masses are summed exactly in 2^-52 fixed point, as in fva_route.
  * kept_dev: int32 [B, Hkv, max_blocks], the kept blocks ascending, -1 behind them; n_kept_dev:
- * int32 [B, Hkv]. scale <= 0 selects 1/sqrt(d) in float64. H a multiple of Hkv, H <= 65535.
- * A NaN in a group's scores leaves no order: the group keeps every block.
+ * int32 [B, Hkv]. scale <= 0 selects 1/sqrt(d) in float64. H a multiple of Hkv, H <= 65535,
+ * H / Hkv <= 128.
+ * A NaN or +infinity in a group's scores leaves no order: the group keeps every block.
  */
 FVA_API size_t fva_cache_route_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H);
 FVA_API int fva_cache_route(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride,
