@@ -120,8 +120,9 @@ constexpr double kMassUnit = 4503599627370496.0;  // 2^52: fixed-point unit of a
 constexpr int kHeadsAtOnce = 8;   // query heads of one pass over the means
 
 struct RouteShared {
-  double red[kRouteWarps];
+  double part[2][kRouteWarps];                  // maxima, then sums, of a head's warps
   double top[kHeadsAtOnce], sum[kHeadsAtOnce];  // this CTA's maximum and sum of each head
+  double all_top[kHeadsAtOnce], inv[kHeadsAtOnce];  // the cluster's maximum, 1 / (sum G)
   double cand_p[kRankMost];
   unsigned long long cand_mass[kRankMost];
   int cand_at[kRankMost];
@@ -133,16 +134,6 @@ struct RouteShared {
   // and its count
   unsigned int bin[4][kDigitBins];
 };
-
-__device__ __forceinline__ double block_reduce(double v, bool take_max, double* sm) {
-  v = take_max ? warp_max_d(v) : warp_sum_d(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double r = sm[0];
-  for (int i = 1; i < kRouteWarps; ++i) r = take_max ? fmax(r, sm[i]) : r + sm[i];
-  return r;
-}
 
 __device__ __forceinline__ unsigned long long fixed_mass(double p) {
   return static_cast<unsigned long long>(__double2ll_rn(p * kMassUnit));
@@ -172,7 +163,7 @@ __device__ __forceinline__ double warp_sum_many(double (&v)[N], int lane) {
 // all on their way before the first is used; lanes over the channels.
 template <typename T, int D, int NG>
 __device__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, int h, int lo, int hi, double scale,
-                             double* scores, int32_t* dev_status) {
+                             double* scores, int64_t stride, int32_t* dev_status) {
   constexpr int V = D / 32, kAtOnce = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double qd[NG][V];
@@ -210,7 +201,7 @@ __device__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, i
       double x = warp_sum_many<NG>(s, lane) * scale;
       // a block without a page is never chosen for its score
       if (__shfl_sync(0xffffffffu, page, k) < 0) x = -INFINITY;
-      if (lane < ng) scores[static_cast<int64_t>(lane) * c.max_blocks + base + k] = x;
+      if (lane < ng) scores[lane * stride + base + k] = x;
     }
   }
 }
@@ -334,19 +325,29 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
     }
     __syncthreads();
     const int n = sm.n_cand;
-    if (tid < n) {
-      const double mine = sm.cand_p[tid];
-      const int at = sm.cand_at[tid];
-      unsigned long long mass = sm.mass_above;
-      int cnt = sm.cnt_above;
-      for (int j = 0; j < n; ++j) {
+    int w = 1;  // lanes of a candidate
+    while (w < 32 && n * w * 2 <= kRouteThreads) w *= 2;
+    const int i = tid / w;
+    const bool on = i < n;
+    const double mine = on ? sm.cand_p[i] : 0.0;
+    const int at = on ? sm.cand_at[i] : 0;
+    unsigned long long mass = 0;
+    int cnt = 0;
+    if (on) {
+      for (int j = tid % w; j < n; j += w) {
         const double o = sm.cand_p[j];
         const bool first = o > mine || (o == mine && sm.cand_at[j] < at);
         mass += first ? sm.cand_mass[j] : 0ull;
         cnt += first;
       }
-      prob[at] = mass < need_mass || cnt < need_cnt ? INFINITY : -1.0;
     }
+    for (int o = w / 2; o > 0; o >>= 1) {
+      mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+    }
+    mass += sm.mass_above;
+    cnt += sm.cnt_above;
+    if (on && tid % w == 0) prob[at] = mass < need_mass || cnt < need_cnt ? INFINITY : -1.0;
     __syncthreads();
     // what is left above the candidates' bin: patterns from the next prefix on
     if (shift == 64) return 0x7fefffffffffffffull;
@@ -379,11 +380,14 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
   return prefix;
 }
 
+// `score_cap`: blocks of a share whose scores (kHeadsAtOnce heads) fit shared memory behind
+// prob, or 0: they go through the workspace.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
                                                               int H, double scale, double p, int k_floor, int n_recent,
-                                                              double* __restrict__ scores, int32_t* __restrict__ kept,
-                                                              int32_t* __restrict__ n_kept, int32_t* dev_status) {
+                                                              int score_cap, double* __restrict__ scores,
+                                                              int32_t* __restrict__ kept, int32_t* __restrict__ n_kept,
+                                                              int32_t* dev_status) {
   extern __shared__ __align__(16) double prob[];  // [max_blocks], used in the cluster's first CTA
   __shared__ RouteShared sm;
   cg::cluster_group cluster = cg::this_cluster();
@@ -392,66 +396,87 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, co
   const int len = seq_len(c, b, dev_status);
   const int nB = (len + kBlock - 1) / kBlock, G = H / c.Hkv;
   const int per = (nB + C - 1) / C, lo = min(rank * per, nB), hi = min(lo + per, nB);
-  double* const gathered = cluster.map_shared_rank(prob, 0);
+  double* const gathered = C > 1 ? cluster.map_shared_rank(prob, 0) : prob;
+  auto sync_all = [&] {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
   if (tid == 0) sm.bad = 0;
 
   for (int g0 = 0; g0 < G; g0 += kHeadsAtOnce) {
     const int ng = min(G - g0, kHeadsAtOnce);
     const T* qg = q + b * q_stride + static_cast<int64_t>(h * G + g0) * D;
-    double* sg = scores + (static_cast<int64_t>(b) * H + h * G + g0) * c.max_blocks;
-    if (ng == 1) block_scores<T, D, 1>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
-    else if (ng == 2) block_scores<T, D, 2>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
-    else if (ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
-    else block_scores<T, D, 8>(c, qg, ng, b, h, lo, hi, scale, sg, dev_status);
+    const int64_t stride = score_cap ? score_cap : c.max_blocks;
+    // score of head g and block i at sg[g * stride + i]
+    double* sg = score_cap ? prob + c.max_blocks - lo : scores + (static_cast<int64_t>(b) * H + h * G + g0) * c.max_blocks;
+    if (ng == 1) block_scores<T, D, 1>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    else if (ng == 2) block_scores<T, D, 2>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    else if (ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    else block_scores<T, D, 8>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
     __syncthreads();
-    for (int g = 0; g < ng; ++g) {
-      const double* s = sg + static_cast<int64_t>(g) * c.max_blocks;
-      double m = -INFINITY;
-      bool nan = false;
-      for (int i = lo + tid; i < hi; i += kRouteThreads) {
+    // maxima and sums, 16 / heads warps a head (their order is fixed: equal inputs, equal bits)
+    const int heads = ng == 1 ? 1 : ng == 2 ? 2 : ng <= 4 ? 4 : 8, wph = kRouteWarps / heads;
+    const int g = warp / wph, first = lo + (warp % wph) * 32 + lane;
+    const double* s = sg + g * stride;
+    double m = -INFINITY;
+    bool nan = false;
+    if (g < ng)
+      for (int i = first; i < hi; i += wph * 32) {
         m = fmax(m, s[i]);
         nan |= isnan(s[i]);
       }
-      if (nan) sm.bad = 1;
-      m = block_reduce(m, true, sm.red);
-      double z = 0.0;
-      for (int i = lo + tid; i < hi; i += kRouteThreads) z += exp(s[i] - m);
-      z = block_reduce(z, false, sm.red);
-      if (tid == 0) {
-        sm.top[g] = m;
-        sm.sum[g] = z;
-      }
+    if (nan) sm.bad = 1;
+    m = warp_max_d(m);
+    if (lane == 0) sm.part[0][warp] = m;
+    __syncthreads();
+    for (int k = 0; k < wph; ++k) m = fmax(m, sm.part[0][g * wph + k]);
+    double z = 0.0;
+    if (g < ng)
+      for (int i = first; i < hi; i += wph * 32) z += exp(s[i] - m);
+    z = warp_sum_d(z);
+    if (lane == 0) {
+      sm.part[1][warp] = z;
+      if (warp % wph == 0 && g < ng) sm.top[g] = m;
     }
-    cluster.sync();
-    double top[kHeadsAtOnce], inv[kHeadsAtOnce];
-#pragma unroll
-    for (int g = 0; g < kHeadsAtOnce; ++g) {
-      top[g] = -INFINITY;
-      double z = 0.0;
-      if (g < ng) {
-        for (int r = 0; r < C; ++r) top[g] = fmax(top[g], cluster.map_shared_rank(sm.top, r)[g]);
+    __syncthreads();
+    if (tid < ng) {
+      double t = 0.0;
+      for (int k = 0; k < wph; ++k) t += sm.part[1][tid * wph + k];
+      sm.sum[tid] = t;
+    }
+    sync_all();
+    if (tid < ng) {  // the cluster's
+      double top = sm.top[tid], sum = sm.sum[tid];
+      if (C > 1) {
+        top = -INFINITY;
+        for (int r = 0; r < C; ++r) top = fmax(top, cluster.map_shared_rank(sm.top, r)[tid]);
+        sum = 0.0;
         for (int r = 0; r < C; ++r) {
-          const double t = cluster.map_shared_rank(sm.top, r)[g];
-          if (t > -INFINITY || nB == 0) z += cluster.map_shared_rank(sm.sum, r)[g] * exp(t - top[g]);
+          const double t = cluster.map_shared_rank(sm.top, r)[tid];
+          if (t > -INFINITY) sum += cluster.map_shared_rank(sm.sum, r)[tid] * exp(t - top);
         }
-        if (!(z > 0.0) || isinf(z)) sm.bad = 1;  // no finite score, or a NaN
       }
-      inv[g] = 1.0 / (z * G);
+      if (!(sum > 0.0) || isinf(sum)) sm.bad = 1;  // no finite score, or a NaN
+      sm.all_top[tid] = top;
+      sm.inv[tid] = 1.0 / (sum * G);
     }
+    __syncthreads();
     // a block's share is a function of its scores alone (the cluster-wide maximum and sum), so
     // blocks of equal scores have equal shares whichever CTA holds them
     for (int i = lo + tid; i < hi; i += kRouteThreads) {
       double x = g0 > 0 ? gathered[i] : 0.0;
 #pragma unroll
-      for (int g = 0; g < kHeadsAtOnce; ++g)
-        if (g < ng) x += exp(sg[static_cast<int64_t>(g) * c.max_blocks + i] - top[g]) * inv[g];
+      for (int k = 0; k < kHeadsAtOnce; ++k)
+        if (k < ng) x += exp(sg[k * stride + i] - sm.all_top[k]) * sm.inv[k];
       gathered[i] = x;
     }
-    cluster.sync();  // the next heads overwrite the maxima; at the end, the shares are complete
+    sync_all();  // the next heads overwrite the maxima; at the end, the shares are complete
   }
-  bool bad = false;
-  for (int r = 0; r < C; ++r) bad |= *cluster.map_shared_rank(&sm.bad, r) != 0;
-  cluster.sync();  // nobody leaves while its shared memory is read
+  bool bad = sm.bad != 0;
+  if (C > 1) {
+    for (int r = 0; r < C; ++r) bad |= *cluster.map_shared_rank(&sm.bad, r) != 0;
+    cluster.sync();  // nobody leaves while its shared memory is read
+  }
   if (rank != 0) return;
 
   const bool all = p >= 1.0 || bad || nB == 0;
@@ -758,11 +783,13 @@ struct RouteCall {
   template <typename T, int D>
   cudaError_t operator()() const {
     const int C = cluster_size(static_cast<int64_t>(s->B) * c->Hkv, s->max_blocks, 64);
+    const int per = (s->max_blocks + C - 1) / C, most = 170 * 1024 / 8;  // float64 beside RouteShared
+    const int cap = s->max_blocks + kHeadsAtOnce * per <= most ? per : 0;
     return launch_cluster(route_kernel<T, D>,
                           dim3(static_cast<unsigned>(C), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
-                          kRouteThreads, C, static_cast<size_t>(s->max_blocks) * sizeof(double), st, cache_view<T>(c, s),
-                          static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, scores, kept, n_kept,
-                          dev_status);
+                          kRouteThreads, C, static_cast<size_t>(s->max_blocks + kHeadsAtOnce * cap) * sizeof(double), st,
+                          cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, cap,
+                          scores, kept, n_kept, dev_status);
   }
 };
 
