@@ -114,15 +114,15 @@ __global__ void __launch_bounds__(kPageThreads) append_kernel(CacheView<T> c, co
 // memory of the cluster's first CTA, which selects.
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRankMost = 512;    // this many blocks are ranked against one another
+constexpr int kRankMost = 256;    // this many blocks are ranked against one another (4 us)
 constexpr int kDigitBits = 11, kDigitBins = 1 << kDigitBits;
 constexpr double kMassUnit = 4503599627370496.0;  // 2^52: fixed-point unit of a block's share
-constexpr int kHeadsAtOnce = 8;   // query heads of one pass over the means
+constexpr int kHeadsMost = 8;     // query heads of one pass over the means at most
 
 struct RouteShared {
   double part[2][kRouteWarps];                  // maxima, then sums, of a head's warps
-  double top[kHeadsAtOnce], sum[kHeadsAtOnce];  // this CTA's maximum and sum of each head
-  double all_top[kHeadsAtOnce], inv[kHeadsAtOnce];  // the cluster's maximum, 1 / (sum G)
+  double top[kHeadsMost], sum[kHeadsMost];          // this CTA's maximum and sum of each head
+  double all_top[kHeadsMost], inv[kHeadsMost];      // the cluster's maximum, 1 / (sum G)
   double cand_p[kRankMost];
   unsigned long long cand_mass[kRankMost];
   int cand_at[kRankMost];
@@ -159,55 +159,67 @@ __device__ __forceinline__ double warp_sum_many(double (&v)[N], int lane) {
   return v[0];
 }
 
-// Scores of `ng` heads for the blocks [lo, hi): a warp takes eight blocks at a time, their means
-// all on their way before the first is used; lanes over the channels.
+// Scores of `ng` heads for the blocks [lo, hi): one warp per block, lanes over the channels, the
+// page ids 32 blocks at a time and the means of the next two blocks on their way. The loop is
+// short on purpose: unrolled, its instructions are fetched once each, and a small call spent
+// most of its time on that (15 us for four blocks).
 template <typename T, int D, int NG>
-__device__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, int h, int lo, int hi, double scale,
-                             double* scores, int64_t stride, int32_t* dev_status) {
-  constexpr int V = D / 32, kAtOnce = 8;
+__device__ __noinline__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, int h, int lo, int hi,
+                                          double scale, double* scores, int64_t stride, int32_t* dev_status) {
+  constexpr int V = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double qd[NG][V];
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
     for (int i = 0; i < V; ++i) qd[g][i] = g < ng ? static_cast<double>(to_f32(q[g * D + lane * V + i])) : 0.0;
-  for (int base = lo + warp * kAtOnce; base < hi; base += kRouteWarps * kAtOnce) {
-    int page = lane < kAtOnce && base + lane < hi ? page_of(c, b, base + lane, dev_status) : -1;
-    float m[kAtOnce][V];
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int pg = __shfl_sync(0xffffffffu, page, k);
-      const float* mean = c.key_mean + (static_cast<int64_t>(pg < 0 ? 0 : pg) * c.Hkv + h) * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(mean);
-        m[k][0] = x.x, m[k][1] = x.y, m[k][2] = x.z, m[k][3] = x.w;
-      } else if constexpr (V == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(mean);
-        m[k][0] = x.x, m[k][1] = x.y;
-      } else {
-        m[k][0] = mean[0];
-      }
+  const int64_t page_stride = static_cast<int64_t>(c.Hkv) * D;
+  const float* means = c.key_mean + static_cast<int64_t>(h) * D + lane * V;
+  auto load = [&](int page, float (&m)[V]) {
+    const float* mean = means + (page < 0 ? 0 : page) * page_stride;
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(mean);
+      m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w;
+    } else if constexpr (V == 2) {
+      const float2 x = *reinterpret_cast<const float2*>(mean);
+      m[0] = x.x, m[1] = x.y;
+    } else {
+      m[0] = mean[0];
     }
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      if (base + k >= hi) break;
+  };
+#pragma unroll 1
+  for (int base = lo + warp; base < hi; base += 32 * kRouteWarps) {
+    const int mine = base + lane * kRouteWarps;
+    const int pages = mine < hi ? page_of(c, b, mine, dev_status) : -1;
+    const int cnt = min(32, (hi - base + kRouteWarps - 1) / kRouteWarps);
+    float m[V], m1[V], m2[V];
+    load(__shfl_sync(0xffffffffu, pages, 0), m);
+    load(__shfl_sync(0xffffffffu, pages, min(1, cnt - 1)), m1);
+#pragma unroll 1
+    for (int k = 0; k < cnt; ++k) {
+      load(__shfl_sync(0xffffffffu, pages, min(k + 2, cnt - 1)), m2);
       double s[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         s[g] = 0.0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[g] = fma(qd[g][i], static_cast<double>(m[k][i]), s[g]);
+        for (int i = 0; i < V; ++i) s[g] = fma(qd[g][i], static_cast<double>(m[i]), s[g]);
       }
       double x = warp_sum_many<NG>(s, lane) * scale;
       // a block without a page is never chosen for its score
-      if (__shfl_sync(0xffffffffu, page, k) < 0) x = -INFINITY;
-      if (lane < ng) scores[lane * stride + base + k] = x;
+      if (__shfl_sync(0xffffffffu, pages, k) < 0) x = -INFINITY;
+      if (lane < ng) scores[lane * stride + base + k * kRouteWarps] = x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        m[i] = m1[i];
+        m1[i] = m2[i];
+      }
     }
   }
 }
 
 // The selection, by the cluster's first CTA. Block i is kept when the blocks before it (larger
-// share, or equal and a lower index) lack the mass or the count the prefix needs. Up to 512
+// share, or equal and a lower index) lack the mass or the count the prefix needs. Up to 256
 // blocks are ranked against one another; of more, the bins of an 11-bit digit of the float64
 // pattern (which orders non-negative values) find the one in which the prefix ends, digit by
 // digit, until its blocks can be ranked. The sums are of integers: any order gives the same.
@@ -353,7 +365,7 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
     if (shift == 64) return 0x7fefffffffffffffull;
     return (((prefix >> shift) + 1) << shift) - 1;
   }
-  // more than 512 blocks of one and the same share: the first ones of them, by index
+  // more than 256 blocks of one and the same share: the first ones of them, by index
   const unsigned long long one = fixed_mass(__longlong_as_double(prefix));
   long long ties = max(need_cnt - sm.cnt_above, 1);
   if (sm.mass_above < need_mass) {
@@ -380,10 +392,12 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
   return prefix;
 }
 
-// `score_cap`: blocks of a share whose scores (kHeadsAtOnce heads) fit shared memory behind
-// prob, or 0: they go through the workspace.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
+// kHeads: query heads of one pass over the means. 8 read them once where a CTA has an SM to
+// itself; with 4 the registers let two CTAs share one.
+// `score_cap`: blocks of a share whose scores (kHeads heads) fit shared memory behind prob, or
+// 0: they go through the workspace.
+template <typename T, int D, int kHeads>
+__global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
                                                               int H, double scale, double p, int k_floor, int n_recent,
                                                               int score_cap, double* __restrict__ scores,
                                                               int32_t* __restrict__ kept, int32_t* __restrict__ n_kept,
@@ -403,16 +417,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, co
   };
   if (tid == 0) sm.bad = 0;
 
-  for (int g0 = 0; g0 < G; g0 += kHeadsAtOnce) {
-    const int ng = min(G - g0, kHeadsAtOnce);
+  for (int g0 = 0; g0 < G; g0 += kHeads) {
+    const int ng = min(G - g0, kHeads);
     const T* qg = q + b * q_stride + static_cast<int64_t>(h * G + g0) * D;
     const int64_t stride = score_cap ? score_cap : c.max_blocks;
     // score of head g and block i at sg[g * stride + i]
     double* sg = score_cap ? prob + c.max_blocks - lo : scores + (static_cast<int64_t>(b) * H + h * G + g0) * c.max_blocks;
     if (ng == 1) block_scores<T, D, 1>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
     else if (ng == 2) block_scores<T, D, 2>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
-    else if (ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
-    else block_scores<T, D, 8>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    else if (kHeads == 4 || ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    else block_scores<T, D, kHeads>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
     __syncthreads();
     // maxima and sums, 16 / heads warps a head (their order is fixed: equal inputs, equal bits)
     const int heads = ng == 1 ? 1 : ng == 2 ? 2 : ng <= 4 ? 4 : 8, wph = kRouteWarps / heads;
@@ -465,9 +479,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(CacheView<T> c, co
     // blocks of equal scores have equal shares whichever CTA holds them
     for (int i = lo + tid; i < hi; i += kRouteThreads) {
       double x = g0 > 0 ? gathered[i] : 0.0;
-#pragma unroll
-      for (int k = 0; k < kHeadsAtOnce; ++k)
-        if (k < ng) x += exp(sg[k * stride + i] - sm.all_top[k]) * sm.inv[k];
+#pragma unroll 1
+      for (int k = 0; k < ng; ++k) x += exp(sg[k * stride + i] - sm.all_top[k]) * sm.inv[k];
       gathered[i] = x;
     }
     sync_all();  // the next heads overwrite the maxima; at the end, the shares are complete
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
                                                                      int hold, int32_t* __restrict__ kept,
                                                                      int32_t* __restrict__ new_len,
                                                                      int32_t* dev_status) {
-  extern __shared__ uint32_t held[];  // [hold]
+  extern __shared__ __align__(16) uint32_t held[];  // [hold]
   __shared__ uint32_t bins[2048];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
@@ -553,8 +566,27 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     const int page = page_of(c, b, t / kBlock, dev_status);
     return page < 0 ? 0u : mass_key(c.mass[(static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock]);
   };
-  if (fits) {
-    for (int t = t0 + tid; t < t1; t += kEvictThreads) held[t - t0] = load_key(t);
+  if (fits) {  // a warp takes whole pages, four on their way at a time
+    const int nb = (t1 - t0 + kBlock - 1) / kBlock, b0 = t0 / kBlock;
+    for (int base = warp; base < nb; base += 32 * kEvictWarps) {
+      const int mine_at = base + lane * kEvictWarps;
+      const int pages = mine_at < nb ? page_of(c, b, b0 + mine_at, dev_status) : -1;
+      const int cnt = min(32, (nb - base + kEvictWarps - 1) / kEvictWarps);
+      for (int k0 = 0; k0 < cnt; k0 += 4) {
+        float2 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int page = __shfl_sync(0xffffffffu, pages, min(k0 + k, cnt - 1));
+          x[k] = page < 0 ? make_float2(NAN, NAN)
+                          : reinterpret_cast<const float2*>(c.mass + (static_cast<int64_t>(page) * c.Hkv + h) * kBlock)[lane];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k0 + k < cnt)
+            *reinterpret_cast<uint2*>(held + (base + (k0 + k) * kEvictWarps) * kBlock + 2 * lane) =
+                make_uint2(mass_key(x[k].x), mass_key(x[k].y));
+      }
+    }
     __syncthreads();
   }
   auto key = [&](int t) -> uint32_t { return fits ? held[t - t0] : load_key(t); };
@@ -569,13 +601,21 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     for (int i = tid; i < 2048; i += kEvictThreads) bins[i] = 0u;
     __syncthreads();
     uint32_t zeros = 0;  // tokens that were never attended to, often many: counted aside
-    for (int t = max(t0, lo) + tid; t < min(t1, hi); t += kEvictThreads) {
-      const uint32_t u = key(t);
-      if (pass > 0 && (u >> up) != (prefix >> up)) continue;
-      if (u == kZeroMass)
-        ++zeros;
-      else
-        atomicAdd(&bins[(u >> shift) & ((1u << width) - 1u)], 1u);
+    for (int t = t0 + 4 * tid; t < t1; t += 4 * kEvictThreads) {
+      uint32_t u[4];
+      if (fits) {
+        const uint4 x = *reinterpret_cast<const uint4*>(held + (t - t0));
+        u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = t + k < t1 ? load_key(t + k) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = t + k >= lo && t + k < min(hi, t1) && (pass == 0 || (u[k] >> up) == (prefix >> up));
+        if (in && u[k] == kZeroMass) ++zeros;
+        if (in && u[k] != kZeroMass) atomicAdd(&bins[(u[k] >> shift) & ((1u << width) - 1u)], 1u);
+      }
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     if (lane == 0 && zeros) atomicAdd(&bins[(kZeroMass >> shift) & ((1u << width) - 1u)], zeros);
@@ -616,11 +656,17 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     equal = in && middle && some && u == prefix;
   };
   int na = 0, ne = 0;
+  unsigned held_a = 0, held_e = 0;  // lane i: the ballots of the piece's i-th 32 tokens
   for (int base = w0; base < w1; base += 32) {
     bool a, e;
     classify(base + lane, a, e);
-    na += __popc(__ballot_sync(0xffffffffu, a));
-    ne += __popc(__ballot_sync(0xffffffffu, e));
+    const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
+    if (lane == (base - w0) / 32) {
+      held_a = am;
+      held_e = em;
+    }
+    na += __popc(am);
+    ne += __popc(em);
   }
   if (lane == 0) {
     warp_a[warp] = na;
@@ -646,13 +692,21 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     above += warp_a[w];
     equal += warp_e[w];
   }
+  const unsigned below = (1u << lane) - 1u;
   for (int base = w0; base < w1; base += 32) {
-    bool a, e;
-    classify(base + lane, a, e);
-    const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
+    unsigned am, em;
+    if (piece <= 1024) {
+      am = __shfl_sync(0xffffffffu, held_a, (base - w0) / 32);
+      em = __shfl_sync(0xffffffffu, held_e, (base - w0) / 32);
+    } else {
+      bool a, e;
+      classify(base + lane, a, e);
+      am = __ballot_sync(0xffffffffu, a);
+      em = __ballot_sync(0xffffffffu, e);
+    }
     const int rank_e = equal + __popc(em & below);
-    if (a || (e && rank_e < need)) out[above + __popc(am & below) + min(rank_e, need)] = base + lane;
+    if (((am >> lane) & 1u) || (((em >> lane) & 1u) && rank_e < need))
+      out[above + __popc(am & below) + min(rank_e, need)] = base + lane;
     above += __popc(am);
     equal += __popc(em);
   }
@@ -715,7 +769,8 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
 // host side
 // ---------------------------------------------------------------------------------
 // CTAs of a unit's cluster: doubled while the units leave SMs idle and every CTA keeps at
-// least `least` items, up to 8 (portable).
+// least `least` items, up to 8 (clusters of 16 found too few places at a time: the eviction's
+// selection over 250 thousand tokens and 8 key heads took 135 us with them, 53 with 8).
 static int cluster_size(int64_t units, int64_t items, int64_t least) {
   int n = 1;
   while (n < 8 && units * n * 2 <= 148 && items / (2 * n) >= least) n *= 2;
@@ -782,12 +837,17 @@ struct RouteCall {
   cudaStream_t st;
   template <typename T, int D>
   cudaError_t operator()() const {
-    const int C = cluster_size(static_cast<int64_t>(s->B) * c->Hkv, s->max_blocks, 64);
-    const int per = (s->max_blocks + C - 1) / C, most = 170 * 1024 / 8;  // float64 beside RouteShared
-    const int cap = s->max_blocks + kHeadsAtOnce * per <= most ? per : 0;
-    return launch_cluster(route_kernel<T, D>,
+    const int64_t units = static_cast<int64_t>(s->B) * c->Hkv;
+    const int C = cluster_size(units, s->max_blocks, 64);
+    return units > 148 ? launch<T, D, 4>(C) : launch<T, D, 8>(C);
+  }
+  template <typename T, int D, int kHeads>
+  cudaError_t launch(int C) const {
+    const int per = (s->max_blocks + C - 1) / C, most = (kHeads == 4 ? 64 : 170) * 1024 / 8;  // beside RouteShared
+    const int cap = s->max_blocks + kHeads * per <= most ? per : 0;
+    return launch_cluster(route_kernel<T, D, kHeads>,
                           dim3(static_cast<unsigned>(C), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
-                          kRouteThreads, C, static_cast<size_t>(s->max_blocks + kHeadsAtOnce * cap) * sizeof(double), st,
+                          kRouteThreads, C, static_cast<size_t>(s->max_blocks + kHeads * cap) * sizeof(double), st,
                           cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, cap,
                           scores, kept, n_kept, dev_status);
   }

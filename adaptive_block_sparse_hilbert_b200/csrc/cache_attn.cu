@@ -13,7 +13,7 @@
 
 namespace fva {
 
-constexpr int kShares = 296;  // CTAs of the split kernels: two per SM
+constexpr int kShares = 296;  // CTAs of the split kernels at most: two per SM
 constexpr int kGroup = 16;    // query heads of a unit at most
 
 template <typename T>
@@ -84,7 +84,7 @@ __device__ Share find_share(const AttnView<T>& a, int share) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const int64_t per = (total + kShares - 1) / kShares;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
   const int64_t at = share * per;
   if (at >= before && at < before + mine) {
     int64_t s = before;
@@ -153,6 +153,58 @@ __device__ __forceinline__ void put_row(const AttnView<T>& a, bool whole, int sh
       part[D + 1] = sum;
     }
   }
+}
+
+// The loading warp of a split kernel: walks its share's lists and the page table 32 entries at
+// a time and has `load(stage, page, head)` request the pages, as the ring's stages come free.
+// `valid` of a stage: its keys that count, 0 for a page that is skipped.
+template <typename T, typename Load>
+__device__ __forceinline__ void feed_pages(const AttnView<T>& a, Walk<T>& w, uint64_t* full, uint64_t* empty, int* valid_of,
+                                           volatile int* abort_flag, uint64_t wait_limit_ns, int stages,
+                                           const Load& load) {
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
+  int stage = 0, phase = 0, issued = 0;
+  bool ok = true;
+  while (ok && w.next(a)) {
+    const int bh = w.u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv, len = seq_len(a.c, b, nullptr);
+    for (int64_t base = w.at; base < w.stop() && ok; base += 32) {
+      const int cnt = static_cast<int>(min(static_cast<int64_t>(32), w.stop() - base));
+      int page = -1, valid = 0;
+      if (lane < cnt) {
+        const int block = unit_block(a, bh, static_cast<int>(base - w.start) + lane, len, a.dev_status);
+        if (block >= 0) page = page_of(a.c, b, block, a.dev_status);
+        if (page >= 0) valid = min(len - block * kBlock, kBlock);
+      }
+      for (int k = 0; k < cnt; ++k) {
+        const int pg = __shfl_sync(0xffffffffu, page, k), va = __shfl_sync(0xffffffffu, valid, k);
+        if (!warp_wait_spin(&empty[stage], phase ^ 1, abort_flag, wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          valid_of[stage] = va;
+          if (pg >= 0) load(stage, pg, h);
+          else mbar_arrive(&full[stage]);
+        }
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    w.at = w.stop();
+  }
+  if (!ok) {
+    report(a.dev_status, FVA_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  __syncwarp();
+  // wait (bounded) for the loads in flight: a CTA that gives up must not leave them behind
+  volatile int never = 0;
+  for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+    mbar_wait(&full[j % stages], (j / stages) & 1, &never, 100000000ull);
 }
 
 // ---------------------------------------------------------------------------------
@@ -247,66 +299,22 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
   Walk<T> w(sh, share);
   volatile int* abort_flag = &s_abort;
-  bool ok = true;
-  int stage = 0, phase = 0;
-
   if (warp == 4) {
-    // ------------------------------------------------------------------ loads
-    const bool leader = elect_one();
-    int issued = 0;
-    while (ok && w.next(a)) {
-      const int bh = w.u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv, len = seq_len(a.c, b, nullptr);
-      for (int64_t base = w.at; base < w.stop() && ok; base += 32) {
-        const int cnt = static_cast<int>(min(static_cast<int64_t>(32), w.stop() - base));
-        int page = -1, valid = 0;
-        if (lane < cnt) {
-          const int block = unit_block(a, bh, static_cast<int>(base - w.start) + lane, len, a.dev_status);
-          if (block >= 0) page = page_of(a.c, b, block, a.dev_status);
-          if (page >= 0) valid = min(len - block * kBlock, kBlock);
-        }
-        for (int k = 0; k < cnt; ++k) {
-          const int pg = __shfl_sync(0xffffffffu, page, k), va = __shfl_sync(0xffffffffu, valid, k);
-          if (!warp_wait_spin(&empty[stage], phase ^ 1, abort_flag, wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          if (leader) {
-            s_valid[stage] = va;
-            if (pg >= 0) {
-              uint8_t* dst = ring + stage * 2 * Cfg::kTile;
-              mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTile);
+    feed_pages(a, w, full, empty, s_valid, abort_flag, wait_limit_ns, Cfg::kStages, [&](int stage, int page, int h) {
+      uint8_t* dst = ring + stage * 2 * Cfg::kTile;
+      mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTile);
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                tma_load_3d(dst + c * (kBlock * 128), &tmk, &full[stage], c * 64, h * kBlock, pg);
-                tma_load_3d(dst + Cfg::kTile + c * (kBlock * 128), &tmv, &full[stage], c * 64, h * kBlock, pg);
-              }
-            } else {
-              mbar_arrive(&full[stage]);
-            }
-          }
-          ++issued;
-          if (++stage == Cfg::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+      for (int c = 0; c < D / 64; ++c) {
+        tma_load_3d(dst + c * (kBlock * 128), &tmk, &full[stage], c * 64, h * kBlock, page);
+        tma_load_3d(dst + Cfg::kTile + c * (kBlock * 128), &tmv, &full[stage], c * 64, h * kBlock, page);
       }
-      w.at = w.stop();
-    }
-    if (!ok) {
-      report(a.dev_status, FVA_DEVERR_TIMEOUT);
-      *abort_flag = 1;
-    }
-    // a CTA that gives up waits (bounded) for its loads in flight
-    if (*abort_flag) {
-      volatile int never = 0;
-      for (int j = issued > Cfg::kStages ? issued - Cfg::kStages : 0; j < issued; ++j)
-        mbar_wait(&full[j % Cfg::kStages], (j / Cfg::kStages) & 1, &never, 100000000ull);
-    }
+    });
     return;
   }
 
   // -------------------------------------------------------------------- products and softmax
+  bool ok = true;
+  int stage = 0, phase = 0;
   const int rg = lane >> 2, ct = lane & 3;  // fragment rows rg, rg + 8; columns 2 ct, 2 ct + 1
   const int lm = lane >> 3, lr = lane & 7;  // ldmatrix: matrix and row of this lane's address
   while (ok && w.next(a)) {
@@ -485,24 +493,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 // ---------------------------------------------------------------------------------
 // fp32 caches
 // ---------------------------------------------------------------------------------
-// CUDA cores, one CTA per share: each of four warps takes 16 keys of every block, lanes hold
-// D / 32 channels each, with softmax statistics and an O of their own.
-template <int N>
-__device__ __forceinline__ float warp_sum_many(float (&v)[N], int lane) {
-#pragma unroll
-  for (int n = N / 2; n > 0; n >>= 1) {
-    const bool up = lane & n;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = up ? v[i] : v[i + n];
-      const float keep = up ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
-    }
-  }
-#pragma unroll
-  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-  return v[0];
-}
+// CUDA cores, the same division of work: four warps with 16 keys each of every block, a fifth
+// that keeps bulk loads of whole pages in flight. Scores: two lanes a key, half of the channels
+// each, in an order rotated by the key so that the lanes' 16-byte reads of a page's rows fall
+// into different banks; the query sits in shared memory. Values: lanes hold D / 32 channels.
+template <int D>
+struct SplitF32Cfg {
+  static constexpr int kTile = kBlock * D * 4;
+  static constexpr int kStages = D == 32 ? 6 : 3;
+  static constexpr int kSmem = 128 + kStages * 2 * kTile;
+  static constexpr int kUseShares = D == 128 ? kShares / 2 : kShares;  // CTAs that are resident at once
+};
 
 template <int V>
 __device__ __forceinline__ void load_vec(const float* p, float (&x)[V]) {
@@ -518,98 +519,139 @@ __device__ __forceinline__ void load_vec(const float* p, float (&x)[V]) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(128) split_f32_kernel(AttnView<float> a) {
-  constexpr int V = D / 32;
-  __shared__ float s_p[4][G][16];
-  __shared__ float s_o[4][G][D];
+__global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float> a, uint64_t wait_limit_ns) {
+  using Cfg = SplitF32Cfg<D>;
+  constexpr int V = D / 32, kHalf = D / 8;  // kHalf: 16-byte pieces of half a row
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) float s_q[G][D];
+  __shared__ __align__(16) float s_p[4][G][16];
+  __shared__ float s_o[G][D];
   __shared__ float s_m[4][G], s_l[4][G];
-  const int share = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Share sh = find_share(a, share);
+  __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
+  __shared__ int s_valid[Cfg::kStages], s_abort;
+  uint8_t* ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  const int share = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
   Walk<float> w(sh, share);
-  while (w.next(a)) {
+  volatile int* abort_flag = &s_abort;
+  if (warp == 4) {
+    feed_pages(a, w, full, empty, s_valid, abort_flag, wait_limit_ns, Cfg::kStages, [&](int stage, int page, int h) {
+      const int64_t at = (static_cast<int64_t>(page) * a.c.Hkv + h) * kBlock * D;
+      mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTile);
+      bulk_load(ring + stage * 2 * Cfg::kTile, a.c.k + at, Cfg::kTile, &full[stage]);
+      bulk_load(ring + stage * 2 * Cfg::kTile + Cfg::kTile, a.c.v + at, Cfg::kTile, &full[stage]);
+    });
+    return;
+  }
+
+  bool ok = true;
+  int stage = 0, phase = 0;
+  const int key = lane & 15, part = lane >> 4;
+  auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+  while (ok && w.next(a)) {
     const int bh = w.u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
     const int g0 = (w.u - bh * a.GS) * kGroup, ng = min(a.G - g0, kGroup);
     const int64_t row0 = static_cast<int64_t>(b) * a.H + h * a.G + g0;
-    const int len = seq_len(a.c, b, nullptr);
-    float q[G][V], acc[G][V], m[G], l[G];
+    for (int i = tid; i < G * D; i += 128)
+      s_q[i / D][i % D] = i / D < ng ? a.q[b * a.q_stride + static_cast<int64_t>(h * a.G + g0) * D + i] * a.scale_log2 : 0.0f;
+    sync4();
+    float acc[G][V], m[G], l[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      if (g < ng) load_vec<V>(a.q + b * a.q_stride + static_cast<int64_t>(h * a.G + g0 + g) * D + lane * V, q[g]);
       m[g] = -INFINITY;
       l[g] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        acc[g][i] = 0.0f;
-        q[g][i] = g < ng ? q[g][i] * a.scale_log2 : 0.0f;
-      }
+      for (int i = 0; i < V; ++i) acc[g][i] = 0.0f;
     }
     const int64_t stop = w.stop();
-    for (int64_t at = w.at; at < stop; ++at) {
-      const int pos = static_cast<int>(at - w.start);
-      const int block = unit_block(a, bh, pos, len, a.dev_status);
-      const int page = block < 0 ? -1 : page_of(a.c, b, block, a.dev_status);
-      const int valid = page < 0 ? 0 : min(len - block * kBlock, kBlock);
-      const int r0 = warp * 16, nk = max(0, min(valid - r0, 16));
-      const int64_t base = (static_cast<int64_t>(page < 0 ? 0 : page) * a.c.Hkv + h) * kBlock + r0;
-      __syncwarp();
+    const int first_pos = static_cast<int>(w.at - w.start), n_pos = static_cast<int>(stop - w.at);
+    for (int j = 0; j < n_pos; ++j) {
+      if (!warp_wait_spin(&full[stage], phase, abort_flag, wait_limit_ns)) {
+        ok = false;
+        break;
+      }
+      const int nk = min(s_valid[stage] - warp * 16, 16);  // this warp's keys that count
+      const float* tk = reinterpret_cast<const float*>(ring + stage * 2 * Cfg::kTile) + warp * 16 * D;
+      const float* tv = tk + kBlock * D;
+      float s[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) s[g] = 0.0f;
+      if (nk > 0) {
 #pragma unroll 4
-      for (int r = 0; r < 16; ++r) {
-        float v[G];
-        if (r < nk) {
-          float k[V];
-          load_vec<V>(a.c.k + (base + r) * D + lane * V, k);
+        for (int c = 0; c < kHalf; ++c) {
+          const int at = 4 * (part * kHalf + ((c + key) & (kHalf - 1)));
+          const float4 k = *reinterpret_cast<const float4*>(tk + key * D + at);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            v[g] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[g] = fmaf(q[g][i], k[i], v[g]);
+            const float4 q = *reinterpret_cast<const float4*>(&s_q[g][at]);
+            s[g] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[g]))));
           }
-          const float s = warp_sum_many<G>(v, lane);
-          if (lane < G) s_p[warp][lane][r] = s;
-        } else if (lane < G) {
-          s_p[warp][lane][r] = -INFINITY;
         }
       }
-      __syncwarp();
-      if (a.ws.scores) {  // kept for the accumulation: -inf behind the last key
-        for (int i = lane; i < ng * 16; i += 32)
-          a.ws.scores[(row0 + i / 16) * a.c.max_blocks * kBlock + static_cast<int64_t>(pos) * kBlock + r0 + i % 16] =
-              s_p[warp][i / 16][i % 16];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+        if (key >= nk) s[g] = -INFINITY;  // also what lies behind the sequence's end, NaN included
+      }
+      if (a.ws.scores && part == 0) {  // kept for the accumulation
+        float* out = a.ws.scores + row0 * a.c.max_blocks * kBlock + static_cast<int64_t>(first_pos + j) * kBlock + warp * 16 + key;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (g < ng) out[static_cast<int64_t>(g) * a.c.max_blocks * kBlock] = s[g];
       }
       if (nk > 0) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float s = s_p[warp][g][lane & 15];
-          float mx = s;
+          float mx = s[g];
 #pragma unroll
           for (int k = 8; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
           const float m_new = fmaxf(m[g], mx);
           const float corr = m_new == -INFINITY ? 1.0f : exp2f(m[g] - m_new);
-          const float p = m_new == -INFINITY ? 0.0f : exp2f(s - m_new);
+          const float p = m_new == -INFINITY ? 0.0f : exp2f(s[g] - m_new);
           m[g] = m_new;
-          l[g] = l[g] * corr + (lane < 16 ? p : 0.0f);
+          l[g] = l[g] * corr + (part == 0 ? p : 0.0f);
 #pragma unroll
           for (int i = 0; i < V; ++i) acc[g][i] *= corr;
-          __syncwarp();
-          if (lane < 16) s_p[warp][g][lane] = p;
+          if (part == 0) s_p[warp][g][key] = p;
         }
         __syncwarp();
-#pragma unroll 4
-        for (int r = 0; r < 16; ++r) {
-          if (r >= nk) break;
-          float v[V];
-          load_vec<V>(a.c.v + (base + r) * D + lane * V, v);
+        const int groups = (nk + 3) / 4;
+        for (int r4 = 0; r4 < groups; ++r4) {
+          float v[4][V];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            load_vec<V>(tv + (4 * r4 + r) * D + lane * V, v[r]);
+            if (4 * r4 + r >= nk) {  // 0 times what lies behind the end may be NaN
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[r][i] = 0.0f;
+            }
+          }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float p = s_p[warp][g][r];
+            const float4 p = *reinterpret_cast<const float4*>(&s_p[warp][g][4 * r4]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[g][i] = fmaf(p, v[i], acc[g][i]);
+            for (int i = 0; i < V; ++i)
+              acc[g][i] = fmaf(p.x, v[0][i], fmaf(p.y, v[1][i], fmaf(p.z, v[2][i], fmaf(p.w, v[3][i], acc[g][i]))));
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    // join the four warps
-    __syncthreads();
+    if (!ok) break;
+    // ---- join the four warps, one after the other, in shared memory
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = l[g];
@@ -619,26 +661,39 @@ __global__ void __launch_bounds__(128) split_f32_kernel(AttnView<float> a) {
         s_m[warp][g] = m[g];
         s_l[warp][g] = sum;
       }
+    }
+    sync4();
+    for (int turn = 0; turn < 4; ++turn) {
+      if (turn == warp) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) s_o[warp][g][lane * V + i] = acc[g][i];
-    }
-    __syncthreads();
-    const bool whole = w.whole();
-    for (int i = threadIdx.x; i < ng * D; i += 128) {
-      const int g = i / D, ch = i % D;
-      float mx = -INFINITY;
-      for (int v = 0; v < 4; ++v) mx = fmaxf(mx, s_m[v][g]);
-      float sum = 0.0f, x = 0.0f;
-      for (int v = 0; v < 4; ++v) {
-        const float f = s_m[v][g] == -INFINITY ? 0.0f : exp2f(s_m[v][g] - mx);
-        sum = fmaf(s_l[v][g], f, sum);
-        x = fmaf(s_o[v][g][ch], f, x);
+        for (int g = 0; g < G; ++g) {
+          const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+          const float f = m[g] == -INFINITY ? 0.0f : exp2f(m[g] - mx);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float* at = &s_o[g][lane * V + i];
+            *at = turn == 0 ? acc[g][i] * f : fmaf(acc[g][i], f, *at);
+          }
+        }
       }
-      put_row<float, D>(a, whole, share, w.slot(), row0 + g, g, ch, x, mx, sum);
+      sync4();
     }
-    if (threadIdx.x == 0) a.ws.start[w.u] = w.start;
-    __syncthreads();
+    const bool whole = w.whole();
+    for (int i = tid; i < ng * D; i += 128) {
+      const int g = i / D, ch = i % D;
+      const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) sum += s_m[v][g] == -INFINITY ? 0.0f : s_l[v][g] * exp2f(s_m[v][g] - mx);
+      put_row<float, D>(a, whole, share, w.slot(), row0 + g, g, ch, s_o[g][ch], mx, sum);
+    }
+    if (tid == 0) a.ws.start[w.u] = w.start;
+    sync4();  // the next unit rewrites what was read here
     w.at = stop;
+  }
+  if (!ok) {
+    report(a.dev_status, FVA_DEVERR_TIMEOUT);
+    *abort_flag = 1;
   }
 }
 
@@ -647,17 +702,18 @@ __global__ void __launch_bounds__(128) split_f32_kernel(AttnView<float> a) {
 // ---------------------------------------------------------------------------------
 // CTA (x, key head, sequence): every CTA forms the heads' log-sum-exp from the shares' maxima
 // and sums; x = 0 also joins their O (a warp per head), and, where weights are accumulated,
-// each adds exp(s - lse), summed over the heads, to the masses of 32 listed blocks.
-constexpr int kJoinThreads = 256, kMassBlocks = 32;
+// each adds exp(s - lse), summed over the heads, to the masses of every gridDim.x-th piece of 16
+// listed blocks.
+constexpr int kJoinThreads = 256, kMassBlocks = 16;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, int accumulate) {
   __shared__ float s_lse[kMaxCacheGroup];
+  __shared__ int s_page[kMassBlocks], s_valid[kMassBlocks];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = b * a.c.Hkv + h;
   const int n = unit_count(a, bh * a.GS, nullptr);
-  const int pos0 = blockIdx.x * kMassBlocks;
-  if (blockIdx.x > 0 && pos0 >= n) return;
+  if (blockIdx.x > 0 && static_cast<int>(blockIdx.x) * kMassBlocks >= n) return;
   const int64_t per = n ? *a.ws.per : 1;
   for (int g = warp; g < a.G; g += kJoinThreads / 32) {
     const int64_t row = static_cast<int64_t>(b) * a.H + h * a.G + g;
@@ -709,20 +765,43 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, int a
     if (lane == 0) s_lse[g] = l2;
   }
   if (!accumulate) return;
-  __syncthreads();
   const int len = seq_len(a.c, b, nullptr);
-  for (int i = tid; i < kMassBlocks * kBlock; i += kJoinThreads) {
-    const int pos = pos0 + i / kBlock, r = i % kBlock;
-    if (pos >= n) break;
-    const int block = a.kept ? a.kept[static_cast<int64_t>(bh) * a.c.max_blocks + pos] : pos;
-    if (block < 0 || static_cast<int64_t>(block) * kBlock + r >= len) continue;
-    const int page = page_of(a.c, b, block, nullptr);
-    if (page < 0) continue;
-    const float* s = a.ws.scores + ((static_cast<int64_t>(b) * a.H + h * a.G) * a.c.max_blocks + pos) * kBlock + r;
-    float w = 0.0f;
-#pragma unroll 4
-    for (int g = 0; g < a.G; ++g) w += exp2f(s[static_cast<int64_t>(g) * a.c.max_blocks * kBlock] - s_lse[g]);
-    atomicAdd(a.c.mass + (static_cast<int64_t>(page) * a.c.Hkv + h) * kBlock + r, w);
+  const int64_t head_stride = static_cast<int64_t>(a.c.max_blocks) * kBlock;
+  for (int pos0 = blockIdx.x * kMassBlocks; pos0 < n; pos0 += gridDim.x * kMassBlocks) {
+    __syncthreads();  // (the first pass: s_lse is complete)
+    if (tid < kMassBlocks) {
+      const int pos = pos0 + tid;
+      int page = -1, valid = 0;
+      if (pos < n) {
+        const int block = unit_block(a, bh, pos, len, nullptr);
+        if (block >= 0) page = page_of(a.c, b, block, nullptr);
+        if (page >= 0) valid = min(len - block * kBlock, kBlock);
+      }
+      s_page[tid] = page;
+      s_valid[tid] = valid;
+    }
+    __syncthreads();
+    const float* s = a.ws.scores + (static_cast<int64_t>(b) * a.H + h * a.G) * head_stride + static_cast<int64_t>(pos0) * kBlock;
+    constexpr int kPer = kMassBlocks * kBlock / kJoinThreads;
+    float w[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = 0.0f;
+    for (int g = 0; g < a.G; ++g) {
+      float x[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int k = tid + i * kJoinThreads;
+        x[i] = k % kBlock < s_valid[k / kBlock] ? s[g * head_stride + k] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) w[i] += exp2f(x[i] - s_lse[g]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = tid + i * kJoinThreads, j = k / kBlock;
+      if (k % kBlock < s_valid[j])
+        atomicAdd(a.c.mass + (static_cast<int64_t>(s_page[j]) * a.c.Hkv + h) * kBlock + k % kBlock, w[i]);
+    }
   }
 }
 
@@ -736,6 +815,15 @@ static bool make_page_map(CUtensorMap* map, const void* base, const fva_cache* c
   return make_rows_map(map, base, c->n_pages, static_cast<int64_t>(c->Hkv) * kBlock, c->d, c->dtype == FVA_F16);
 }
 
+template <int D, int G>
+static cudaError_t launch_f32(const AttnView<float>& a, cudaStream_t st) {
+  using Cfg = SplitF32Cfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(split_f32_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  split_f32_kernel<D, G><<<Cfg::kUseShares, kSplitThreads, Cfg::kSmem, st>>>(a, attn_wait_limit_ns());
+  return cudaGetLastError();
+}
+
 template <typename T, int D>
 static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
@@ -747,10 +835,11 @@ static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaSt
     split_kernel<T, D><<<kShares, kSplitThreads, SplitCfg<D>::kSmem, st>>>(mk, mv, a, attn_wait_limit_ns());
   } else {
     const int g = a.G < kGroup ? a.G : kGroup;
-    if (g <= 1) split_f32_kernel<D, 1><<<kShares, 128, 0, st>>>(a);
-    else if (g <= 4) split_f32_kernel<D, 4><<<kShares, 128, 0, st>>>(a);
-    else if (g <= 8) split_f32_kernel<D, 8><<<kShares, 128, 0, st>>>(a);
-    else split_f32_kernel<D, 16><<<kShares, 128, 0, st>>>(a);
+    return g <= 1   ? launch_f32<D, 1>(a, st)
+           : g <= 2 ? launch_f32<D, 2>(a, st)
+           : g <= 4 ? launch_f32<D, 4>(a, st)
+           : g <= 8 ? launch_f32<D, 8>(a, st)
+                    : launch_f32<D, 16>(a, st);
   }
   return cudaGetLastError();
 }
@@ -776,7 +865,13 @@ struct AttnCall {
                            s->B * c->Hkv * GS, scale * 1.4426950408889634f, ws, static_cast<T*>(o), lse, dev_status};
     const cudaError_t e = launch_split<T, D>(c, a, st);
     if (e != cudaSuccess) return e;
-    const unsigned chunks = accumulate ? static_cast<unsigned>((s->max_blocks + kMassBlocks - 1) / kMassBlocks) : 1u;
+    // pieces of the accumulation: about eight CTAs an SM, were every list of full length
+    unsigned chunks = 1;
+    if (accumulate) {
+      const int64_t pieces = (s->max_blocks + kMassBlocks - 1) / kMassBlocks;
+      const int64_t most = (8 * 148 + static_cast<int64_t>(s->B) * c->Hkv - 1) / (static_cast<int64_t>(s->B) * c->Hkv);
+      chunks = static_cast<unsigned>(pieces < most ? pieces : most);
+    }
     join_kernel<T, D><<<dim3(chunks, static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)), kJoinThreads, 0, st>>>(
         a, accumulate);
     return cudaGetLastError();

@@ -384,29 +384,43 @@ def fva_dense_attn(s, q, k, v, o, scale=0.0, dev_status=None, stream=None, v_dty
 
 # ------------------------------------------------------------------------------ training
 
-def _expect(fn, what, t, shape, dtype, device=None, last_dims=None):
-    """Shape, type, device and contiguity of one tensor argument; `last_dims`: only that many
-    trailing dimensions need be contiguous (the first may have a stride of its own)."""
-    if tuple(t.shape) != tuple(shape):
+def _expect(fn, what, t, shape, dtype, device, rows=False):
+    """Shape, type, device and contiguity of one tensor argument; `rows`: the first dimension
+    may have a stride of its own."""
+    if t.shape == shape and t.dtype is dtype and t.device == device:
+        if t.is_contiguous() or (rows and (t.stride()[1:] == (shape[2], 1) or t[0].is_contiguous())):
+            return
+        raise ValueError(f"{fn}: {'a row of ' if rows else ''}{what} is not contiguous")
+    if t.shape != shape:
         raise ValueError(f"{fn}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{fn}: {what} has type {t.dtype}, expected {dtype}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{fn}: {what} is on {t.device}, expected {device or 'a CUDA device'}")
-    if last_dims is None:
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {what} is not contiguous")
-    elif t.numel() and not t[0].is_contiguous():
-        raise ValueError(f"{fn}: a row of {what} is not contiguous")
+    raise ValueError(f"{fn}: {what} is on {t.device}, expected {device}")
 
 
-def _on(device):
-    """The call's launches go to the tensors' device, whichever device is current."""
-    return torch.cuda.device(device)
+# The current stream's handle without building a Stream object: that takes 3 us, a third of
+# what a small call costs on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _stream_on(stream, device):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+def _call(fn, device, stream, *args):
+    """Calls libfva's `fn` with the stream last, on the tensors' device whichever is current;
+    stream None: that device's current one."""
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: the tensors are on {device}, expected a CUDA device")
+    f, st = getattr(_lib, fn), _raw_stream(device.index) if stream is None else _stream(stream)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, st)
+    if rc != FVA_OK:
+        raise FvaError(fn, rc)
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size()
 
 
 def _shape_dtype(s):
@@ -421,10 +435,8 @@ def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=No
         _expect(fn, what, t, four, _shape_dtype(s), dev)
     _expect(fn, "v", v, four, v.dtype if v.dtype in (torch.float16, torch.bfloat16) else _shape_dtype(s), dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    m = mask.c()
-    with _on(dev):
-        _check(fn, _lib.fva_sparse_attn_lse(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dtype_code(v), ctypes.byref(m),
-                                            _ptr(o), _ptr(lse), float(scale), _ptr(dev_status), _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dtype_code(v), ctypes.byref(mask.c()), _ptr(o),
+          _ptr(lse), float(scale), _ptr(dev_status))
 
 
 def fva_sparse_attn_bwd_workspace_bytes(s): return _lib.fva_sparse_attn_bwd_workspace_bytes(ctypes.byref(s))
@@ -439,12 +451,9 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
     for what, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
         _expect(fn, what, t, four, dt, dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    m = mask.c()
-    with _on(dev):
-        _check(fn, _lib.fva_sparse_attn_bwd(
-            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), ctypes.byref(m), _ptr(dq), _ptr(dk),
-            _ptr(dv), float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-            _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
+          ctypes.byref(mask.c()), _ptr(dq), _ptr(dk), _ptr(dv), float(scale), _ptr(workspace), _nbytes(workspace),
+          _ptr(dev_status))
 
 
 # ------------------------------------------------------------------------------ serving
@@ -496,15 +505,14 @@ def fva_cache_append(cache: Cache, table, length, k_new, v_new, new_ptr, max_new
     fn, dev = "fva_cache_append", cache.k.device
     c, q = cache.c(), _seqs(fn, cache, table, length)
     shape = (k_new.shape[0], c.Hkv, c.d)
-    _expect(fn, "k_new", k_new, shape, cache.k.dtype, dev, 2)
-    _expect(fn, "v_new", v_new, shape, cache.k.dtype, dev, 2)
+    _expect(fn, "k_new", k_new, shape, cache.k.dtype, dev, True)
+    _expect(fn, "v_new", v_new, shape, cache.k.dtype, dev, True)
     _expect(fn, "new_ptr", new_ptr, (q.B + 1,), torch.int32, dev)
     if k_new.stride(0) != v_new.stride(0) and shape[0] > 1:
         raise ValueError(f"{fn}: k_new and v_new have different token strides")
     stride = max(k_new.stride(0), c.Hkv * c.d) if shape[0] > 1 else c.Hkv * c.d
-    with _on(dev):
-        _check(fn, _lib.fva_cache_append(ctypes.byref(c), ctypes.byref(q), _ptr(k_new), _ptr(v_new), stride,
-                                         _ptr(new_ptr), int(max_new), _ptr(dev_status), _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), _ptr(k_new), _ptr(v_new), stride, _ptr(new_ptr),
+          int(max_new), _ptr(dev_status))
 
 
 def fva_cache_route_workspace_bytes(cache, B, max_blocks, H):
@@ -513,7 +521,7 @@ def fva_cache_route_workspace_bytes(cache, B, max_blocks, H):
 
 def _query(fn, cache, B, q):
     c = cache.c()
-    _expect(fn, "q", q, (B, q.shape[1], c.d), cache.k.dtype, cache.k.device, 2)
+    _expect(fn, "q", q, (B, q.shape[1], c.d), cache.k.dtype, cache.k.device, True)
     return q.shape[1], q.stride(0) if B > 1 else q.shape[1] * c.d
 
 
@@ -526,11 +534,8 @@ def fva_cache_route(cache: Cache, table, length, q, p, k_floor, n_recent, kept, 
     H, q_stride = _query(fn, cache, sq.B, q)
     _expect(fn, "kept", kept, (sq.B, c.Hkv, sq.max_blocks), torch.int32, dev)
     _expect(fn, "n_kept", n_kept, (sq.B, c.Hkv), torch.int32, dev)
-    with _on(dev):
-        _check(fn, _lib.fva_cache_route(
-            ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, float(p), int(k_floor), int(n_recent), float(scale),
-            _ptr(kept), _ptr(n_kept), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-            _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, float(p), int(k_floor),
+          int(n_recent), float(scale), _ptr(kept), _ptr(n_kept), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
 
 
 def fva_cache_attn_workspace_bytes(cache, B, max_blocks, H, accumulate):
@@ -551,11 +556,8 @@ def fva_cache_attn(cache: Cache, table, length, q, kept, n_kept, o, workspace, l
     _expect(fn, "o", o, (sq.B, H, c.d), cache.k.dtype, dev)
     if lse is not None:
         _expect(fn, "lse", lse, (sq.B, H), torch.float32, dev)
-    with _on(dev):
-        _check(fn, _lib.fva_cache_attn(
-            ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, _ptr(kept), _ptr(n_kept), _ptr(o), _ptr(lse),
-            float(scale), int(bool(accumulate)), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(dev_status), _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, _ptr(kept), _ptr(n_kept), _ptr(o),
+          _ptr(lse), float(scale), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
 
 
 def fva_cache_evict_workspace_bytes(cache, B, max_blocks):
@@ -571,11 +573,8 @@ def fva_cache_evict(cache: Cache, table, length, keep, n_sink, n_recent, dst_tab
     _expect(fn, "dst_table", dst_table, (sq.B, dst_table.shape[1]), torch.int32, dev)
     _expect(fn, "kept", kept, (sq.B, c.Hkv, int(keep)), torch.int32, dev)
     _expect(fn, "new_len", new_len, (sq.B,), torch.int32, dev)
-    with _on(dev):
-        _check(fn, _lib.fva_cache_evict(
-            ctypes.byref(c), ctypes.byref(sq), int(keep), int(n_sink), int(n_recent), _ptr(dst_table), dst_table.shape[1],
-            _ptr(kept), _ptr(new_len), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-            _stream_on(stream, dev)))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), int(keep), int(n_sink), int(n_recent), _ptr(dst_table),
+          dst_table.shape[1], _ptr(kept), _ptr(new_len), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
 
 
 def call_raw(name, *args):

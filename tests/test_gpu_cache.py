@@ -444,7 +444,8 @@ def test_evict_reports_destinations_that_cannot_be():
     torch = s.torch
     kept = torch.empty((2, 1, 128), dtype=torch.int32, device="cuda")
     s.fva.fva_cache_evict(s.cache, s.table, s.length, 128, 0, 0, torch.from_numpy(dst).cuda(), kept,
-                          torch.empty(2, dtype=torch.int32, device="cuda"), s.ws(256), s.st)
+                          torch.empty(2, dtype=torch.int32, device="cuda"),
+                          s.ws(s.fva.fva_cache_evict_workspace_bytes(s.cache, 2, s.max_blocks)), s.st)
     s.ok(s.fva.FVA_DEVERR_BAD_LIST)
     for page in range(before.shape[0]):
         same = bool((s.cache.k[page].view(torch.int16) == before[page].view(torch.int16)).all())
