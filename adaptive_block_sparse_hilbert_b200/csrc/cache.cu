@@ -117,12 +117,14 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRankMost = 256;    // this many blocks are ranked against one another (4 us)
 constexpr int kDigitBits = 11, kDigitBins = 1 << kDigitBits;
 constexpr double kMassUnit = 4503599627370496.0;  // 2^52: fixed-point unit of a block's share
-constexpr int kHeadsMost = 8;     // query heads of one pass over the means at most
+constexpr int kHeads = 8;         // query heads of one pass over the means
+constexpr int kMaxCluster = 8;
 
 struct RouteShared {
   double part[2][kRouteWarps];                  // maxima, then sums, of a head's warps
-  double top[kHeadsMost], sum[kHeadsMost];          // this CTA's maximum and sum of each head
-  double all_top[kHeadsMost], inv[kHeadsMost];      // the cluster's maximum, 1 / (sum G)
+  double top[kHeads], sum[kHeads];              // this CTA's maximum and sum of each head
+  double cta_top[kMaxCluster][kHeads], cta_sum[kMaxCluster][kHeads];  // every CTA's
+  double all_top[kHeads], inv[kHeads];          // the cluster's maximum, 1 / (sum G)
   double cand_p[kRankMost];
   unsigned long long cand_mass[kRankMost];
   int cand_at[kRankMost];
@@ -139,95 +141,62 @@ __device__ __forceinline__ unsigned long long fixed_mass(double p) {
   return static_cast<unsigned long long>(__double2ll_rn(p * kMassUnit));
 }
 
-// Sums v[i] over the warp for N values at once (N a power of two): lane l ends with value
-// l % N. Each halving step keeps half of the values, so N - 1 + log2(32 / N) exchanges do what
-// 5 N would.
-template <int N>
-__device__ __forceinline__ double warp_sum_many(double (&v)[N], int lane) {
-#pragma unroll
-  for (int n = N / 2; n > 0; n >>= 1) {
-    const bool up = lane & n;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const double send = up ? v[i] : v[i + n];
-      const double keep = up ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
-    }
-  }
-#pragma unroll
-  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-  return v[0];
-}
-
-// Scores of `ng` heads for the blocks [lo, hi): one warp per block, lanes over the channels, the
-// page ids 32 blocks at a time and the means of the next two blocks on their way. The loop is
-// short on purpose: unrolled, its instructions are fetched once each, and a small call spent
-// most of its time on that (15 us for four blocks).
-template <typename T, int D, int NG>
-__device__ __noinline__ void block_scores(const CacheView<T>& c, const T* q, int ng, int b, int h, int lo, int hi,
-                                          double scale, double* scores, int64_t stride, int32_t* dev_status) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double qd[NG][V];
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int i = 0; i < V; ++i) qd[g][i] = g < ng ? static_cast<double>(to_f32(q[g * D + lane * V + i])) : 0.0;
-  const int64_t page_stride = static_cast<int64_t>(c.Hkv) * D;
-  const float* means = c.key_mean + static_cast<int64_t>(h) * D + lane * V;
-  auto load = [&](int page, float (&m)[V]) {
-    const float* mean = means + (page < 0 ? 0 : page) * page_stride;
-    if constexpr (V == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(mean);
-      m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w;
-    } else if constexpr (V == 2) {
-      const float2 x = *reinterpret_cast<const float2*>(mean);
-      m[0] = x.x, m[1] = x.y;
-    } else {
-      m[0] = mean[0];
-    }
-  };
+// Scores of up to 8 heads for the blocks [lo, hi): a warp takes eight blocks at a time through
+// the float64 tensor cores (8 heads x 8 blocks x 4 channels an instruction), their means all on
+// their way before the first is used. (Dot products by lanes and shuffles took 42 thousand
+// cycles for a CTA's 488 blocks and 5 heads.) Lane (row, t) of a warp holds channels 16 i + 4 t
+// .. + 3 of its head or block: the four products of 16 channels pair them in that order.
+template <typename T, int D>
+__device__ __forceinline__ void block_scores(const CacheView<T>& c, const double (*s_q)[D + 1], int ng, int b, int h,
+                                             int lo, int hi, double scale, double* scores, int64_t stride,
+                                             int32_t* dev_status) {
+  constexpr int V = D / 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, t = lane & 3;
 #pragma unroll 1
-  for (int base = lo + warp; base < hi; base += 32 * kRouteWarps) {
-    const int mine = base + lane * kRouteWarps;
-    const int pages = mine < hi ? page_of(c, b, mine, dev_status) : -1;
-    const int cnt = min(32, (hi - base + kRouteWarps - 1) / kRouteWarps);
-    float m[V], m1[V], m2[V];
-    load(__shfl_sync(0xffffffffu, pages, 0), m);
-    load(__shfl_sync(0xffffffffu, pages, min(1, cnt - 1)), m1);
-#pragma unroll 1
-    for (int k = 0; k < cnt; ++k) {
-      load(__shfl_sync(0xffffffffu, pages, min(k + 2, cnt - 1)), m2);
-      double s[NG];
+  for (int base = lo + warp * 8; base < hi; base += kRouteWarps * 8) {
+    const int page = base + row < hi ? page_of(c, b, base + row, dev_status) : 0;
+    const float* mean = c.key_mean + (static_cast<int64_t>(page < 0 ? 0 : page) * c.Hkv + h) * D + 4 * t;
+    float4 m[V];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        s[g] = 0.0;
+    for (int i = 0; i < V; ++i) m[i] = *reinterpret_cast<const float4*>(mean + 16 * i);
+    double x[2] = {0.0, 0.0};
+    const double* q = s_q[row] + 4 * t;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[g] = fma(qd[g][i], static_cast<double>(m[i]), s[g]);
-      }
-      double x = warp_sum_many<NG>(s, lane) * scale;
-      // a block without a page is never chosen for its score
-      if (__shfl_sync(0xffffffffu, pages, k) < 0) x = -INFINITY;
-      if (lane < ng) scores[lane * stride + base + k * kRouteWarps] = x;
+    for (int i = 0; i < V; ++i) {
+      dmma_8x8x4(x[0], x[1], q[16 * i], static_cast<double>(m[i].x));
+      dmma_8x8x4(x[0], x[1], q[16 * i + 1], static_cast<double>(m[i].y));
+      dmma_8x8x4(x[0], x[1], q[16 * i + 2], static_cast<double>(m[i].z));
+      dmma_8x8x4(x[0], x[1], q[16 * i + 3], static_cast<double>(m[i].w));
+    }
+    // lane (head, t) holds blocks 2 t and 2 t + 1 of the eight
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        m[i] = m1[i];
-        m1[i] = m2[i];
-      }
+    for (int k = 0; k < 2; ++k) {
+      const bool gone = __shfl_sync(0xffffffffu, page, (2 * t + k) * 4) < 0;  // no page: never chosen for its score
+      if (row < ng && base + 2 * t + k < hi) scores[row * stride + base + 2 * t + k] = gone ? -INFINITY : x[k] * scale;
     }
   }
 }
 
 // The selection, by the cluster's first CTA. Block i is kept when the blocks before it (larger
 // share, or equal and a lower index) lack the mass or the count the prefix needs. Up to 256
-// blocks are ranked against one another; of more, the bins of an 11-bit digit of the float64
-// pattern (which orders non-negative values) find the one in which the prefix ends, digit by
-// digit, until its blocks can be ranked. The sums are of integers: any order gives the same.
-// On return a kept block's share is +infinity or above the returned pattern.
+// blocks are ranked against one another. Of more, a histogram finds the bin in which the prefix
+// ends: its key is the float64 pattern of 1 less that of the share, which orders shares from the
+// largest down, and its first digit key >> 47, 32 bins an octave over 64 octaves, so that as a
+// rule one pass leaves a few blocks to rank. Blocks of a bin that holds too many are told apart
+// by the key's next 11 bits, and so on; shares below 2^-64 (all in the last bin) by the digits
+// from the top. The sums are of integers: any order gives the same.
+// Returns the key below which blocks are kept; a ranked block's share is set to 2 if it is kept,
+// else to -1.
+constexpr unsigned long long kOnePattern = 0x3ff0000000000000ull;
+constexpr int kFirstShift = 47;
+__device__ __forceinline__ unsigned long long share_key(double share) {
+  return kOnePattern - static_cast<unsigned long long>(__double_as_longlong(share));
+}
 __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int nB, double p, int k_floor) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned long long need_mass = static_cast<unsigned long long>(ceil(p * kMassUnit));
   const int need_cnt = min(k_floor, nB);
+  bool ranged = true;  // the first, logarithmic digit
   int shift = 64;
   if (tid == 0) {
     sm.prefix = 0;
@@ -239,15 +208,17 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
   __syncthreads();
   while (sm.in_bin > kRankMost && shift > 0) {
     const int up = shift, width = shift >= kDigitBits ? kDigitBits : shift;
-    shift -= width;
+    shift = ranged ? kFirstShift : shift - width;
     for (int i = tid; i < kDigitBins; i += kRouteThreads) sm.bin[0][i] = sm.bin[1][i] = sm.bin[2][i] = sm.bin[3][i] = 0u;
     __syncthreads();
     const unsigned long long prefix = sm.prefix;
     for (int base = 0; base < nB; base += kRouteThreads) {
       const int i = base + tid;
-      const unsigned long long bits = i < nB ? __double_as_longlong(prob[i]) : 0ull;
-      const bool in = i < nB && (up == 64 || (bits >> up) == (prefix >> up));
-      const int d = in ? static_cast<int>((bits >> shift) & (kDigitBins - 1) & ((1 << width) - 1)) : -1;
+      const unsigned long long key = i < nB ? share_key(prob[i]) : 0ull;
+      const bool in = i < nB && (up == 64 || (key >> up) == (prefix >> up));
+      const int d = !in      ? -1
+                    : ranged ? static_cast<int>(min(key >> kFirstShift, static_cast<unsigned long long>(kDigitBins - 1)))
+                             : static_cast<int>((key >> shift) & ((1 << width) - 1));
       int same;
       __match_all_sync(0xffffffffu, d, &same);
       const unsigned long long m = in ? fixed_mass(prob[i]) : 0ull;
@@ -264,13 +235,13 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
       }
     }
     __syncthreads();
-    // bins from the highest down: four a thread, then a scan over the threads
+    // bins in order: four a thread, then a scan over the threads
     constexpr int kPer = kDigitBins / kRouteThreads;
     unsigned long long m[kPer], tm = 0;
     int n[kPer], tn = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int d = kDigitBins - 1 - (tid * kPer + k);
+      const int d = tid * kPer + k;
       m[k] = sm.bin[0][d] + (static_cast<unsigned long long>(sm.bin[1][d]) << 18) +
              (static_cast<unsigned long long>(sm.bin[2][d]) << 36);
       n[k] = static_cast<int>(sm.bin[3][d]);
@@ -305,7 +276,7 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
     }
     __syncthreads();
     // the bin in which the prefix first has both; where rounding leaves the total below p, the
-    // lowest one that holds a block
+    // last one that holds a block
     const bool short_of = total < need_mass;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -313,22 +284,32 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
       const bool after = mass + m[k] < need_mass || cnt + n[k] < need_cnt;
       const bool here = n[k] > 0 && before && (!after || (short_of && cnt + n[k] == cnt_before + in_bin));
       if (here) {
-        const int d = kDigitBins - 1 - (tid * kPer + k);
-        sm.prefix = prefix | (static_cast<unsigned long long>(d) << shift);
-        sm.mass_above = mass;
-        sm.cnt_above = cnt;
-        sm.in_bin = n[k];
+        const int d = tid * kPer + k;
+        if (ranged && d == kDigitBins - 1) {  // shares below 2^-64: all digits from the top
+          sm.prefix = ~0ull;
+        } else {
+          sm.prefix = prefix | (static_cast<unsigned long long>(d) << shift);
+          sm.mass_above = mass;
+          sm.cnt_above = cnt;
+          sm.in_bin = n[k];
+        }
       }
       mass += m[k];
       cnt += n[k];
     }
     __syncthreads();
+    if (ranged && sm.prefix == ~0ull) {
+      __syncthreads();
+      if (tid == 0) sm.prefix = 0;
+      shift = 64;
+      __syncthreads();
+    }
+    ranged = false;
   }
   const unsigned long long prefix = sm.prefix;
   if (sm.in_bin <= kRankMost) {
     for (int i = tid; i < nB; i += kRouteThreads) {
-      const unsigned long long bits = __double_as_longlong(prob[i]);
-      if (shift == 64 || (bits >> shift) == (prefix >> shift)) {
+      if (shift == 64 || (share_key(prob[i]) >> shift) == (prefix >> shift)) {
         const int at = atomicAdd(&sm.n_cand, 1);
         sm.cand_p[at] = prob[i];
         sm.cand_mass[at] = fixed_mass(prob[i]);
@@ -359,14 +340,12 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
     }
     mass += sm.mass_above;
     cnt += sm.cnt_above;
-    if (on && tid % w == 0) prob[at] = mass < need_mass || cnt < need_cnt ? INFINITY : -1.0;
+    if (on && tid % w == 0) prob[at] = mass < need_mass || cnt < need_cnt ? 2.0 : -1.0;
     __syncthreads();
-    // what is left above the candidates' bin: patterns from the next prefix on
-    if (shift == 64) return 0x7fefffffffffffffull;
-    return (((prefix >> shift) + 1) << shift) - 1;
+    return shift == 64 ? 0ull : prefix;  // the bins before the candidates' own
   }
   // more than 256 blocks of one and the same share: the first ones of them, by index
-  const unsigned long long one = fixed_mass(__longlong_as_double(prefix));
+  const unsigned long long one = fixed_mass(__longlong_as_double(static_cast<long long>(kOnePattern - prefix)));
   long long ties = max(need_cnt - sm.cnt_above, 1);
   if (sm.mass_above < need_mass) {
     const unsigned long long lack = need_mass - sm.mass_above;
@@ -376,7 +355,7 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
   int before = 0;  // equal ones at lower indices
   for (int base = 0; base < nB; base += kRouteThreads) {
     const int i = base + tid;
-    const bool eq = i < nB && static_cast<unsigned long long>(__double_as_longlong(prob[i])) == prefix;
+    const bool eq = i < nB && share_key(prob[i]) == prefix;
     const unsigned mask = __ballot_sync(0xffffffffu, eq);
     __syncthreads();
     if (lane == 0) sm.warp_cnt[warp] = __popc(mask);
@@ -386,24 +365,23 @@ __device__ unsigned long long select_blocks(RouteShared& sm, double* prob, int n
       if (w < warp) at += sm.warp_cnt[w];
       before += sm.warp_cnt[w];
     }
-    if (eq) prob[i] = at < ties ? INFINITY : -1.0;
+    if (eq) prob[i] = at < ties ? 2.0 : -1.0;
   }
   __syncthreads();
   return prefix;
 }
 
-// kHeads: query heads of one pass over the means. 8 read them once where a CTA has an SM to
-// itself; with 4 the registers let two CTAs share one.
 // `score_cap`: blocks of a share whose scores (kHeads heads) fit shared memory behind prob, or
 // 0: they go through the workspace.
-template <typename T, int D, int kHeads>
-__global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
+template <typename T, int D>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_kernel(CacheView<T> c, const T* __restrict__ q, int64_t q_stride,
                                                               int H, double scale, double p, int k_floor, int n_recent,
                                                               int score_cap, double* __restrict__ scores,
                                                               int32_t* __restrict__ kept, int32_t* __restrict__ n_kept,
                                                               int32_t* dev_status) {
   extern __shared__ __align__(16) double prob[];  // [max_blocks], used in the cluster's first CTA
   __shared__ RouteShared sm;
+  __shared__ double s_q[kHeads][D + 1];  // (the odd stride spreads the lanes' reads over the banks)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -423,10 +401,10 @@ __global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kern
     const int64_t stride = score_cap ? score_cap : c.max_blocks;
     // score of head g and block i at sg[g * stride + i]
     double* sg = score_cap ? prob + c.max_blocks - lo : scores + (static_cast<int64_t>(b) * H + h * G + g0) * c.max_blocks;
-    if (ng == 1) block_scores<T, D, 1>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
-    else if (ng == 2) block_scores<T, D, 2>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
-    else if (kHeads == 4 || ng <= 4) block_scores<T, D, 4>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
-    else block_scores<T, D, kHeads>(c, qg, ng, b, h, lo, hi, scale, sg, stride, dev_status);
+    for (int i = tid; i < kHeads * D; i += kRouteThreads)
+      s_q[i / D][i % D] = i / D < ng ? static_cast<double>(to_f32(qg[i])) : 0.0;
+    __syncthreads();
+    block_scores<T, D>(c, s_q, ng, b, h, lo, hi, scale, sg, stride, dev_status);
     __syncthreads();
     // maxima and sums, 16 / heads warps a head (their order is fixed: equal inputs, equal bits)
     const int heads = ng == 1 ? 1 : ng == 2 ? 2 : ng <= 4 ? 4 : 8, wph = kRouteWarps / heads;
@@ -459,19 +437,27 @@ __global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kern
       sm.sum[tid] = t;
     }
     sync_all();
-    if (tid < ng) {  // the cluster's
-      double top = sm.top[tid], sum = sm.sum[tid];
-      if (C > 1) {
-        top = -INFINITY;
-        for (int r = 0; r < C; ++r) top = fmax(top, cluster.map_shared_rank(sm.top, r)[tid]);
-        sum = 0.0;
-        for (int r = 0; r < C; ++r) {
-          const double t = cluster.map_shared_rank(sm.top, r)[tid];
-          if (t > -INFINITY) sum += cluster.map_shared_rank(sm.sum, r)[tid] * exp(t - top);
-        }
-      }
+    if (tid < C * kHeads) {  // a thread per CTA of the cluster and head
+      const int r = tid / kHeads, k = tid % kHeads;
+      const bool far = C > 1;
+      sm.cta_top[r][k] = k < ng ? (far ? cluster.map_shared_rank(sm.top, r)[k] : sm.top[k]) : 0.0;
+      sm.cta_sum[r][k] = k < ng ? (far ? cluster.map_shared_rank(sm.sum, r)[k] : sm.sum[k]) : 1.0;
+    }
+    __syncthreads();
+    if (tid < C * kHeads) {
+      const int r = tid / kHeads, k = tid % kHeads;
+      double top = -INFINITY;
+      for (int i = 0; i < C; ++i) top = fmax(top, sm.cta_top[i][k]);
+      const double t = sm.cta_top[r][k];
+      if (r == 0) sm.all_top[k] = top;
+      // a CTA without a finite score (none of its own, or none at all) adds nothing
+      sm.cta_sum[r][k] = t > -INFINITY ? sm.cta_sum[r][k] * exp(t - top) : 0.0;
+    }
+    __syncthreads();
+    if (tid < ng) {
+      double sum = 0.0;
+      for (int i = 0; i < C; ++i) sum += sm.cta_sum[i][tid];
       if (!(sum > 0.0) || isinf(sum)) sm.bad = 1;  // no finite score, or a NaN
-      sm.all_top[tid] = top;
       sm.inv[tid] = 1.0 / (sum * G);
     }
     __syncthreads();
@@ -481,7 +467,7 @@ __global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kern
       double x = g0 > 0 ? gathered[i] : 0.0;
 #pragma unroll 1
       for (int k = 0; k < ng; ++k) x += exp(sg[k * stride + i] - sm.all_top[k]) * sm.inv[k];
-      gathered[i] = x;
+      gathered[i] = fmin(x, 1.0);  // (a share is at most 1 but for its last bit)
     }
     sync_all();  // the next heads overwrite the maxima; at the end, the shares are complete
   }
@@ -493,14 +479,14 @@ __global__ void __launch_bounds__(kRouteThreads, kHeads == 4 ? 2 : 1) route_kern
   if (rank != 0) return;
 
   const bool all = p >= 1.0 || bad || nB == 0;
-  const unsigned long long above = all ? 0ull : select_blocks(sm, prob, nB, p, k_floor);
+  const unsigned long long border = all ? 0ull : select_blocks(sm, prob, nB, p, k_floor);
   // emission in block order, a contiguous piece a warp
   int32_t* out = kept + (static_cast<int64_t>(b) * c.Hkv + h) * c.max_blocks;
   const int piece = ((nB + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32, w0 = warp * piece;
   auto keep = [&](int i) -> bool {
     if (i >= nB) return false;
     const double x = prob[i];
-    return all || i >= nB - n_recent || (x >= 0.0 && static_cast<unsigned long long>(__double_as_longlong(x)) > above);
+    return all || i >= nB - n_recent || x > 1.0 || (x >= 0.0 && share_key(x) < border);
   };
   int n = 0;
   for (int i = w0; i < w0 + piece && i < nB; i += 32) n += __popc(__ballot_sync(0xffffffffu, keep(i + lane)));
@@ -546,7 +532,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
                                                                      int32_t* __restrict__ new_len,
                                                                      int32_t* dev_status) {
   extern __shared__ __align__(16) uint32_t held[];  // [hold]
-  __shared__ uint32_t bins[2048];
+  __shared__ __align__(16) uint32_t bins[2048];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
   cg::cluster_group cluster = cg::this_cluster();
@@ -566,22 +552,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     const int page = page_of(c, b, t / kBlock, dev_status);
     return page < 0 ? 0u : mass_key(c.mass[(static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock]);
   };
-  if (fits) {  // a warp takes whole pages, four on their way at a time
+  if (fits) {  // a warp takes whole pages, eight on their way at a time
     const int nb = (t1 - t0 + kBlock - 1) / kBlock, b0 = t0 / kBlock;
     for (int base = warp; base < nb; base += 32 * kEvictWarps) {
       const int mine_at = base + lane * kEvictWarps;
       const int pages = mine_at < nb ? page_of(c, b, b0 + mine_at, dev_status) : -1;
       const int cnt = min(32, (nb - base + kEvictWarps - 1) / kEvictWarps);
-      for (int k0 = 0; k0 < cnt; k0 += 4) {
-        float2 x[4];
+      for (int k0 = 0; k0 < cnt; k0 += 8) {
+        float2 x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int page = __shfl_sync(0xffffffffu, pages, min(k0 + k, cnt - 1));
           x[k] = page < 0 ? make_float2(NAN, NAN)
                           : reinterpret_cast<const float2*>(c.mass + (static_cast<int64_t>(page) * c.Hkv + h) * kBlock)[lane];
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (k0 + k < cnt)
             *reinterpret_cast<uint2*>(held + (base + (k0 + k) * kEvictWarps) * kBlock + 2 * lane) =
                 make_uint2(mass_key(x[k].x), mass_key(x[k].y));
@@ -601,6 +587,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     for (int i = tid; i < 2048; i += kEvictThreads) bins[i] = 0u;
     __syncthreads();
     uint32_t zeros = 0;  // tokens that were never attended to, often many: counted aside
+    const uint32_t mask = (1u << width) - 1u;
+    const int end = min(hi, t1);
     for (int t = t0 + 4 * tid; t < t1; t += 4 * kEvictThreads) {
       uint32_t u[4];
       if (fits) {
@@ -610,11 +598,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
 #pragma unroll
         for (int k = 0; k < 4; ++k) u[k] = t + k < t1 ? load_key(t + k) : 0u;
       }
+      const bool inner = t >= lo && t + 4 <= end;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool in = t + k >= lo && t + k < min(hi, t1) && (pass == 0 || (u[k] >> up) == (prefix >> up));
-        if (in && u[k] == kZeroMass) ++zeros;
-        if (in && u[k] != kZeroMass) atomicAdd(&bins[(u[k] >> shift) & ((1u << width) - 1u)], 1u);
+        if (!inner && (t + k < lo || t + k >= end)) continue;
+        if (pass > 0 && (u[k] >> up) != (prefix >> up)) continue;
+        if (u[k] == kZeroMass) ++zeros;
+        else atomicAdd(&bins[(u[k] >> shift) & mask], 1u);
       }
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
@@ -623,10 +613,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     // two bins a thread, from the highest down; every CTA finds the same one
     uint32_t n0 = 0, n1 = 0;
     const int d0 = 2047 - 2 * tid;
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* o = cluster.map_shared_rank(bins, r);
-      n0 += o[d0];
-      n1 += o[d0 - 1];
+    for (int r0 = 0; r0 < C; r0 += 8) {
+      uint2 x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        x[r] = r0 + r < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(bins, r0 + r) + d0 - 1) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        n1 += x[r].x;
+        n0 += x[r].y;
+      }
     }
     int inc = static_cast<int>(n0 + n1);
 #pragma unroll
@@ -659,7 +655,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
   unsigned held_a = 0, held_e = 0;  // lane i: the ballots of the piece's i-th 32 tokens
   for (int base = w0; base < w1; base += 32) {
     bool a, e;
-    classify(base + lane, a, e);
+    if (fits && some && base >= lo && base + 32 <= min(hi, w1)) {
+      const uint32_t u = held[base - t0 + lane];
+      a = u > prefix;
+      e = u == prefix;
+    } else {
+      classify(base + lane, a, e);
+    }
     const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
     if (lane == (base - w0) / 32) {
       held_a = am;
@@ -739,8 +741,8 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
       const int page = page_of(c, b, t / kBlock, dev_status);
       if (page >= 0) {
         const int64_t from = (static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock;
-        k[i] = reinterpret_cast<const uint4*>(c.k + from * D)[piece];
-        v[i] = reinterpret_cast<const uint4*>(c.v + from * D)[piece];
+        k[i] = __ldcs(reinterpret_cast<const uint4*>(c.k + from * D) + piece);
+        v[i] = __ldcs(reinterpret_cast<const uint4*>(c.v + from * D) + piece);
         if (piece == 0) mass[i] = c.mass[from];
       }
     }
@@ -757,8 +759,8 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
   for (int i = 0; i < P::kRows; ++i) {
     const int r = lane + i * P::kLanes;
     if (r < n) {
-      reinterpret_cast<uint4*>(c.k + (to + r) * D)[piece] = k[i];
-      reinterpret_cast<uint4*>(c.v + (to + r) * D)[piece] = v[i];
+      __stcs(reinterpret_cast<uint4*>(c.k + (to + r) * D) + piece, k[i]);
+      __stcs(reinterpret_cast<uint4*>(c.v + (to + r) * D) + piece, v[i]);
       if (piece == 0) c.mass[to + r] = mass[i];
     }
   }
@@ -837,15 +839,10 @@ struct RouteCall {
   cudaStream_t st;
   template <typename T, int D>
   cudaError_t operator()() const {
-    const int64_t units = static_cast<int64_t>(s->B) * c->Hkv;
-    const int C = cluster_size(units, s->max_blocks, 64);
-    return units > 148 ? launch<T, D, 4>(C) : launch<T, D, 8>(C);
-  }
-  template <typename T, int D, int kHeads>
-  cudaError_t launch(int C) const {
-    const int per = (s->max_blocks + C - 1) / C, most = (kHeads == 4 ? 64 : 170) * 1024 / 8;  // beside RouteShared
+    const int C = cluster_size(static_cast<int64_t>(s->B) * c->Hkv, s->max_blocks, 64);
+    const int per = (s->max_blocks + C - 1) / C, most = 60 * 1024 / 8;  // two CTAs an SM
     const int cap = s->max_blocks + kHeads * per <= most ? per : 0;
-    return launch_cluster(route_kernel<T, D, kHeads>,
+    return launch_cluster(route_kernel<T, D>,
                           dim3(static_cast<unsigned>(C), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
                           kRouteThreads, C, static_cast<size_t>(s->max_blocks + kHeads * cap) * sizeof(double), st,
                           cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, cap,

@@ -390,6 +390,14 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 
+// One 8 x 8 x 4 float64 tensor-core product: lane (row, t) = (lane / 4, lane % 4) holds A[row][t],
+// B[t][row] and D[row][2 t], D[row][2 t + 1].
+__device__ __forceinline__ void dmma_8x8x4(double& d0, double& d1, double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+               : "+d"(d0), "+d"(d1)
+               : "d"(a), "d"(b));
+}
+
 // Warp reductions with a fixed butterfly order (deterministic).
 __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll

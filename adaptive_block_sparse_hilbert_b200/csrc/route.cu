@@ -28,12 +28,6 @@ constexpr int kDK = 16;       // d-chunk per pipeline stage (every supported d i
 constexpr int kDP = kDK + 4;  // padded row (doubles): a half-warp's fragment loads hit 32 banks
 constexpr int kStages = 3;    // d-chunks in flight, so one barrier per chunk suffices
 
-__device__ __forceinline__ void dmma_8x8x4(double& d0, double& d1, double a, double b) {
-  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
-               : "+d"(d0), "+d"(d1)
-               : "d"(a), "d"(b));
-}
-
 // 16-byte global -> shared copy; with `valid` false the destination is zero-filled and
 // nothing is read
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, bool valid) {
