@@ -6,7 +6,8 @@
 // The gradient runs as two passes over the kept blocks, one that owns query rows (dQ) and
 // walks the rows' lists, one that owns key rows (dK, dV) and walks the transposed lists. Each
 // output row has one owner, so nothing is summed with atomics and equal inputs give equal
-// bits; the price is that Q K^T and dO V^T are computed twice (7 products instead of 5).
+// bits; the price is that Q K^T and dO V^T are computed twice (7 products instead of 5). Both
+// passes are one launch.
 #include <math.h>
 
 #include "fva_internal.cuh"
@@ -14,48 +15,22 @@
 namespace fva {
 
 // ---------------------------------------------------------------------------------
-// Transposed lists: bit a of key row b = bit b of query row a
+// Transposed lists and row statistics
 // ---------------------------------------------------------------------------------
-// One warp per 32 x 32 bit tile: lane i holds query row 32 i0 + i's word, and 32 ballots
-// give the 32 key rows' words.
-__global__ void __launch_bounds__(256) transpose_bits_kernel(const uint32_t* __restrict__ bits, int nB, int nWords,
-                                                             int64_t n_tiles, uint32_t* __restrict__ bits_t) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= n_tiles) return;
-  const int64_t per_head = static_cast<int64_t>(nWords) * nWords;
-  const int64_t bh = w / per_head;
-  const int a0 = static_cast<int>((w - bh * per_head) / nWords), b0 = static_cast<int>((w - bh * per_head) % nWords);
-  const int a = 32 * a0 + lane;
-  const uint32_t word = a < nB ? bits[(bh * nB + a) * nWords + b0] : 0u;
-  uint32_t mine = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t col = __ballot_sync(0xffffffffu, (word >> j) & 1u);
-    if (lane == j) mine = col;
-  }
-  const int b = 32 * b0 + lane;
-  if (b < nB) bits_t[(bh * nB + b) * nWords + a0] = mine;
-}
-
-// One warp per key row: how many query blocks keep it.
-__global__ void __launch_bounds__(256) count_bits_kernel(const uint32_t* __restrict__ bits, int64_t rows, int nWords,
-                                                         int32_t* __restrict__ cnt) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  int n = 0;
-  for (int k = lane; k < nWords; k += 32) n += __popc(bits[r * nWords + k]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if (lane == 0) cnt[r] = n;
-}
-
-// ---------------------------------------------------------------------------------
-// Row statistics: -lse in log2 units and -D, D_i = sum_c dO_ic O_ic
-// ---------------------------------------------------------------------------------
+// One launch: the first CTAs build lists, the others statistics.
+//
+// Lists: a CTA has 64 key blocks of one (b, h) as bit rows in shared memory (bit a of row b:
+// query block a keeps key block b), reads the head's whole CSR, four rows and up to 128 entries
+// of each at a time, and writes the lists of its 32 tiles (pairs of key blocks): ascending, the
+// entry's low bits saying which of the two keep the query block, as in tile_col. Tile t's list
+// starts at t * nB, so no counts have to be summed first.
+//
+// Statistics: -lse in log2 units and -D, D_i = sum_c dO_ic O_ic, 64 rows as one 512-byte piece.
 // d * sizeof(T) / 16 lanes per row, 16 bytes each; a row without keys (lse = -inf) and the rows
 // past N of the last block get -infinity and 0, so that their P is 0.
+constexpr int kPrepThreads = 512;
+constexpr int kListRows = 64;
+
 __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float) {
   const float* x = reinterpret_cast<const float*>(&a);
   const float* y = reinterpret_cast<const float*>(&b);
@@ -73,12 +48,76 @@ __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, __nv_bflo
   return s;
 }
 
+__device__ void build_lists(int chunk, int bh, const int32_t* __restrict__ row_ptr, const int32_t* __restrict__ col_idx,
+                            int nB, int nWords, int nPairs, const BwdLists& out, uint32_t* bits, int32_t* dev_status) {
+  constexpr int kWarps = kPrepThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c0 = chunk * kListRows;
+  for (int i = tid; i < kListRows * nWords; i += kPrepThreads) bits[i] = 0u;
+  __syncthreads();
+  auto set = [&](int a, int c) {
+    if (c < 0 || c >= nB) report(dev_status, FVA_DEVERR_BAD_LIST);
+    else if (c >= c0 && c < c0 + kListRows) atomicOr(&bits[(c - c0) * nWords + (a >> 5)], 1u << (a & 31));
+  };
+  for (int a0 = warp * 4; a0 < nB; a0 += kWarps * 4) {
+    const int64_t r0 = static_cast<int64_t>(bh) * nB;
+    const int p = a0 + lane <= nB && lane < 5 ? row_ptr[r0 + a0 + lane] : 0;
+    int lo[4], hi[4], c[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool in = a0 + r < nB;
+      lo[r] = __shfl_sync(0xffffffffu, p, r);
+      hi[r] = __shfl_sync(0xffffffffu, p, r + 1);
+      if (!in) hi[r] = lo[r] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lo[r] + k * 32 + lane;
+        c[r][k] = i < hi[r] ? col_idx[i] : -1;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (lo[r] + k * 32 + lane < hi[r]) set(a0 + r, c[r][k]);
+      for (int i = lo[r] + 128 + lane; i < hi[r]; i += 32) set(a0 + r, col_idx[i]);
+    }
+  }
+  __syncthreads();
+  const uint32_t below = (1u << lane) - 1u;
+  for (int t = warp; t < kListRows / 2; t += kWarps) {
+    const int pair = chunk * (kListRows / 2) + t;
+    if (pair >= nPairs) break;
+    const int64_t tile = static_cast<int64_t>(bh) * nPairs + pair;
+    int32_t* list = out.col + tile * nB;
+    const uint32_t* wa = bits + 2 * t * nWords;
+    const uint32_t* wb = wa + nWords;  // past the last key block: all 0
+    int n = 0;
+    for (int k = 0; k < nWords; ++k) {
+      const uint32_t a = wa[k], b = wb[k], u = a | b;
+      if ((u >> lane) & 1u)
+        list[n + __popc(u & below)] = ((32 * k + lane) << 2) | static_cast<int>((a >> lane) & 1u) |
+                                      (static_cast<int>((b >> lane) & 1u) << 1);
+      n += __popc(u);
+    }
+    if (lane == 0) out.cost[tile] = n;
+  }
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) row_stats_kernel(const T* __restrict__ o, const T* __restrict__ d_o,
-                                                        const float* __restrict__ lse, int64_t rows, int N, int nB,
-                                                        float* __restrict__ stats) {
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const int32_t* __restrict__ row_ptr,
+                                                               const int32_t* __restrict__ col_idx, int nB, int nWords,
+                                                               int nPairs, int chunks, int list_ctas, BwdLists lists,
+                                                               const T* __restrict__ o, const T* __restrict__ d_o,
+                                                               const float* __restrict__ lse, int64_t rows, int N,
+                                                               float* __restrict__ stats, int32_t* dev_status) {
+  extern __shared__ uint32_t bits[];  // [kListRows][nWords]
+  if (static_cast<int>(blockIdx.x) < list_ctas) {
+    build_lists(blockIdx.x % chunks, blockIdx.x / chunks, row_ptr, col_idx, nB, nWords, nPairs, lists, bits, dev_status);
+    return;
+  }
   constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16;  // 8, 16 or 32
-  const int64_t r = (blockIdx.x * 256ll + threadIdx.x) / kLanes;  // row of the padded [BH, nB * 64]
+  const int64_t r = ((blockIdx.x - list_ctas) * static_cast<int64_t>(kPrepThreads) + threadIdx.x) / kLanes;
   const int l = threadIdx.x % kLanes;
   const int64_t bh = r / (static_cast<int64_t>(nB) * kBlock);
   const int64_t n = r - bh * nB * kBlock;
@@ -98,216 +137,286 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const T* __restrict__ o,
   }
 }
 
+// Order of the transposed tiles: head by head, the longest list first. One CTA per head.
+__global__ void __launch_bounds__(512) order_kernel(const int32_t* __restrict__ cost, int nPairs,
+                                                    int32_t* __restrict__ worklist) {
+  extern __shared__ int32_t sc[];
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * nPairs;
+  for (int i = threadIdx.x; i < nPairs; i += 512) sc[i] = cost[base + i];
+  __syncthreads();
+  for (int t = threadIdx.x; t < nPairs; t += 512) {
+    const int32_t ct = sc[t];
+    int r = 0;
+    for (int i = 0; i < nPairs; ++i) r += (sc[i] > ct) || (sc[i] == ct && i < t);
+    worklist[base + r] = static_cast<int32_t>(base + t);
+  }
+}
+
 // ---------------------------------------------------------------------------------
 // CUDA-core gradient
 // ---------------------------------------------------------------------------------
-// One CTA owns one 64-row block and streams the blocks of its list through shared memory.
+// One CTA owns 32 rows (half a block: small layers then have CTAs for more SMs) and streams the
+// blocks of its list through two shared-memory buffers.
 //   KV = false: owns query rows (a0 = Q, a1 = dO), streams K and V:  out0 = dQ = scale dS K
 //   KV = true:  owns key rows   (a0 = K, a1 = V), streams Q and dO:  out0 = dK = scale dS^T Q,
 //                                                                     out1 = dV = P^T dO
-// Both form X = a0 b0^T and Y = a1 b1^T (scores and dP, transposed when KV), 4 x 4 values a
-// thread, then accumulate out0 += dS b0 (and out1 += P b1) from the 64 x 64 tiles.
-template <int D, bool KV>
-__global__ void __launch_bounds__(256) attn_bwd_f32_kernel(const float* __restrict__ a0, const float* __restrict__ a1,
-                                                           const float* __restrict__ b0, const float* __restrict__ b1,
-                                                           const float* __restrict__ stats,
-                                                           const int32_t* __restrict__ tile_ptr,
-                                                           const int32_t* __restrict__ tile_col,
-                                                           float* __restrict__ out0, float* __restrict__ out1, int N,
-                                                           int nB, int nPairs, float scale, int32_t* dev_status) {
-  constexpr int LD = D + 4, LP = kBlock + 1, NC = D / 16;
-  extern __shared__ __align__(16) float smem_bwd[];
-  float* sA0 = smem_bwd;
-  float* sA1 = sA0 + kBlock * LD;
-  float* sB0 = sA1 + kBlock * LD;
-  float* sB1 = sB0 + kBlock * LD;
-  float* sP = sB1 + kBlock * LD;  // only used when KV
-  float* sDS = sP + kBlock * LP;
-  float* sL = sDS + kBlock * LP;
-  float* sD = sL + kBlock;
-  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
-  const int a = blockIdx.x;
-  const int64_t bh = blockIdx.y;
-  const int64_t base = bh * N;
-  const int64_t tile = bh * nPairs + (a >> 1);
-  const int half = a & 1;
-  const float scale_log2 = scale * 1.4426950408889634f;
+// Both form X = a0 b0^T and Y = a1 b1^T (scores and dP, transposed when KV), 2 x 4 values a
+// thread, then accumulate out0 += dS b0 (and out1 += P b1), 2 rows x D / 16 channels a thread.
+// Bound by fp32 FMAs and the shared-memory reads that feed them, about one 16-byte read for
+// every four.
+struct F32Args {
+  const float *q, *k, *v, *d_o, *stats;
+  float *dq, *dk, *dv;
+};
+constexpr int kF32Rows = 32;
 
-  auto load = [&](float* dst, const float* src, int block) {
-    for (int i = tid; i < kBlock * D; i += 256) {
-      const int r = i / D, c = i % D;
-      const int n = block * kBlock + r;
-      dst[r * LD + c] = n < N ? src[(base + n) * D + c] : 0.0f;
+template <int D>
+struct F32Cfg {
+  static constexpr int kLD = D + 4, kLP = kBlock + 4;  // row strides: 16-byte pieces fall into different banks
+  static constexpr int kA = kF32Rows * kLD, kB = kBlock * kLD, kP = kF32Rows * kLP;
+  static constexpr int kSmem = 4 * (2 * kA + 4 * kB + 2 * kP + 4 * kBlock);
+};
+
+__device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(valid ? 16 : 0)
+               : "memory");
+}
+
+template <int D, bool KV>
+__device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, const int32_t* list, int n_list, int N,
+                                        int nB, float scale, float* smem, int32_t* dev_status) {
+  using Cfg = F32Cfg<D>;
+  constexpr int LD = Cfg::kLD, LP = Cfg::kLP, NC = D / 16;
+  constexpr int kW = NC >= 4 ? 4 : NC, kG = NC / kW;  // channels of a vector, vectors of a thread
+  float* sA0 = smem;
+  float* sA1 = sA0 + Cfg::kA;
+  float* sB = sA1 + Cfg::kA;        // two buffers of b0, b1
+  float* sP = sB + 4 * Cfg::kB;     // only used when KV
+  float* sDS = sP + Cfg::kP;
+  float* sStat = sDS + Cfg::kP;     // two buffers of -lse2, -D (64 each)
+  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
+  const int block = own / (kBlock / kF32Rows), r0 = own * kF32Rows, half = block & 1;
+  const int64_t base = bh * N;
+  const float *a0 = KV ? x.k : x.q, *a1 = KV ? x.v : x.d_o, *b0 = KV ? x.q : x.k, *b1 = KV ? x.d_o : x.v;
+
+  auto load = [&](float* dst, const float* src, int row, int rows) {
+    for (int i = tid; i < rows * (D / 4); i += 256) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4;
+      const bool in = row + r < N;
+      copy16(dst + r * LD + c, src + (base + (in ? row + r : 0)) * D + c, in);
     }
   };
-  auto load_rows = [&](int block) {
-    if (tid < kBlock) {
-      const float* st = stats + (bh * nB + block) * 128 + tid;
-      sL[tid] = st[0];
-      sD[tid] = st[64];
-    }
+  auto load_stats = [&](float* dst, int blk) {
+    if (tid < 32) copy16(dst + 4 * tid, x.stats + (bh * nB + blk) * 128 + 4 * tid, true);
   };
-  load(sA0, a0, a);
-  load(sA1, a1, a);
-  if (!KV) load_rows(a);
-  float acc0[4][NC], acc1[4][NC];
+  auto next_of = [&](int e) {  // the next entry at e or behind it that this half keeps
+    for (; e < n_list; ++e) {
+      const int entry = list[e];
+      if (!((entry >> half) & 1)) continue;
+      if ((entry >> 2) >= 0 && (entry >> 2) < nB) break;
+      if (tid == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
+    }
+    return e;
+  };
+  auto fetch = [&](int e, int buf) {
+    if (e < n_list) {
+      const int blk = list[e] >> 2;
+      load(sB + buf * 2 * Cfg::kB, b0, blk * kBlock, kBlock);
+      load(sB + buf * 2 * Cfg::kB + Cfg::kB, b1, blk * kBlock, kBlock);
+      if (KV) load_stats(sStat + buf * 128, blk);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  load(sA0, a0, r0, kF32Rows);
+  load(sA1, a1, r0, kF32Rows);
+  if (!KV) load_stats(sStat, block);
+  float acc0[2][NC], acc1[2][NC];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc0[i][j] = acc1[i][j] = 0.0f;
+  const float scale_log2 = scale * 1.4426950408889634f;
 
-  const int lo = tile_ptr[tile], hi = tile_ptr[tile + 1];
-  for (int e = lo; e < hi; ++e) {
-    const int entry = tile_col[e];
-    if (!((entry >> half) & 1)) continue;  // uniform over the CTA
-    const int blk = entry >> 2;
-    if (blk < 0 || blk >= nB) {
-      if (tid == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
-      continue;
-    }
+  int e = next_of(0);
+  fetch(e, 0);
+  for (int buf = 0; e < n_list; buf ^= 1) {
+    const int blk = list[e] >> 2;
+    const int following = next_of(e + 1);
+    fetch(following, buf ^ 1);  // (its last readers are behind the barrier that ended the step before)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    load(sB0, b0, blk);
-    load(sB1, b1, blk);
-    if (KV) load_rows(blk);
-    __syncthreads();
-    float x[4][4], y[4][4];
+    const float* sB0 = sB + buf * 2 * Cfg::kB;
+    const float* sB1 = sB0 + Cfg::kB;
+    const float* st = sStat + (KV ? buf * 128 : (block * kBlock == r0 ? 0 : kF32Rows));
+    float u[2][4], w[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = y[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) u[i][j] = w[i][j] = 0.0f;
+#pragma unroll 2
     for (int c = 0; c < D; c += 4) {
-      float4 u0[4], u1[4];
+      float4 p0[2], p1[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u0[i] = *reinterpret_cast<const float4*>(sA0 + (tr + 16 * i) * LD + c);
-        u1[i] = *reinterpret_cast<const float4*>(sA1 + (tr + 16 * i) * LD + c);
+      for (int i = 0; i < 2; ++i) {
+        p0[i] = *reinterpret_cast<const float4*>(sA0 + (tr + 16 * i) * LD + c);
+        p1[i] = *reinterpret_cast<const float4*>(sA1 + (tr + 16 * i) * LD + c);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 w0 = *reinterpret_cast<const float4*>(sB0 + (tc + 16 * j) * LD + c);
         const float4 w1 = *reinterpret_cast<const float4*>(sB1 + (tc + 16 * j) * LD + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i][j] = fmaf(u0[i].x, w0.x, fmaf(u0[i].y, w0.y, fmaf(u0[i].z, w0.z, fmaf(u0[i].w, w0.w, x[i][j]))));
-          y[i][j] = fmaf(u1[i].x, w1.x, fmaf(u1[i].y, w1.y, fmaf(u1[i].z, w1.z, fmaf(u1[i].w, w1.w, y[i][j]))));
+        for (int i = 0; i < 2; ++i) {
+          u[i][j] = fmaf(p0[i].x, w0.x, fmaf(p0[i].y, w0.y, fmaf(p0[i].z, w0.z, fmaf(p0[i].w, w0.w, u[i][j]))));
+          w[i][j] = fmaf(p1[i].x, w1.x, fmaf(p1[i].y, w1.y, fmaf(p1[i].z, w1.z, fmaf(p1[i].w, w1.w, w[i][j]))));
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = tr + 16 * i, s = tc + 16 * j;
-        const int qi = KV ? s : r, key = (KV ? a : blk) * kBlock + (KV ? r : s);
+        const int r = tr + 16 * i, s = tc + 16 * j, q = KV ? s : r, key = KV ? r0 + r : blk * kBlock + s;
         // keys past N hold zero scores, not -inf: their weight is forced to 0
-        const float p = key < N ? exp2f(fmaf(x[i][j], scale_log2, sL[qi])) : 0.0f;
+        const float p = key < N ? exp2f(fmaf(u[i][j], scale_log2, st[q])) : 0.0f;
         if (KV) sP[r * LP + s] = p;
-        sDS[r * LP + s] = p * (y[i][j] + sD[qi]);
+        sDS[r * LP + s] = p * (w[i][j] + st[64 + q]);
       }
     }
     __syncthreads();
-    for (int s = 0; s < kBlock; ++s) {
-      float w0[NC], w1[NC];
+#pragma unroll 2
+    for (int s = 0; s < kBlock; s += 4) {
+      float4 ds[2], p[2];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        w0[j] = sB0[s * LD + tc + 16 * j];
-        if (KV) w1[j] = sB1[s * LD + tc + 16 * j];
+      for (int i = 0; i < 2; ++i) {
+        ds[i] = *reinterpret_cast<const float4*>(sDS + (tr + 16 * i) * LP + s);
+        if (KV) p[i] = *reinterpret_cast<const float4*>(sP + (tr + 16 * i) * LP + s);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ds = sDS[(tr + 16 * i) * LP + s];
-        const float p = KV ? sP[(tr + 16 * i) * LP + s] : 0.0f;
+      for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          acc0[i][j] = fmaf(ds, w0[j], acc0[i][j]);
-          if (KV) acc1[i][j] = fmaf(p, w1[j], acc1[i][j]);
+        for (int g = 0; g < kG; ++g) {
+          float w0[kW], w1[kW];
+          const float* at0 = sB0 + (s + k) * LD + (g * 16 + tc) * kW;
+          const float* at1 = sB1 + (s + k) * LD + (g * 16 + tc) * kW;
+          if constexpr (kW == 4) {
+            *reinterpret_cast<float4*>(w0) = *reinterpret_cast<const float4*>(at0);
+            if (KV) *reinterpret_cast<float4*>(w1) = *reinterpret_cast<const float4*>(at1);
+          } else {
+            *reinterpret_cast<float2*>(w0) = *reinterpret_cast<const float2*>(at0);
+            if (KV) *reinterpret_cast<float2*>(w1) = *reinterpret_cast<const float2*>(at1);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float d = reinterpret_cast<const float*>(&ds[i])[k];
+#pragma unroll
+            for (int j = 0; j < kW; ++j) acc0[i][g * kW + j] = fmaf(d, w0[j], acc0[i][g * kW + j]);
+            if (KV) {
+              const float y = reinterpret_cast<const float*>(&p[i])[k];
+#pragma unroll
+              for (int j = 0; j < kW; ++j) acc1[i][g * kW + j] = fmaf(y, w1[j], acc1[i][g * kW + j]);
+            }
+          }
         }
       }
     }
+    __syncthreads();
+    e = following;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = a * kBlock + tr + 16 * i;
+  for (int i = 0; i < 2; ++i) {
+    const int n = r0 + tr + 16 * i;
     if (n >= N) continue;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      out0[(base + n) * D + tc + 16 * j] = acc0[i][j] * scale;
-      if (KV) out1[(base + n) * D + tc + 16 * j] = acc1[i][j];
+      const int64_t at = (base + n) * D + ((j / kW) * 16 + tc) * kW + j % kW;
+      (KV ? x.dk : x.dq)[at] = acc0[i][j] * scale;
+      if (KV) x.dv[at] = acc1[i][j];
     }
   }
 }
 
-template <int D, bool KV>
-static cudaError_t launch_f32_t(const Dims& Dm, const void* a0, const void* a1, const void* b0, const void* b1,
-                                const float* stats, const fva_mask* m, void* out0, void* out1, float scale,
-                                int32_t* dev_status, cudaStream_t st) {
-  const size_t smem = sizeof(float) * (4 * kBlock * (D + 4) + 2 * kBlock * (kBlock + 1) + 2 * kBlock);
-  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_f32_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(Dm.nB), static_cast<unsigned>(Dm.BH));
-  attn_bwd_f32_kernel<D, KV><<<grid, 256, smem, st>>>(
-      static_cast<const float*>(a0), static_cast<const float*>(a1), static_cast<const float*>(b0),
-      static_cast<const float*>(b1), stats, m->tile_ptr, m->tile_col, static_cast<float*>(out0),
-      static_cast<float*>(out1), static_cast<int>(Dm.N), static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), scale,
-      dev_status);
-  return cudaGetLastError();
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_f32_kernel(F32Args x, const int32_t* __restrict__ tile_ptr,
+                                                           const int32_t* __restrict__ tile_col, BwdLists lists, int N,
+                                                           int nB, int nPairs, int owners, float scale,
+                                                           int32_t* dev_status) {
+  extern __shared__ __align__(16) float smem_bwd[];
+  const bool kv = static_cast<int>(blockIdx.x) < owners;
+  const int own = static_cast<int>(blockIdx.x) - (kv ? 0 : owners);
+  const int64_t bh = blockIdx.y, tile = bh * nPairs + own / (2 * kBlock / kF32Rows);
+  if (kv) {
+    bwd_f32<D, true>(x, bh, own, lists.col + tile * nB, lists.cost[tile], N, nB, scale, smem_bwd, dev_status);
+  } else {
+    const int at = tile_ptr[tile];
+    bwd_f32<D, false>(x, bh, own, tile_col + at, tile_ptr[tile + 1] - at, N, nB, scale, smem_bwd, dev_status);
+  }
 }
 
 template <int D>
-static cudaError_t launch_f32_d(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
-                                int32_t* dev_status, cudaStream_t st) {
-  const cudaError_t e = launch_f32_t<D, true>(Dm, x.k, x.v, x.q, x.d_o, ws.stats, &ws.mask_t, x.dk, x.dv, x.scale,
-                                              dev_status, st);
+static cudaError_t launch_f32(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+                              int32_t* dev_status, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             F32Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_f32_t<D, false>(Dm, x.q, x.d_o, x.k, x.v, ws.stats, m, x.dq, nullptr, x.scale, dev_status, st);
-}
-
-template <typename T, int D>
-static cudaError_t launch_stats(const Dims& Dm, const BwdArgs& x, float* stats, cudaStream_t st) {
-  const int64_t rows = Dm.rows * kBlock, per_cta = 256 * 16 / (D * static_cast<int>(sizeof(T)));
-  row_stats_kernel<T, D><<<static_cast<unsigned>((rows + per_cta - 1) / per_cta), 256, 0, st>>>(
-      static_cast<const T*>(x.o), static_cast<const T*>(x.d_o), x.lse, rows, static_cast<int>(Dm.N),
-      static_cast<int>(Dm.nB), stats);
+  const F32Args a = {static_cast<const float*>(x.q),   static_cast<const float*>(x.k), static_cast<const float*>(x.v),
+                     static_cast<const float*>(x.d_o), ws.stats,                       static_cast<float*>(x.dq),
+                     static_cast<float*>(x.dk),        static_cast<float*>(x.dv)};
+  const int owners = static_cast<int>((Dm.N + kF32Rows - 1) / kF32Rows);
+  attn_bwd_f32_kernel<D><<<dim3(static_cast<unsigned>(2 * owners), static_cast<unsigned>(Dm.BH)), 256, F32Cfg<D>::kSmem, st>>>(
+      a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N), static_cast<int>(Dm.nB),
+      static_cast<int>(Dm.nPairs), owners, x.scale, dev_status);
   return cudaGetLastError();
 }
 
-// The transposed mask's tile lists (tiles of two key blocks over the union of the query
-// blocks that keep them) and work list, longest first within a head.
-static cudaError_t launch_transposed_lists(const Dims& Dm, const fva_mask* m, const BwdScratch& ws,
-                                           int32_t* dev_status, cudaStream_t st) {
-  cudaError_t e = launch_csr_to_bits(Dm, m, ws.bits, dev_status, st);
+template <typename T, int D>
+static cudaError_t launch_prepare(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+                                  int32_t* dev_status, cudaStream_t st) {
+  const int chunks = static_cast<int>((Dm.nB + kListRows - 1) / kListRows);
+  const int64_t list_ctas = chunks * Dm.BH, rows = Dm.rows * kBlock;
+  const int64_t per_cta = kPrepThreads * 16 / (D * static_cast<int>(sizeof(T)));
+  const size_t smem = static_cast<size_t>(kListRows) * Dm.nWords * 4;
+  const cudaError_t e = cudaFuncSetAttribute(prepare_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t n = Dm.BH * Dm.nWords * Dm.nWords;
-  transpose_bits_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(
-      ws.bits, static_cast<int>(Dm.nB), static_cast<int>(Dm.nWords), n, ws.route_t.bits);
-  count_bits_kernel<<<static_cast<unsigned>((Dm.rows + 7) / 8), 256, 0, st>>>(
-      ws.route_t.bits, Dm.rows, static_cast<int>(Dm.nWords), ws.route_t.row_cnt);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_tiles_from_bits(Dm, &ws.mask_t, FVA_ORDER_HEAD_LPT, ws.route_t, ws.route_t.row_cnt, 0, dev_status, st);
+  prepare_kernel<T, D><<<static_cast<unsigned>(list_ctas + (rows + per_cta - 1) / per_cta), kPrepThreads, smem, st>>>(
+      m->row_ptr, m->col_idx, static_cast<int>(Dm.nB), static_cast<int>(Dm.nWords), static_cast<int>(Dm.nPairs), chunks,
+      static_cast<int>(list_ctas), ws.lists, static_cast<const T*>(x.o), static_cast<const T*>(x.d_o), x.lse, rows,
+      static_cast<int>(Dm.N), ws.stats, dev_status);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attn_bwd(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
                             int32_t* dev_status, cudaStream_t st) {
-  cudaError_t e = launch_transposed_lists(Dm, m, ws, dev_status, st);
+  cudaError_t e;
+  if (Dm.esize == 4) {
+    switch (Dm.d) {
+      case 32:
+        e = launch_prepare<float, 32>(Dm, x, m, ws, dev_status, st);
+        return e != cudaSuccess ? e : launch_f32<32>(Dm, x, m, ws, dev_status, st);
+      case 64:
+        e = launch_prepare<float, 64>(Dm, x, m, ws, dev_status, st);
+        return e != cudaSuccess ? e : launch_f32<64>(Dm, x, m, ws, dev_status, st);
+      default:
+        e = launch_prepare<float, 128>(Dm, x, m, ws, dev_status, st);
+        return e != cudaSuccess ? e : launch_f32<128>(Dm, x, m, ws, dev_status, st);
+    }
+  }
+  e = Dm.d == 128 ? launch_prepare<__nv_bfloat16, 128>(Dm, x, m, ws, dev_status, st)
+                  : launch_prepare<__nv_bfloat16, 64>(Dm, x, m, ws, dev_status, st);
   if (e != cudaSuccess) return e;
-  if (Dm.esize == 2) {
-    e = Dm.d == 128 ? launch_stats<__nv_bfloat16, 128>(Dm, x, ws.stats, st)
-                    : launch_stats<__nv_bfloat16, 64>(Dm, x, ws.stats, st);
-    return e != cudaSuccess ? e : launch_attn_bwd_tc(Dm, x, m, &ws.mask_t, ws.stats, dev_status, st);
+  // where every tile is resident at once (one CTA an SM) their order does not matter
+  const bool ordered = 2 * Dm.tiles > 148;
+  if (ordered) {
+    const size_t smem = static_cast<size_t>(Dm.nPairs) * 4;
+    e = cudaFuncSetAttribute(order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    order_kernel<<<static_cast<unsigned>(Dm.BH), 512, smem, st>>>(ws.lists.cost, static_cast<int>(Dm.nPairs), ws.worklist);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
-  switch (Dm.d) {
-    case 32:
-      e = launch_stats<float, 32>(Dm, x, ws.stats, st);
-      return e != cudaSuccess ? e : launch_f32_d<32>(Dm, x, m, ws, dev_status, st);
-    case 64:
-      e = launch_stats<float, 64>(Dm, x, ws.stats, st);
-      return e != cudaSuccess ? e : launch_f32_d<64>(Dm, x, m, ws, dev_status, st);
-    default:
-      e = launch_stats<float, 128>(Dm, x, ws.stats, st);
-      return e != cudaSuccess ? e : launch_f32_d<128>(Dm, x, m, ws, dev_status, st);
-  }
+  return launch_attn_bwd_tc(Dm, x, m, ws, ordered ? ws.worklist : nullptr, dev_status, st);
 }
 
 }  // namespace fva

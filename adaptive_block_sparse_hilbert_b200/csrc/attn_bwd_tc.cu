@@ -1,6 +1,6 @@
 // Gradient of block-sparse attention on sm_100a tensor cores (bf16, d in {64, 128}).
 //
-// Two kernels of one shape. A CTA owns 128 rows (two adjacent blocks) and walks its tile's
+// Two passes of one shape, one launch. A CTA owns 128 rows (two adjacent blocks) and walks its tile's
 // list of 64-row blocks of the other side:
 //   KV = false  owns query rows; streams K, V.   S = Q K^T, dP = dO V^T, dQ += dS K
 //   KV = true   owns key rows; streams Q, dO.    S^T = K Q^T, dP^T = V dO^T,
@@ -25,7 +25,7 @@
 //       dK, dV d = 128: 256 (K, V in smem) + 2 x 64 + 2 x 64    d = 64: 128 + 32 + 32 + 2 x 64 + 3 x 64
 //     (dK, dV at d = 128 with K in TMEM and one S buffer: 5.3 ms where this takes 5.2.)
 //   * The statistics of a 64-row block, -lse2 and -D, are one 512-byte piece (see
-//     row_stats_kernel): the key kernel streams it with Q and dO. Rows without keys and rows
+//     prepare_kernel): the key kernel streams it with Q and dO. Rows without keys and rows
 //     past N have -lse2 = -infinity, so their P is 0.
 //   * Every wait is bounded; on expiry the CTA reports FVA_DEVERR_TIMEOUT, drains its own
 //     loads and products, frees TMEM and exits.
@@ -114,19 +114,33 @@ constexpr size_t bwd_smem_bytes() {
   return 1024 /*alignment slack*/ + BwdCfg<D, KV>::kSmemData + sizeof(BwdBars<D, KV>);
 }
 
-// own0, own1: the owned pair, Q and dO or K and V, tmo0, tmo1 maps of them; tm0,
-// tm1: maps of the streamed pair.
+struct BwdTcArgs {
+  const __nv_bfloat16 *q, *k, *v, *d_o;
+  const float* stats;
+  __nv_bfloat16 *dq, *dk, *dv;
+  const int32_t *tile_ptr, *tile_col, *worklist;  // of the query rows
+  BwdLists lists;                                 // of the key rows
+  const int32_t* worklist_t;                      // or null: their own order
+  int ntiles, N, nB, nPairs;
+  float scale, scale_log2;
+  uint64_t wait_limit_ns;
+  uint32_t diag_flags;
+  int32_t* dev_status;
+};
+
+// tmo0, tmo1: maps of the owned pair; tm0, tm1: maps of the streamed pair.
 template <int D, bool KV>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmo0, const __grid_constant__ CUtensorMap tmo1,
-                       const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
-                       const __nv_bfloat16* __restrict__ own0, const __nv_bfloat16* __restrict__ own1,
-                       const float* __restrict__ stats, __nv_bfloat16* __restrict__ out0,
-                       __nv_bfloat16* __restrict__ out1, const int32_t* __restrict__ tile_ptr,
-                       const int32_t* __restrict__ tile_col, const int32_t* __restrict__ worklist, int ntiles, int N,
-                       int nB, int nPairs, float scale, float scale_log2, uint64_t wait_limit_ns, uint32_t diag_flags,
-                       int32_t* dev_status) {
+__device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& tmo0, const CUtensorMap& tmo1,
+                                         const CUtensorMap& tm0, const CUtensorMap& tm1, int slot) {
   using Cfg = BwdCfg<D, KV>;
+  const __nv_bfloat16 *own0 = KV ? x.k : x.q, *own1 = KV ? x.v : x.d_o;
+  __nv_bfloat16 *out0 = KV ? x.dk : x.dq, *out1 = x.dv;
+  const float* stats = x.stats;
+  const int N = x.N, nB = x.nB, nPairs = x.nPairs;
+  const float scale = x.scale, scale_log2 = x.scale_log2;
+  const uint64_t wait_limit_ns = x.wait_limit_ns;
+  const uint32_t diag_flags = x.diag_flags;
+  int32_t* dev_status = x.dev_status;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* s_own = smem;
@@ -137,16 +151,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   // (through a shuffle: the compiler then knows that the warp takes each role as a whole)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  int tile = worklist[blockIdx.x];
-  const bool tile_ok = tile >= 0 && tile < ntiles;
+  int tile = KV ? (x.worklist_t ? x.worklist_t[slot] : slot) : x.worklist[slot];
+  const bool tile_ok = tile >= 0 && tile < x.ntiles;
   if (!tile_ok) {
     if (threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
     tile = 0;
   }
+  const int32_t* list = KV ? x.lists.col + static_cast<int64_t>(tile) * nB : x.tile_col + x.tile_ptr[tile];
+  const int n_iter = !tile_ok ? 0 : KV ? x.lists.cost[tile] : x.tile_ptr[tile + 1] - x.tile_ptr[tile];
   const int bh = tile / nPairs, t = tile - bh * nPairs;
-  const int list_base = tile_ptr[tile];
-  const int n_iter = tile_ok ? tile_ptr[tile + 1] - list_base : 0;
-
   if (threadIdx.x == 512) {
     tma_prefetch_desc(&tm0);
     tma_prefetch_desc(&tm1);
@@ -209,7 +222,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ------------------------------------------------------------------ TMA producer
     const bool leader = elect_one();
     const bool withhold = diag_flags & FVA_DIAG_WITHHOLD_Q;
-    ListReader entries(tile_col + list_base, n_iter, lane);
+    ListReader entries(list, n_iter, lane);
     if (Cfg::kOwnSmem && !withhold && n_iter > 0 && leader) {
       mbar_arrive_expect_tx(&bar.own_full, Cfg::kOwn);
       for (int c = 0; c < Cfg::kChunks; ++c)
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       nd_row = in ? st[64] : 0.0f;
     }
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
-    ListReader entries(tile_col + list_base, n_iter, lane);
+    ListReader entries(list, n_iter, lane);
     bool ok = true;
     RingPos<Cfg::kSBufs> sb;
     RingPos<Cfg::kDPBufs> db;
@@ -510,37 +523,43 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-template <int D, bool KV>
-static cudaError_t launch_tc_t(const Dims& Dm, const BwdArgs& x, const CUtensorMap& mq, const CUtensorMap& mk,
-                               const CUtensorMap& mv, const CUtensorMap& mdo, const fva_mask* m, const float* stats,
-                               int32_t* dev_status, cudaStream_t st) {
-  const size_t smem = bwd_smem_bytes<D, KV>();
-  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+// Both passes in one launch: CTAs 0 .. tiles - 1 own key rows (the longer work), the others
+// query rows, so the second pass fills the SMs that the first one's tail leaves idle.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
+                       const __grid_constant__ BwdTcArgs x) {
+  const int slot = static_cast<int>(blockIdx.x);
+  if (slot < x.ntiles) bwd_tile<D, true>(x, tmk, tmv, tmq, tmdo, slot);
+  else bwd_tile<D, false>(x, tmq, tmdo, tmk, tmv, slot - x.ntiles);
+}
+
+template <int D>
+static cudaError_t launch_tc_d(const BwdTcArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CUtensorMap& mdo, cudaStream_t st) {
+  constexpr size_t kKv = bwd_smem_bytes<D, true>(), kQ = bwd_smem_bytes<D, false>(), smem = kKv > kQ ? kKv : kQ;
+  const cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  using bf = __nv_bfloat16;
-  attn_bwd_tc_kernel<D, KV><<<static_cast<unsigned>(Dm.tiles), kBwdThreads, smem, st>>>(
-      KV ? mk : mq, KV ? mv : mdo, KV ? mq : mk, KV ? mdo : mv, static_cast<const bf*>(KV ? x.k : x.q),
-      static_cast<const bf*>(KV ? x.v : x.d_o), stats, static_cast<bf*>(KV ? x.dk : x.dq), static_cast<bf*>(KV ? x.dv : nullptr),
-      m->tile_ptr, m->tile_col, m->worklist, static_cast<int>(Dm.tiles), static_cast<int>(Dm.N),
-      static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), x.scale, x.scale * 1.4426950408889634f,
-      attn_wait_limit_ns(), attn_diag_flags(), dev_status);
+  attn_bwd_tc_kernel<D><<<2 * static_cast<unsigned>(a.ntiles), kBwdThreads, smem, st>>>(mq, mk, mv, mdo, a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_attn_bwd_tc(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const fva_mask* m_t,
-                               const float* stats, int32_t* dev_status, cudaStream_t st) {
+cudaError_t launch_attn_bwd_tc(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+                               const int32_t* worklist, int32_t* dev_status, cudaStream_t st) {
   CUtensorMap mq, mk, mv, mdo;
   if (!make_rows_map(&mq, x.q, Dm.BH, Dm.N, Dm.d, false) || !make_rows_map(&mk, x.k, Dm.BH, Dm.N, Dm.d, false) ||
       !make_rows_map(&mv, x.v, Dm.BH, Dm.N, Dm.d, false) || !make_rows_map(&mdo, x.d_o, Dm.BH, Dm.N, Dm.d, false))
     return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (Dm.d == 128) {
-    e = launch_tc_t<128, true>(Dm, x, mq, mk, mv, mdo, m_t, stats, dev_status, st);
-    return e != cudaSuccess ? e : launch_tc_t<128, false>(Dm, x, mq, mk, mv, mdo, m, stats, dev_status, st);
-  }
-  e = launch_tc_t<64, true>(Dm, x, mq, mk, mv, mdo, m_t, stats, dev_status, st);
-  return e != cudaSuccess ? e : launch_tc_t<64, false>(Dm, x, mq, mk, mv, mdo, m, stats, dev_status, st);
+  using bf = __nv_bfloat16;
+  const BwdTcArgs a = {static_cast<const bf*>(x.q), static_cast<const bf*>(x.k), static_cast<const bf*>(x.v),
+                       static_cast<const bf*>(x.d_o), ws.stats, static_cast<bf*>(x.dq), static_cast<bf*>(x.dk),
+                       static_cast<bf*>(x.dv), m->tile_ptr, m->tile_col, m->worklist, ws.lists, worklist,
+                       static_cast<int>(Dm.tiles), static_cast<int>(Dm.N), static_cast<int>(Dm.nB),
+                       static_cast<int>(Dm.nPairs), x.scale, x.scale * 1.4426950408889634f, attn_wait_limit_ns(),
+                       attn_diag_flags(), dev_status};
+  return Dm.d == 128 ? launch_tc_d<128>(a, mq, mk, mv, mdo, st) : launch_tc_d<64>(a, mq, mk, mv, mdo, st);
 }
 
 }  // namespace fva

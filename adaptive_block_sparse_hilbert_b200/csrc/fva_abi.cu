@@ -353,29 +353,20 @@ int fva_sparse_attn_lse(const fva_shape* s, const void* q_dev, const void* k_dev
                      stream);
 }
 
-// Shapes that the gradient takes: the attention's head dims, int32 list offsets, and the
-// ordering kernel's one int32 per tile of a head in shared memory.
+// Shapes that the gradient takes: the attention's head dims, int32 list offsets, and in shared
+// memory one int32 per tile of a head (order) and 64 bit rows of nB bits (transposition).
 static bool bwd_shape_supported(const Dims& D) {
   if (D.d != 64 && D.d != 128 && !(D.esize == 4 && D.d == 32)) return false;
-  return D.BH * D.nB * D.nB <= 0x7fffffffLL && D.nPairs * 4 <= 200 * 1024;
+  return D.BH * D.nB * D.nB <= 0x7fffffffLL && D.nB <= 25600;
 }
 
 static size_t bwd_scratch_layout(const Dims& D, void* ws, BwdScratch* out) {
   Carver c{static_cast<uint8_t*>(ws), 0};
   BwdScratch b{};
   b.stats = c.take<float>(static_cast<size_t>(D.rows) * 2 * kBlock * 4);
-  b.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
-  b.route_t.bits = c.take<uint32_t>(static_cast<size_t>(D.rows * D.nWords) * 4);
-  b.route_t.row_cnt = c.take<int32_t>(static_cast<size_t>(D.rows) * 4);
-  b.route_t.head_load = c.take<int64_t>(static_cast<size_t>(D.BH) * 8);
-  b.mask_t.capacity = D.BH * D.nB * D.nB;
-  b.mask_t.tile_capacity = D.BH * D.nPairs * D.nB;
-  b.mask_t.row_ptr = c.take<int32_t>(static_cast<size_t>(D.rows + 1) * 4);
-  b.mask_t.head_kept = c.take<int64_t>(static_cast<size_t>(D.BH) * 8);
-  b.mask_t.tile_ptr = c.take<int32_t>(static_cast<size_t>(D.tiles + 1) * 4);
-  b.mask_t.tile_cost = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
-  b.mask_t.worklist = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
-  b.mask_t.tile_col = c.take<int32_t>(static_cast<size_t>(b.mask_t.tile_capacity) * 4);
+  b.lists.cost = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
+  b.worklist = c.take<int32_t>(static_cast<size_t>(D.tiles) * 4);
+  b.lists.col = c.take<int32_t>(static_cast<size_t>(D.tiles * D.nB) * 4);
   if (out) *out = b;
   return c.off;
 }

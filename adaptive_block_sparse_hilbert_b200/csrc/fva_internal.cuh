@@ -76,16 +76,20 @@ struct BwdArgs {
   void *dq, *dk, *dv;
   float scale;
 };
+struct BwdLists {
+  int32_t* col;   // [tiles * nB]: tile t's query blocks from t * nB on, entries as in tile_col
+  int32_t* cost;  // [tiles] their number
+};
 struct BwdScratch {
-  float* stats;          // [BH, nB, 2, 64] -lse in log2 units and -rowsum(dO O) of every row
-  uint32_t* bits;        // [rows, nWords] the mask, by query row
-  RouteScratch route_t;  // bits by key row, their counts, head loads
-  fva_mask mask_t;       // the transposed lists (no col_idx)
+  float* stats;       // [BH, nB, 2, 64] -lse in log2 units and -rowsum(dO O) of every row
+  BwdLists lists;     // by tile of two key blocks
+  int32_t* worklist;  // [tiles] the lists' order
 };
 cudaError_t launch_attn_bwd(const Dims& D, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
                             int32_t* dev_status, cudaStream_t st);
-cudaError_t launch_attn_bwd_tc(const Dims& D, const BwdArgs& x, const fva_mask* m, const fva_mask* m_t,
-                               const float* stats, int32_t* dev_status, cudaStream_t st);
+// worklist null: the transposed tiles in their own order.
+cudaError_t launch_attn_bwd_tc(const Dims& D, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
+                               const int32_t* worklist, int32_t* dev_status, cudaStream_t st);
 // 3-D TMA map over an [n, rows, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
 bool make_rows_map(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t d, bool f16);
 

@@ -314,7 +314,7 @@ FVA_API int fva_dense_attn(const fva_shape* s, const void* q_dev, const void* k_
  * (fva_sparse_attn_bwd_workspace_bytes, 16-byte aligned; calls that may overlap need one each,
  * captured graphs that may run at once among them). The gradients must not overlap each other
  * or any input. scale <= 0 selects 1/sqrt(d), and has to be the forward's.
- * Limits: B*H*nB*nB <= 2^31 - 1, nPairs <= 51200.
+ * Limits: B*H*nB*nB <= 2^31 - 1, nB <= 25600.
  */
 FVA_API int fva_sparse_attn_lse(const fva_shape* s, const void* q_dev, const void* k_dev, const void* v_dev,
                                 int v_dtype, const fva_mask* mask, void* o_dev, float* lse_dev, float scale,
