@@ -8,11 +8,14 @@
 // output row has one owner, so nothing is summed with atomics and equal inputs give equal
 // bits; the price is that Q K^T and dO V^T are computed twice (7 products instead of 5). Both
 // passes are one launch.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "fva_internal.cuh"
 
 namespace fva {
+
+namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------------
 // Transposed lists and row statistics
@@ -29,7 +32,7 @@ namespace fva {
 // d * sizeof(T) / 16 lanes per row, 16 bytes each; a row without keys (lse = -inf) and the rows
 // past N of the last block get -infinity and 0, so that their P is 0.
 constexpr int kPrepThreads = 512;
-constexpr int kListRows = 64;
+constexpr int kListRows = 64, kStatRows = 4;
 
 __device__ __forceinline__ float dot16(const uint4& a, const uint4& b, float) {
   const float* x = reinterpret_cast<const float*>(&a);
@@ -62,25 +65,25 @@ __device__ void build_lists(int chunk, int bh, const int32_t* __restrict__ row_p
   for (int a0 = warp * 4; a0 < nB; a0 += kWarps * 4) {
     const int64_t r0 = static_cast<int64_t>(bh) * nB;
     const int p = a0 + lane <= nB && lane < 5 ? row_ptr[r0 + a0 + lane] : 0;
-    int lo[4], hi[4], c[4][4];
+    int lo[4], hi[4], most = 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const bool in = a0 + r < nB;
       lo[r] = __shfl_sync(0xffffffffu, p, r);
       hi[r] = __shfl_sync(0xffffffffu, p, r + 1);
-      if (!in) hi[r] = lo[r] = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = lo[r] + k * 32 + lane;
-        c[r][k] = i < hi[r] ? col_idx[i] : -1;
-      }
+      if (a0 + r >= nB) hi[r] = lo[r] = 0;
+      most = max(most, hi[r] - lo[r]);
     }
+    for (int off = lane; off - lane < most; off += 128) {
+      int c[4][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (lo[r] + k * 32 + lane < hi[r]) set(a0 + r, c[r][k]);
-      for (int i = lo[r] + 128 + lane; i < hi[r]; i += 32) set(a0 + r, col_idx[i]);
+        for (int k = 0; k < 4; ++k) c[r][k] = lo[r] + off + k * 32 < hi[r] ? col_idx[lo[r] + off + k * 32] : -1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (lo[r] + off + k * 32 < hi[r]) set(a0 + r, c[r][k]);
     }
   }
   __syncthreads();
@@ -116,24 +119,34 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const int32_t* __
     build_lists(blockIdx.x % chunks, blockIdx.x / chunks, row_ptr, col_idx, nB, nWords, nPairs, lists, bits, dev_status);
     return;
   }
+  // four rows a thread, their loads all on the way before the first is used
   constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16;  // 8, 16 or 32
-  const int64_t r = ((blockIdx.x - list_ctas) * static_cast<int64_t>(kPrepThreads) + threadIdx.x) / kLanes;
+  constexpr int kRowsAtOnce = kPrepThreads / kLanes;
   const int l = threadIdx.x % kLanes;
-  const int64_t bh = r / (static_cast<int64_t>(nB) * kBlock);
-  const int64_t n = r - bh * nB * kBlock;
-  const bool in = r < rows && n < N;
-  float s = 0.0f;
-  if (in) {
-    const int64_t at = (bh * N + n) * kLanes + l;
-    s = dot16(reinterpret_cast<const uint4*>(o)[at], reinterpret_cast<const uint4*>(d_o)[at], T());
+  const int64_t first = static_cast<int64_t>(blockIdx.x - list_ctas) * (kStatRows * kRowsAtOnce) + threadIdx.x / kLanes;
+  uint4 x[kStatRows], y[kStatRows];
+  int64_t at[kStatRows];  // row of [BH, N]; -1: past N
+#pragma unroll
+  for (int k = 0; k < kStatRows; ++k) {
+    const int64_t r = first + k * kRowsAtOnce, bh = r / (static_cast<int64_t>(nB) * kBlock), n = r - bh * nB * kBlock;
+    at[k] = r < rows && n < N ? bh * N + n : -1;
+    if (at[k] >= 0) {
+      x[k] = reinterpret_cast<const uint4*>(o)[at[k] * kLanes + l];
+      y[k] = reinterpret_cast<const uint4*>(d_o)[at[k] * kLanes + l];
+    }
   }
 #pragma unroll
-  for (int k = kLanes / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  if (l == 0 && r < rows) {
-    const float x = in ? lse[bh * N + n] : -INFINITY;
-    float* out = stats + (r / kBlock) * 128 + r % kBlock;
-    out[0] = x == -INFINITY ? -INFINITY : -1.4426950408889634f * x;
-    out[64] = -s;
+  for (int k = 0; k < kStatRows; ++k) {
+    const int64_t r = first + k * kRowsAtOnce;
+    float s = at[k] >= 0 ? dot16(x[k], y[k], T()) : 0.0f;
+#pragma unroll
+    for (int i = kLanes / 2; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+    if (l == 0 && r < rows) {
+      const float e = at[k] >= 0 ? lse[at[k]] : -INFINITY;
+      float* out = stats + (r / kBlock) * 128 + r % kBlock;
+      out[0] = e == -INFINITY ? -INFINITY : -1.4426950408889634f * e;
+      out[64] = -s;
+    }
   }
 }
 
@@ -155,15 +168,16 @@ __global__ void __launch_bounds__(512) order_kernel(const int32_t* __restrict__ 
 // ---------------------------------------------------------------------------------
 // CUDA-core gradient
 // ---------------------------------------------------------------------------------
-// One CTA owns 32 rows (half a block: small layers then have CTAs for more SMs) and streams the
-// blocks of its list through two shared-memory buffers.
+// A cluster of two CTAs owns 32 rows (half a block) and takes the blocks of its list in turn, so
+// that a small layer has CTAs for every SM and its longest list is halved; the second CTA's sums
+// are added to the first's at the end. Blocks stream through two shared-memory buffers.
 //   KV = false: owns query rows (a0 = Q, a1 = dO), streams K and V:  out0 = dQ = scale dS K
 //   KV = true:  owns key rows   (a0 = K, a1 = V), streams Q and dO:  out0 = dK = scale dS^T Q,
 //                                                                     out1 = dV = P^T dO
-// Both form X = a0 b0^T and Y = a1 b1^T (scores and dP, transposed when KV), 2 x 4 values a
-// thread, then accumulate out0 += dS b0 (and out1 += P b1), 2 rows x D / 16 channels a thread.
-// Bound by fp32 FMAs and the shared-memory reads that feed them, about one 16-byte read for
-// every four.
+// Warps 0-3 form X = a0 b0^T and P, warps 4-7 Y = a1 b1^T and dS (scores and dP, transposed when
+// KV), 4 x 4 values a thread; then the two groups accumulate P b1 and dS b0 (KV) or half of the
+// block's rows of dS b0 each, 4 rows x D / 16 channels a thread. Bound by fp32 FMAs, with one
+// 16-byte shared-memory read (two cycles) for every eight of them.
 struct F32Args {
   const float *q, *k, *v, *d_o, *stats;
   float *dq, *dk, *dv;
@@ -175,6 +189,7 @@ struct F32Cfg {
   static constexpr int kLD = D + 4, kLP = kBlock + 4;  // row strides: 16-byte pieces fall into different banks
   static constexpr int kA = kF32Rows * kLD, kB = kBlock * kLD, kP = kF32Rows * kLP;
   static constexpr int kSmem = 4 * (2 * kA + 4 * kB + 2 * kP + 4 * kBlock);
+  static_assert(2 * kF32Rows * D <= 4 * kB, "the sums of both groups fit the stream's buffers");
 };
 
 __device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid) {
@@ -188,13 +203,15 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   using Cfg = F32Cfg<D>;
   constexpr int LD = Cfg::kLD, LP = Cfg::kLP, NC = D / 16;
   constexpr int kW = NC >= 4 ? 4 : NC, kG = NC / kW;  // channels of a vector, vectors of a thread
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
   float* sA0 = smem;
   float* sA1 = sA0 + Cfg::kA;
   float* sB = sA1 + Cfg::kA;        // two buffers of b0, b1
-  float* sP = sB + 4 * Cfg::kB;     // only used when KV
+  float* sP = sB + 4 * Cfg::kB;
   float* sDS = sP + Cfg::kP;
   float* sStat = sDS + Cfg::kP;     // two buffers of -lse2, -D (64 each)
-  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
+  const int tid = threadIdx.x, group = tid >> 7, tr = (tid & 127) >> 4, tc = tid & 15;
   const int block = own / (kBlock / kF32Rows), r0 = own * kF32Rows, half = block & 1;
   const int64_t base = bh * N;
   const float *a0 = KV ? x.k : x.q, *a1 = KV ? x.v : x.d_o, *b0 = KV ? x.q : x.k, *b1 = KV ? x.d_o : x.v;
@@ -209,12 +226,16 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   auto load_stats = [&](float* dst, int blk) {
     if (tid < 32) copy16(dst + 4 * tid, x.stats + (bh * nB + blk) * 128 + 4 * tid, true);
   };
-  auto next_of = [&](int e) {  // the next entry at e or behind it that this half keeps
+  int nth = 0;  // kept entries so far: this CTA takes those of its parity
+  auto next_of = [&](int e) {
     for (; e < n_list; ++e) {
       const int entry = list[e];
       if (!((entry >> half) & 1)) continue;
-      if ((entry >> 2) >= 0 && (entry >> 2) < nB) break;
-      if (tid == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
+      if ((entry >> 2) < 0 || (entry >> 2) >= nB) {
+        if (tid == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
+        continue;
+      }
+      if ((nth++ & 1) == rank) break;
     }
     return e;
   };
@@ -230,11 +251,11 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   load(sA0, a0, r0, kF32Rows);
   load(sA1, a1, r0, kF32Rows);
   if (!KV) load_stats(sStat, block);
-  float acc0[2][NC], acc1[2][NC];
+  float acc[4][NC];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < NC; ++j) acc0[i][j] = acc1[i][j] = 0.0f;
+    for (int j = 0; j < NC; ++j) acc[i][j] = 0.0f;
   const float scale_log2 = scale * 1.4426950408889634f;
 
   int e = next_of(0);
@@ -248,74 +269,68 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     const float* sB0 = sB + buf * 2 * Cfg::kB;
     const float* sB1 = sB0 + Cfg::kB;
     const float* st = sStat + (KV ? buf * 128 : (block * kBlock == r0 ? 0 : kF32Rows));
-    float u[2][4], w[2][4];
+    const float* pa = (group == 0 ? sA0 : sA1) + tr * LD;
+    const float* pb = (group == 0 ? sB0 : sB1) + tc * LD;
+    float u[4][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[i][j] = w[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) u[i][j] = 0.0f;
 #pragma unroll 2
     for (int c = 0; c < D; c += 4) {
-      float4 p0[2], p1[2];
+      float4 a[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        p0[i] = *reinterpret_cast<const float4*>(sA0 + (tr + 16 * i) * LD + c);
-        p1[i] = *reinterpret_cast<const float4*>(sA1 + (tr + 16 * i) * LD + c);
-      }
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(pa + 8 * i * LD + c);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 w0 = *reinterpret_cast<const float4*>(sB0 + (tc + 16 * j) * LD + c);
-        const float4 w1 = *reinterpret_cast<const float4*>(sB1 + (tc + 16 * j) * LD + c);
+        const float4 w = *reinterpret_cast<const float4*>(pb + 16 * j * LD + c);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          u[i][j] = fmaf(p0[i].x, w0.x, fmaf(p0[i].y, w0.y, fmaf(p0[i].z, w0.z, fmaf(p0[i].w, w0.w, u[i][j]))));
-          w[i][j] = fmaf(p1[i].x, w1.x, fmaf(p1[i].y, w1.y, fmaf(p1[i].z, w1.z, fmaf(p1[i].w, w1.w, w[i][j]))));
-        }
+        for (int i = 0; i < 4; ++i)
+          u[i][j] = fmaf(a[i].x, w.x, fmaf(a[i].y, w.y, fmaf(a[i].z, w.z, fmaf(a[i].w, w.w, u[i][j]))));
       }
     }
+    if (group == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = tr + 16 * i, s = tc + 16 * j, q = KV ? s : r, key = KV ? r0 + r : blk * kBlock + s;
-        // keys past N hold zero scores, not -inf: their weight is forced to 0
-        const float p = key < N ? exp2f(fmaf(u[i][j], scale_log2, st[q])) : 0.0f;
-        if (KV) sP[r * LP + s] = p;
-        sDS[r * LP + s] = p * (w[i][j] + st[64 + q]);
-      }
+        for (int j = 0; j < 4; ++j) {
+          const int r = tr + 8 * i, s = tc + 16 * j, key = KV ? r0 + r : blk * kBlock + s;
+          // keys past N hold zero scores, not -inf: their weight is forced to 0
+          sP[r * LP + s] = key < N ? exp2f(fmaf(u[i][j], scale_log2, st[KV ? s : r])) : 0.0f;
+        }
     }
     __syncthreads();
-#pragma unroll 2
-    for (int s = 0; s < kBlock; s += 4) {
-      float4 ds[2], p[2];
+    if (group == 1) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ds[i] = *reinterpret_cast<const float4*>(sDS + (tr + 16 * i) * LP + s);
-        if (KV) p[i] = *reinterpret_cast<const float4*>(sP + (tr + 16 * i) * LP + s);
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = tr + 8 * i, s = tc + 16 * j;
+          sDS[r * LP + s] = sP[r * LP + s] * (u[i][j] + st[64 + (KV ? s : r)]);
+        }
+    }
+    __syncthreads();
+    const float* px = (KV && group == 0 ? sP : sDS) + tr * LP;
+    const float* pw = KV && group == 0 ? sB1 : sB0;
+    const int s0 = KV ? 0 : group * (kBlock / 2), s1 = KV ? kBlock : s0 + kBlock / 2;
+#pragma unroll 2
+    for (int s = s0; s < s1; s += 4) {
+      float4 d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const float4*>(px + 8 * i * LP + s);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          float w0[kW], w1[kW];
-          const float* at0 = sB0 + (s + k) * LD + (g * 16 + tc) * kW;
-          const float* at1 = sB1 + (s + k) * LD + (g * 16 + tc) * kW;
-          if constexpr (kW == 4) {
-            *reinterpret_cast<float4*>(w0) = *reinterpret_cast<const float4*>(at0);
-            if (KV) *reinterpret_cast<float4*>(w1) = *reinterpret_cast<const float4*>(at1);
-          } else {
-            *reinterpret_cast<float2*>(w0) = *reinterpret_cast<const float2*>(at0);
-            if (KV) *reinterpret_cast<float2*>(w1) = *reinterpret_cast<const float2*>(at1);
-          }
+          float w[kW];
+          const float* at = pw + (s + k) * LD + (g * 16 + tc) * kW;
+          if constexpr (kW == 4) *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(at);
+          else *reinterpret_cast<float2*>(w) = *reinterpret_cast<const float2*>(at);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float d = reinterpret_cast<const float*>(&ds[i])[k];
+          for (int i = 0; i < 4; ++i) {
+            const float y = reinterpret_cast<const float*>(&d[i])[k];
 #pragma unroll
-            for (int j = 0; j < kW; ++j) acc0[i][g * kW + j] = fmaf(d, w0[j], acc0[i][g * kW + j]);
-            if (KV) {
-              const float y = reinterpret_cast<const float*>(&p[i])[k];
-#pragma unroll
-              for (int j = 0; j < kW; ++j) acc1[i][g * kW + j] = fmaf(y, w1[j], acc1[i][g * kW + j]);
-            }
+            for (int j = 0; j < kW; ++j) acc[i][g * kW + j] = fmaf(y, w[j], acc[i][g * kW + j]);
           }
         }
       }
@@ -324,27 +339,49 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     e = following;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  // the sums of the second CTA, and for dQ of the second group, go through the first's buffers
+  // [2][32][D]: KV: dV and dK of rank 1; else dQ of the groups
+  float* sum = sB + group * kF32Rows * D;
+  auto slot = [&](int i, int j) { return (tr + 8 * i) * D + ((j / kW) * 16 + tc) * kW + j % kW; };
+  if (rank == 1 || (!KV && group == 1)) {
+    float* to = sum;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = r0 + tr + 16 * i;
-    if (n >= N) continue;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int64_t at = (base + n) * D + ((j / kW) * 16 + tc) * kW + j % kW;
-      (KV ? x.dk : x.dq)[at] = acc0[i][j] * scale;
-      if (KV) x.dv[at] = acc1[i][j];
+      for (int j = 0; j < NC; ++j) to[slot(i, j)] = acc[i][j];
+  }
+  cluster.sync();
+  if (rank == 0) {
+    const float* far = cluster.map_shared_rank(sB, 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = r0 + tr + 8 * i;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int at = slot(i, j);
+        if (KV) {
+          const float v = acc[i][j] + far[group * kF32Rows * D + at];
+          if (n < N) (group == 0 ? x.dv : x.dk)[(base + r0) * D + at] = group == 0 ? v : v * scale;
+        } else if (group == 0) {
+          const float v = (acc[i][j] + sB[kF32Rows * D + at]) + (far[at] + far[kF32Rows * D + at]);
+          if (n < N) x.dq[(base + r0) * D + at] = v * scale;
+        }
+      }
     }
   }
+  cluster.sync();  // nobody leaves while its buffers are read
 }
 
+// CTAs of a head: pairs for the key rows, then pairs for the query rows.
 template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_f32_kernel(F32Args x, const int32_t* __restrict__ tile_ptr,
-                                                           const int32_t* __restrict__ tile_col, BwdLists lists, int N,
-                                                           int nB, int nPairs, int owners, float scale,
-                                                           int32_t* dev_status) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256)
+    attn_bwd_f32_kernel(F32Args x, const int32_t* __restrict__ tile_ptr, const int32_t* __restrict__ tile_col,
+                        BwdLists lists, int N, int nB, int nPairs, int owners, float scale, int32_t* dev_status) {
   extern __shared__ __align__(16) float smem_bwd[];
-  const bool kv = static_cast<int>(blockIdx.x) < owners;
-  const int own = static_cast<int>(blockIdx.x) - (kv ? 0 : owners);
+  const int pair = static_cast<int>(blockIdx.x) / 2;
+  const bool kv = pair < owners;
+  const int own = pair - (kv ? 0 : owners);
   const int64_t bh = blockIdx.y, tile = bh * nPairs + own / (2 * kBlock / kF32Rows);
   if (kv) {
     bwd_f32<D, true>(x, bh, own, lists.col + tile * nB, lists.cost[tile], N, nB, scale, smem_bwd, dev_status);
@@ -364,7 +401,7 @@ static cudaError_t launch_f32(const Dims& Dm, const BwdArgs& x, const fva_mask* 
                      static_cast<const float*>(x.d_o), ws.stats,                       static_cast<float*>(x.dq),
                      static_cast<float*>(x.dk),        static_cast<float*>(x.dv)};
   const int owners = static_cast<int>((Dm.N + kF32Rows - 1) / kF32Rows);
-  attn_bwd_f32_kernel<D><<<dim3(static_cast<unsigned>(2 * owners), static_cast<unsigned>(Dm.BH)), 256, F32Cfg<D>::kSmem, st>>>(
+  attn_bwd_f32_kernel<D><<<dim3(static_cast<unsigned>(4 * owners), static_cast<unsigned>(Dm.BH)), 256, F32Cfg<D>::kSmem, st>>>(
       a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N), static_cast<int>(Dm.nB),
       static_cast<int>(Dm.nPairs), owners, x.scale, dev_status);
   return cudaGetLastError();
@@ -375,7 +412,7 @@ static cudaError_t launch_prepare(const Dims& Dm, const BwdArgs& x, const fva_ma
                                   int32_t* dev_status, cudaStream_t st) {
   const int chunks = static_cast<int>((Dm.nB + kListRows - 1) / kListRows);
   const int64_t list_ctas = chunks * Dm.BH, rows = Dm.rows * kBlock;
-  const int64_t per_cta = kPrepThreads * 16 / (D * static_cast<int>(sizeof(T)));
+  const int64_t per_cta = kStatRows * kPrepThreads * 16 / (D * static_cast<int>(sizeof(T)));
   const size_t smem = static_cast<size_t>(kListRows) * Dm.nWords * 4;
   const cudaError_t e = cudaFuncSetAttribute(prepare_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
