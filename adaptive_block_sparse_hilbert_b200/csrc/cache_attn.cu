@@ -134,24 +134,18 @@ struct Walk {
   __device__ int slot() const { return at == first_at ? 0 : 1; }
 };
 
-// Writes a finished row, or its unnormalised parts for the join. x: this thread's channel.
+// A row's statistics: the log-sum-exp of a finished row, or maximum and sum for the join.
 template <typename T, int D>
-__device__ __forceinline__ void put_row(const AttnView<T>& a, bool whole, int share, int slot, int64_t row, int g, int ch,
-                                        float x, float mx, float sum) {
+__device__ __forceinline__ void put_stats(const AttnView<T>& a, bool whole, int share, int slot, int64_t row, int g,
+                                          float mx, float sum) {
   if (whole) {
-    from_f32(sum > 0.0f ? x / sum : 0.0f, a.o + row * D + ch);
-    if (ch == 0) {
-      const float l2 = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
-      if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-      if (a.ws.scores) a.ws.lse[row] = l2;
-    }
+    const float l2 = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
+    if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+    if (a.ws.scores) a.ws.lse[row] = l2;
   } else {
     float* part = a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + g) * (D + 2);
-    part[ch] = x;
-    if (ch == 0) {
-      part[D] = mx;
-      part[D + 1] = sum;
-    }
+    part[D] = mx;
+    part[D + 1] = sum;
   }
 }
 
@@ -282,7 +276,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   using Cfg = SplitCfg<D>;
   using F = Frag<T>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float s_o[kGroup][D];
+  __shared__ float2 s_o[2][8][D / 2 + 4];  // (the padding spreads the rows over the banks)
   __shared__ float s_m[4][kGroup], s_l[4][kGroup];
   __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
   __shared__ int s_valid[Cfg::kStages], s_abort;
@@ -348,11 +342,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       }
       const int nk = s_valid[stage] - warp * 16;  // this warp's keys that count
       const uint32_t sk = smem_u32(ring + stage * 2 * Cfg::kTile), sv = sk + Cfg::kTile;
-      float s[2][4];
+      float s[2][4], s1[2][4];  // sums over the even and the odd steps: two chains of products
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) s[n][i] = s1[n][i] = 0.0f;
       if (nk > 0) {
         if (nk < 16) {  // values behind the sequence's end may be NaN, and 0 NaN is NaN: clear them
           for (int i = lane; i < (16 - nk) * (D / 8); i += 32) {
@@ -366,8 +360,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t kb[4];
           ldmatrix4(kb, sk + tile_at(warp * 16 + (lm >> 1) * 8 + lr, kk * 2 + (lm & 1)));
-          F::mma(s[0], qa[kk], kb[0], kb[1]);
-          F::mma(s[1], qa[kk], kb[2], kb[3]);
+          F::mma(kk & 1 ? s1[0] : s[0], qa[kk], kb[0], kb[1]);
+          F::mma(kk & 1 ? s1[1] : s[1], qa[kk], kb[2], kb[3]);
         }
       }
 #pragma unroll
@@ -375,7 +369,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = n * 8 + ct * 2 + (i & 1);
-          s[n][i] = key < nk ? s[n][i] * a.scale_log2 : -INFINITY;
+          s[n][i] = key < nk ? (s[n][i] + s1[n][i]) * a.scale_log2 : -INFINITY;
         }
       if (a.ws.scores) {  // kept for the accumulation: -inf behind the last key
         float* out = a.ws.scores + row0 * a.c.max_blocks * kBlock + static_cast<int64_t>(first_pos + j) * kBlock + warp * 16;
@@ -417,13 +411,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
           }
         }
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t vb[4];
-          ldmatrix4_trans(vb, sv + tile_at(warp * 16 + (lm & 1) * 8 + lr, n * 2 + (lm >> 1)));
-          F::mma(o[2 * n], ph, vb[0], vb[1]);
-          F::mma(o[2 * n + 1], ph, vb[2], vb[3]);
-          F::mma(o[2 * n], pl, vb[0], vb[1]);
-          F::mma(o[2 * n + 1], pl, vb[2], vb[3]);
+        for (int n0 = 0; n0 < D / 16; n0 += 2) {  // two pieces at a time: a product between dependent ones
+          uint32_t vb[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            ldmatrix4_trans(vb[k], sv + tile_at(warp * 16 + (lm & 1) * 8 + lr, (n0 + k) * 2 + (lm >> 1)));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            F::mma(o[2 * (n0 + k)], ph, vb[k][0], vb[k][1]);
+            F::mma(o[2 * (n0 + k) + 1], ph, vb[k][2], vb[k][3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            F::mma(o[2 * (n0 + k)], pl, vb[k][0], vb[k][1]);
+            F::mma(o[2 * (n0 + k) + 1], pl, vb[k][2], vb[k][3]);
+          }
         }
         if (nk < 16) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next load overwrites them
       }
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       }
     }
     if (!ok) break;
-    // ---- join the four warps, one after the other, in shared memory
+    // ---- join the four warps: 2 and 3 hand over to 0 and 1, then 1 to 0, eight rows at a time
     auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -448,40 +450,53 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       }
     }
     sync4();
-    float f[2];
+    const bool whole = w.whole();
+    const int slot = w.slot();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i) {  // fragment rows rg, then rg + 8
+      if (i * 8 >= ng) break;
       const int r = rg + i * 8;
       const float mx = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-      f[i] = m[i] == -INFINITY ? 0.0f : exp2f(s_m[warp][r] - mx);
-    }
-    for (int turn = 0; turn < 4; ++turn) {
-      if (turn == warp) {
+      const float f = m[i] == -INFINITY ? 0.0f : exp2f(s_m[warp][r] - mx);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+      for (int step = 2; step > 0; step >>= 1) {
+        if (warp >= step && warp < 2 * step) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = rg + (i >> 1) * 8;
-            if (r < ng) {
-              float* at = &s_o[r][n * 8 + ct * 2 + (i & 1)];
-              const float x = o[n][i] * f[i >> 1];
-              *at = turn == 0 ? x : *at + x;
-            }
+          for (int n = 0; n < D / 8; ++n)
+            s_o[warp - step][rg][n * 4 + ct] = step == 2 ? make_float2(o[n][2 * i] * f, o[n][2 * i + 1] * f)
+                                                         : make_float2(o[n][2 * i], o[n][2 * i + 1]);
+        }
+        sync4();
+        if (warp < step) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float2 x = s_o[warp][rg][n * 4 + ct];
+            o[n][2 * i] = (step == 2 ? o[n][2 * i] * f : o[n][2 * i]) + x.x;
+            o[n][2 * i + 1] = (step == 2 ? o[n][2 * i + 1] * f : o[n][2 * i + 1]) + x.y;
           }
+        }
+        if (step == 2) sync4();
       }
-      sync4();
-    }
-    const bool whole = w.whole();
-    for (int i = tid; i < ng * D; i += 128) {
-      const int g = i / D, ch = i % D;
-      const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
-      float sum = 0.0f;
+      if (warp == 0 && r < ng) {
+        float sum = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) sum += s_m[v][g] == -INFINITY ? 0.0f : s_l[v][g] * exp2f(s_m[v][g] - mx);
-      put_row<T, D>(a, whole, share, w.slot(), row0 + g, g, ch, s_o[g][ch], mx, sum);
+        for (int v = 0; v < 4; ++v) sum += s_m[v][r] == -INFINITY ? 0.0f : s_l[v][r] * exp2f(s_m[v][r] - mx);
+        const int64_t row = row0 + r;
+        if (whole) {
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          uint32_t* out = reinterpret_cast<uint32_t*>(a.o + row * D);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) out[n * 4 + ct] = F::pack(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+        } else {
+          float2* part = reinterpret_cast<float2*>(a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + r) * (D + 2));
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) part[n * 4 + ct] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+        }
+        if (ct == 0) put_stats<T, D>(a, whole, share, slot, row, r, mx, sum);
+      }
+      sync4();  // the buffers are rewritten by the next rows, s_m and s_l by the next unit
     }
     if (tid == 0) a.ws.start[w.u] = w.start;
-    sync4();  // s_m, s_l and s_o are rewritten by the next unit
     w.at = stop;
   }
   if (!ok) {
@@ -518,6 +533,13 @@ __device__ __forceinline__ void load_vec(const float* p, float (&x)[V]) {
   }
 }
 
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  else p[0] = x[0];
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float> a, uint64_t wait_limit_ns) {
   using Cfg = SplitF32Cfg<D>;
@@ -525,7 +547,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) float s_q[G][D];
   __shared__ __align__(16) float s_p[4][G][16];
-  __shared__ float s_o[G][D];
+  __shared__ __align__(16) float s_o[2][G][D];
   __shared__ float s_m[4][G], s_l[4][G];
   __shared__ uint64_t full[Cfg::kStages], empty[Cfg::kStages];
   __shared__ int s_valid[Cfg::kStages], s_abort;
@@ -651,7 +673,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
       }
     }
     if (!ok) break;
-    // ---- join the four warps, one after the other, in shared memory
+    // ---- join the four warps: 2 and 3 hand over to 0 and 1, then 1 to 0
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = l[g];
@@ -663,29 +685,48 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
       }
     }
     sync4();
-    for (int turn = 0; turn < 4; ++turn) {
-      if (turn == warp) {
+    const bool whole = w.whole();
+    const int slot = w.slot();
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
-          const float f = m[g] == -INFINITY ? 0.0f : exp2f(m[g] - mx);
+    for (int g = 0; g < G; ++g) {
+      const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+      const float f = m[g] == -INFINITY ? 0.0f : exp2f(m[g] - mx);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float* at = &s_o[g][lane * V + i];
-            *at = turn == 0 ? acc[g][i] * f : fmaf(acc[g][i], f, *at);
-          }
-        }
+      for (int i = 0; i < V; ++i) acc[g][i] *= f;
+      m[g] = mx;
+    }
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1) {
+      if (warp >= step && warp < 2 * step) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) store_vec<V>(&s_o[warp - step][g][lane * V], acc[g]);
       }
       sync4();
-    }
-    const bool whole = w.whole();
-    for (int i = tid; i < ng * D; i += 128) {
-      const int g = i / D, ch = i % D;
-      const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
-      float sum = 0.0f;
+      if (warp < step) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) sum += s_m[v][g] == -INFINITY ? 0.0f : s_l[v][g] * exp2f(s_m[v][g] - mx);
-      put_row<float, D>(a, whole, share, w.slot(), row0 + g, g, ch, s_o[g][ch], mx, sum);
+        for (int g = 0; g < G; ++g) {
+          float x[V];
+          load_vec<V>(&s_o[warp][g][lane * V], x);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[g][i] += x[i];
+        }
+      }
+      if (step == 2) sync4();
+    }
+    if (warp == 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (g >= ng) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum += s_m[v][g] == -INFINITY ? 0.0f : s_l[v][g] * exp2f(s_m[v][g] - m[g]);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        float* out = whole ? a.o + (row0 + g) * D
+                           : a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + g) * (D + 2);
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[lane * V + i] = whole ? acc[g][i] * inv : acc[g][i];
+        if (lane == 0) put_stats<float, D>(a, whole, share, slot, row0 + g, g, m[g], sum);
+      }
     }
     if (tid == 0) a.ws.start[w.u] = w.start;
     sync4();  // the next unit rewrites what was read here
