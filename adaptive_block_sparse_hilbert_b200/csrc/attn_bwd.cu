@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const int32_t* __
                                                                const float* __restrict__ lse, int64_t rows, int N,
                                                                float* __restrict__ stats, int32_t* dev_status) {
   extern __shared__ uint32_t bits[];  // [kListRows][nWords]
+  grid_wait();
+  grid_release();
   if (static_cast<int>(blockIdx.x) < list_ctas) {
     build_lists(blockIdx.x % chunks, blockIdx.x / chunks, row_ptr, col_idx, nB, nWords, nPairs, lists, bits, dev_status);
     return;
@@ -154,6 +156,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const int32_t* __
 __global__ void __launch_bounds__(512) order_kernel(const int32_t* __restrict__ cost, int nPairs,
                                                     int32_t* __restrict__ worklist) {
   extern __shared__ int32_t sc[];
+  grid_wait();
+  grid_release();
   const int64_t base = static_cast<int64_t>(blockIdx.x) * nPairs;
   for (int i = threadIdx.x; i < nPairs; i += 512) sc[i] = cost[base + i];
   __syncthreads();
@@ -375,10 +379,11 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
 
 // CTAs of a head: pairs for the key rows, then pairs for the query rows.
 template <int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256)
+__global__ void __launch_bounds__(256)
     attn_bwd_f32_kernel(F32Args x, const int32_t* __restrict__ tile_ptr, const int32_t* __restrict__ tile_col,
                         BwdLists lists, int N, int nB, int nPairs, int owners, float scale, int32_t* dev_status) {
   extern __shared__ __align__(16) float smem_bwd[];
+  grid_wait();
   const int pair = static_cast<int>(blockIdx.x) / 2;
   const bool kv = pair < owners;
   const int own = pair - (kv ? 0 : owners);
@@ -401,10 +406,9 @@ static cudaError_t launch_f32(const Dims& Dm, const BwdArgs& x, const fva_mask* 
                      static_cast<const float*>(x.d_o), ws.stats,                       static_cast<float*>(x.dq),
                      static_cast<float*>(x.dk),        static_cast<float*>(x.dv)};
   const int owners = static_cast<int>((Dm.N + kF32Rows - 1) / kF32Rows);
-  attn_bwd_f32_kernel<D><<<dim3(static_cast<unsigned>(4 * owners), static_cast<unsigned>(Dm.BH)), 256, F32Cfg<D>::kSmem, st>>>(
-      a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N), static_cast<int>(Dm.nB),
-      static_cast<int>(Dm.nPairs), owners, x.scale, dev_status);
-  return cudaGetLastError();
+  return launch_chained(attn_bwd_f32_kernel<D>, dim3(static_cast<unsigned>(4 * owners), static_cast<unsigned>(Dm.BH)), 256,
+                        2, F32Cfg<D>::kSmem, st, a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N),
+                        static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), owners, x.scale, dev_status);
 }
 
 template <typename T, int D>
@@ -417,11 +421,11 @@ static cudaError_t launch_prepare(const Dims& Dm, const BwdArgs& x, const fva_ma
   const cudaError_t e = cudaFuncSetAttribute(prepare_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  prepare_kernel<T, D><<<static_cast<unsigned>(list_ctas + (rows + per_cta - 1) / per_cta), kPrepThreads, smem, st>>>(
-      m->row_ptr, m->col_idx, static_cast<int>(Dm.nB), static_cast<int>(Dm.nWords), static_cast<int>(Dm.nPairs), chunks,
-      static_cast<int>(list_ctas), ws.lists, static_cast<const T*>(x.o), static_cast<const T*>(x.d_o), x.lse, rows,
-      static_cast<int>(Dm.N), ws.stats, dev_status);
-  return cudaGetLastError();
+  return launch_chained(prepare_kernel<T, D>, dim3(static_cast<unsigned>(list_ctas + (rows + per_cta - 1) / per_cta)),
+                        kPrepThreads, 0, smem, st, m->row_ptr, m->col_idx, static_cast<int>(Dm.nB),
+                        static_cast<int>(Dm.nWords), static_cast<int>(Dm.nPairs), chunks, static_cast<int>(list_ctas),
+                        ws.lists, static_cast<const T*>(x.o), static_cast<const T*>(x.d_o), x.lse, rows,
+                        static_cast<int>(Dm.N), ws.stats, dev_status);
 }
 
 cudaError_t launch_attn_bwd(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,
@@ -449,8 +453,8 @@ cudaError_t launch_attn_bwd(const Dims& Dm, const BwdArgs& x, const fva_mask* m,
     const size_t smem = static_cast<size_t>(Dm.nPairs) * 4;
     e = cudaFuncSetAttribute(order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    order_kernel<<<static_cast<unsigned>(Dm.BH), 512, smem, st>>>(ws.lists.cost, static_cast<int>(Dm.nPairs), ws.worklist);
-    e = cudaGetLastError();
+    e = launch_chained(order_kernel, dim3(static_cast<unsigned>(Dm.BH)), 512, 0, smem, st, ws.lists.cost,
+                       static_cast<int>(Dm.nPairs), ws.worklist);
     if (e != cudaSuccess) return e;
   }
   return launch_attn_bwd_tc(Dm, x, m, ws, ordered ? ws.worklist : nullptr, dev_status, st);

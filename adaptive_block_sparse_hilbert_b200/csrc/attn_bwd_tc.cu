@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                        const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
                        const __grid_constant__ BwdTcArgs x) {
   const int slot = static_cast<int>(blockIdx.x);
+  grid_wait();
   if (slot < x.ntiles) bwd_tile<D, true>(x, tmk, tmv, tmq, tmdo, slot);
   else bwd_tile<D, false>(x, tmq, tmdo, tmk, tmv, slot - x.ntiles);
 }
@@ -542,8 +543,8 @@ static cudaError_t launch_tc_d(const BwdTcArgs& a, const CUtensorMap& mq, const 
   const cudaError_t e = cudaFuncSetAttribute(attn_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_bwd_tc_kernel<D><<<2 * static_cast<unsigned>(a.ntiles), kBwdThreads, smem, st>>>(mq, mk, mv, mdo, a);
-  return cudaGetLastError();
+  return launch_chained(attn_bwd_tc_kernel<D>, dim3(2 * static_cast<unsigned>(a.ntiles)), kBwdThreads, 0, smem, st, mq, mk,
+                        mv, mdo, a);
 }
 
 cudaError_t launch_attn_bwd_tc(const Dims& Dm, const BwdArgs& x, const fva_mask* m, const BwdScratch& ws,

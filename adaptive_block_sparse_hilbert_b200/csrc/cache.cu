@@ -385,6 +385,8 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_kernel(CacheView<T> c,
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_wait();
+  grid_release();
   const int len = seq_len(c, b, dev_status);
   const int nB = (len + kBlock - 1) / kBlock, G = H / c.Hkv;
   const int per = (nB + C - 1) / C, lo = min(rank * per, nB), hi = min(lo + per, nB);
@@ -538,6 +540,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_wait();
+  grid_release();
   const int len = seq_len(c, b, dev_status);
   int32_t* out = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep;
   if (h == 0 && rank == 0 && tid == 0) new_len[b] = min(len, keep);
@@ -723,6 +727,7 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
                                                                   int32_t* dev_status) {
   using P = PageRows<T, D>;
   const int b = blockIdx.z, h = blockIdx.y, block = blockIdx.x;
+  grid_wait();
   const int len = seq_len(c, b, nullptr);
   const int n = min(min(len, keep) - block * kBlock, kBlock);
   if (n <= 0) return;
@@ -779,24 +784,12 @@ static int cluster_size(int64_t units, int64_t items, int64_t least) {
   return n;
 }
 
-template <typename... Args>
-static cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int threads, int cluster, size_t smem,
-                                  cudaStream_t st, Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+template <typename... Params, typename... Args>
+static cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, int cluster, size_t smem,
+                                  cudaStream_t st, const Args&... args) {
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_chained(kernel, grid, threads, cluster, smem, st, args...);
 }
 
 struct AppendCall {
@@ -875,9 +868,8 @@ struct EvictCall {
                                    static_cast<size_t>(hold) * 4, st, v, keep, n_sink, n_recent, hold, kept, new_len,
                                    dev_status);
     if (e != cudaSuccess) return e;
-    evict_copy_kernel<T, D><<<dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B), kPageThreads, 0, st>>>(
-        v, keep, dst_table, dst_blocks, kept, dev_status);
-    return cudaGetLastError();
+    return launch_chained(evict_copy_kernel<T, D>, dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B),
+                          kPageThreads, 0, 0, st, v, keep, dst_table, dst_blocks, kept, dev_status);
   }
 };
 

@@ -290,6 +290,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     s_abort = 0;
     fence_mbar_init();
   }
+  grid_wait();
+  grid_release();
   const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
   Walk<T> w(sh, share);
   volatile int* abort_flag = &s_abort;
@@ -561,6 +563,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
     s_abort = 0;
     fence_mbar_init();
   }
+  grid_wait();
+  grid_release();
   const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
   Walk<float> w(sh, share);
   volatile int* abort_flag = &s_abort;
@@ -741,27 +745,45 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
 // ---------------------------------------------------------------------------------
 // Join and accumulation
 // ---------------------------------------------------------------------------------
-// CTA (x, key head, sequence): every CTA forms the heads' log-sum-exp from the shares' maxima
-// and sums; x = 0 also joins their O (a warp per head), and, where weights are accumulated,
-// each adds exp(s - lse), summed over the heads, to the masses of every gridDim.x-th piece of 16
-// listed blocks.
+// CTA (x, key head, sequence), 0 < x: forms the heads' log-sum-exp from the shares' maxima and
+// sums and adds exp(s - lse), summed over the heads, to the masses of pieces x - 1, x - 1 + (the
+// grid's x less one), .. of 16 listed blocks. x = 0 joins the shares' O, a warp per head. Little
+// is moved: what such a CTA takes is its chain of dependent loads.
 constexpr int kJoinThreads = 256, kMassBlocks = 16;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, int accumulate) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
   __shared__ float s_lse[kMaxCacheGroup];
   __shared__ int s_page[kMassBlocks], s_valid[kMassBlocks];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = b * a.c.Hkv + h;
-  const int n = unit_count(a, bh * a.GS, nullptr);
-  if (blockIdx.x > 0 && static_cast<int>(blockIdx.x) * kMassBlocks >= n) return;
+  const bool joins = blockIdx.x == 0;
+  grid_wait();
+  grid_release();
+  const int len = seq_len(a.c, b, nullptr), n = unit_count(a, bh * a.GS, nullptr);
+  const int first = joins ? 0 : (blockIdx.x - 1) * kMassBlocks;
+  if (!joins && first >= n) return;
+  auto find_pages = [&](int pos0) {
+    if (tid < kMassBlocks) {
+      const int pos = pos0 + tid;
+      int page = -1, valid = 0;
+      if (pos < n) {
+        const int block = unit_block(a, bh, pos, len, nullptr);
+        if (block >= 0) page = page_of(a.c, b, block, nullptr);
+        if (page >= 0) valid = min(len - block * kBlock, kBlock);
+      }
+      s_page[tid] = page;
+      s_valid[tid] = valid;
+    }
+  };
+  if (!joins) find_pages(first);
   const int64_t per = n ? *a.ws.per : 1;
   for (int g = warp; g < a.G; g += kJoinThreads / 32) {
     const int64_t row = static_cast<int64_t>(b) * a.H + h * a.G + g;
     const int64_t start = n ? a.ws.start[bh * a.GS + g / kGroup] : 0;
     const int c0 = static_cast<int>(start / per), c1 = n ? static_cast<int>((start + n - 1) / per) : c0;
     if (n && c0 == c1) {  // finished by the split kernel
-      if (lane == 0 && accumulate) s_lse[g] = a.ws.lse[row];
+      if (!joins && lane == 0) s_lse[g] = a.ws.lse[row];
       continue;
     }
     constexpr int V = D / 32;
@@ -784,58 +806,55 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, int a
       for (int k = 16; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
       sum = sum * f0 + t;
       mx = m_new;
-      if (blockIdx.x == 0) {
+      if (joins) {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] *= f0;
         const int cnt = min(32, c1 - s0 + 1);
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k) {
-          const float fk = __shfl_sync(0xffffffffu, f, k);
-          const float* x = part_of(s0 + k) + lane * V;
+        for (int k0 = 0; k0 < cnt; k0 += 8) {  // eight shares' rows on their way at a time
+          float x[8][V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fk == 0.0f ? acc[i] : fmaf(fk, x[i], acc[i]);
+          for (int k = 0; k < 8; ++k) {
+            const float* from = part_of(s0 + min(k0 + k, cnt - 1)) + lane * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[k][i] = from[i];
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = k0 + k < cnt && fk != 0.0f ? fmaf(fk, x[k][i], acc[i]) : acc[i];
+          }
         }
       }
     }
     const float l2 = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
-    if (blockIdx.x == 0) {
+    if (joins) {
 #pragma unroll
       for (int i = 0; i < V; ++i) from_f32(sum > 0.0f ? acc[i] / sum : 0.0f, a.o + row * D + lane * V + i);
       if (lane == 0 && a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+    } else if (lane == 0) {
+      s_lse[g] = l2;
     }
-    if (lane == 0) s_lse[g] = l2;
   }
-  if (!accumulate) return;
-  const int len = seq_len(a.c, b, nullptr);
+  if (joins) return;
   const int64_t head_stride = static_cast<int64_t>(a.c.max_blocks) * kBlock;
-  for (int pos0 = blockIdx.x * kMassBlocks; pos0 < n; pos0 += gridDim.x * kMassBlocks) {
-    __syncthreads();  // (the first pass: s_lse is complete)
-    if (tid < kMassBlocks) {
-      const int pos = pos0 + tid;
-      int page = -1, valid = 0;
-      if (pos < n) {
-        const int block = unit_block(a, bh, pos, len, nullptr);
-        if (block >= 0) page = page_of(a.c, b, block, nullptr);
-        if (page >= 0) valid = min(len - block * kBlock, kBlock);
-      }
-      s_page[tid] = page;
-      s_valid[tid] = valid;
-    }
-    __syncthreads();
+  for (int pos0 = first; pos0 < n;) {
+    __syncthreads();  // s_lse and the pages are there
+    // scores behind a sequence's end and of skipped pages are -inf; entries behind the list's
+    // end were not written
     const float* s = a.ws.scores + (static_cast<int64_t>(b) * a.H + h * a.G) * head_stride + static_cast<int64_t>(pos0) * kBlock;
     constexpr int kPer = kMassBlocks * kBlock / kJoinThreads;
     float w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) w[i] = 0.0f;
+#pragma unroll 4
     for (int g = 0; g < a.G; ++g) {
-      float x[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int k = tid + i * kJoinThreads;
-        x[i] = k % kBlock < s_valid[k / kBlock] ? s[g * head_stride + k] : -INFINITY;
+        const float x = k % kBlock < s_valid[k / kBlock] ? s[g * head_stride + k] : -INFINITY;
+        w[i] += exp2f(x - s_lse[g]);
       }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) w[i] += exp2f(x[i] - s_lse[g]);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -843,6 +862,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, int a
       if (k % kBlock < s_valid[j])
         atomicAdd(a.c.mass + (static_cast<int64_t>(s_page[j]) * a.c.Hkv + h) * kBlock + k % kBlock, w[i]);
     }
+    pos0 += (gridDim.x - 1) * kMassBlocks;
+    __syncthreads();  // the pages are rewritten
+    find_pages(pos0);
   }
 }
 
@@ -861,8 +883,8 @@ static cudaError_t launch_f32(const AttnView<float>& a, cudaStream_t st) {
   using Cfg = SplitF32Cfg<D>;
   const cudaError_t e = cudaFuncSetAttribute(split_f32_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  split_f32_kernel<D, G><<<Cfg::kUseShares, kSplitThreads, Cfg::kSmem, st>>>(a, attn_wait_limit_ns());
-  return cudaGetLastError();
+  return launch_chained(split_f32_kernel<D, G>, dim3(Cfg::kUseShares), kSplitThreads, 0, Cfg::kSmem, st, a,
+                        attn_wait_limit_ns());
 }
 
 template <typename T, int D>
@@ -873,7 +895,8 @@ static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaSt
     const cudaError_t e = cudaFuncSetAttribute(split_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                SplitCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    split_kernel<T, D><<<kShares, kSplitThreads, SplitCfg<D>::kSmem, st>>>(mk, mv, a, attn_wait_limit_ns());
+    return launch_chained(split_kernel<T, D>, dim3(kShares), kSplitThreads, 0, SplitCfg<D>::kSmem, st, mk, mv, a,
+                          attn_wait_limit_ns());
   } else {
     const int g = a.G < kGroup ? a.G : kGroup;
     return g <= 1   ? launch_f32<D, 1>(a, st)
@@ -882,7 +905,6 @@ static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaSt
            : g <= 8 ? launch_f32<D, 8>(a, st)
                     : launch_f32<D, 16>(a, st);
   }
-  return cudaGetLastError();
 }
 
 struct AttnCall {
@@ -907,15 +929,14 @@ struct AttnCall {
     const cudaError_t e = launch_split<T, D>(c, a, st);
     if (e != cudaSuccess) return e;
     // pieces of the accumulation: about eight CTAs an SM, were every list of full length
-    unsigned chunks = 1;
+    unsigned chunks = 0;
     if (accumulate) {
-      const int64_t pieces = (s->max_blocks + kMassBlocks - 1) / kMassBlocks;
-      const int64_t most = (8 * 148 + static_cast<int64_t>(s->B) * c->Hkv - 1) / (static_cast<int64_t>(s->B) * c->Hkv);
+      const int64_t units = static_cast<int64_t>(s->B) * c->Hkv, pieces = (s->max_blocks + kMassBlocks - 1) / kMassBlocks;
+      const int64_t most = (8 * 148 + units - 1) / units;
       chunks = static_cast<unsigned>(pieces < most ? pieces : most);
     }
-    join_kernel<T, D><<<dim3(chunks, static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)), kJoinThreads, 0, st>>>(
-        a, accumulate);
-    return cudaGetLastError();
+    return launch_chained(join_kernel<T, D>, dim3(1 + chunks, static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
+                          kJoinThreads, 0, 0, st, a);
   }
 };
 

@@ -93,9 +93,34 @@ cudaError_t launch_attn_bwd_tc(const Dims& D, const BwdArgs& x, const fva_mask* 
 // 3-D TMA map over an [n, rows, d] 16-bit tensor, box = 64 elements (128 B) x 64 rows x 1.
 bool make_rows_map(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t d, bool f16);
 
+// Launch as a programmatic dependent of the stream's last kernel: the launch itself and the
+// kernel's start overlap that kernel's end. Every such kernel calls grid_wait() before it reads
+// or writes global memory, and grid_release() where its own dependents may start.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, int cluster, size_t smem,
+                                  cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---------------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------------
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
