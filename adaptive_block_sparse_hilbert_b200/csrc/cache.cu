@@ -11,12 +11,13 @@ namespace cg = cooperative_groups;
 // ---------------------------------------------------------------------------------
 // Rows of a page: copy and mean (append, eviction)
 // ---------------------------------------------------------------------------------
-// A CTA of 256 threads holds the 64 rows of one (page, key head), 16 bytes a thread and row:
-// thread = (row lane, 16-byte piece), rows row lane, row lane + kLanes, ... All of a thread's
-// loads are issued before its first store, so a CTA has up to 32 KB in flight.
-constexpr int kPageThreads = 256;
+// A CTA holds the 64 rows of one (page, key head), 16 bytes a thread and row: thread = (row
+// lane, 16-byte piece), rows row lane, row lane + kLanes, ... All of a thread's loads are issued
+// before its first store, so a CTA has up to 32 KB in flight. (16 prompts, d = 128, on 128 / 256
+// / 512 threads: 41 / 44 / 50 us; eviction of 62500 of 250 thousand tokens: 136 / 113 / 120 us.)
+constexpr int kAppendThreads = 128, kEvictCopyThreads = 256;
 
-template <typename T, int D>
+template <typename T, int D, int kPageThreads>
 struct PageRows {
   static constexpr int kPieces = D * static_cast<int>(sizeof(T)) / 16;
   static constexpr int kLanes = kPageThreads / kPieces;
@@ -27,9 +28,9 @@ struct PageRows {
 // key_mean of the page from its rows' keys in registers (rows >= n are not counted): sums in
 // float64 (exact for 16-bit keys of a usual range), divided, rounded once. A row's place in
 // the sum depends on the row alone, so the mean does not depend on how the tokens came.
-template <typename T, int D>
-__device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D>::kRows], int n, float* mean) {
-  using P = PageRows<T, D>;
+template <typename T, int D, int kPageThreads>
+__device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D, kPageThreads>::kRows], int n, float* mean) {
+  using P = PageRows<T, D, kPageThreads>;
   __shared__ double sums[P::kLanes][D];
   const int lane = threadIdx.x / P::kPieces, piece = threadIdx.x % P::kPieces;
   double s[P::kPer];
@@ -60,11 +61,11 @@ __device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D>::kRow
 // One CTA per (touched block, key head, sequence). Bound by the copy: 16 prompts of 1 to 4001
 // tokens, 8 key heads, d = 128.
 template <typename T, int D>
-__global__ void __launch_bounds__(kPageThreads) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
                                                               const T* __restrict__ v_new, int64_t token_stride,
                                                               const int32_t* __restrict__ new_ptr, int max_new,
                                                               int32_t* dev_status) {
-  using P = PageRows<T, D>;
+  using P = PageRows<T, D, kAppendThreads>;
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = seq_len(c, b, dev_status);
   const int from = new_ptr[b], n_new = new_ptr[b + 1] - from;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kPageThreads) append_kernel(CacheView<T> c, co
       if (c.mass && piece == 0) c.mass[base + r] = 0.0f;
     }
   }
-  write_mean<T, D>(k, r1, c.key_mean + (static_cast<int64_t>(page) * c.Hkv + h) * D);
+  write_mean<T, D, kAppendThreads>(k, r1, c.key_mean + (static_cast<int64_t>(page) * c.Hkv + h) * D);
 }
 
 // ---------------------------------------------------------------------------------
@@ -152,22 +153,27 @@ __device__ __forceinline__ void block_scores(const CacheView<T>& c, const double
                                              int32_t* dev_status) {
   constexpr int V = D / 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, t = lane & 3;
+  auto find_page = [&](int at) { return at < hi ? page_of(c, b, at, dev_status) : 0; };
+  int next = find_page(lo + warp * 8 + row);
 #pragma unroll 1
   for (int base = lo + warp * 8; base < hi; base += kRouteWarps * 8) {
-    const int page = base + row < hi ? page_of(c, b, base + row, dev_status) : 0;
+    const int page = next;
     const float* mean = c.key_mean + (static_cast<int64_t>(page < 0 ? 0 : page) * c.Hkv + h) * D + 4 * t;
     float4 m[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) m[i] = *reinterpret_cast<const float4*>(mean + 16 * i);
-    double x[2] = {0.0, 0.0};
+    next = find_page(base + kRouteWarps * 8 + row);
+    double x[2] = {0.0, 0.0}, y[2] = {0.0, 0.0};  // two chains of products
     const double* q = s_q[row] + 4 * t;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       dmma_8x8x4(x[0], x[1], q[16 * i], static_cast<double>(m[i].x));
-      dmma_8x8x4(x[0], x[1], q[16 * i + 1], static_cast<double>(m[i].y));
+      dmma_8x8x4(y[0], y[1], q[16 * i + 1], static_cast<double>(m[i].y));
       dmma_8x8x4(x[0], x[1], q[16 * i + 2], static_cast<double>(m[i].z));
-      dmma_8x8x4(x[0], x[1], q[16 * i + 3], static_cast<double>(m[i].w));
+      dmma_8x8x4(y[0], y[1], q[16 * i + 3], static_cast<double>(m[i].w));
     }
+    x[0] += y[0];
+    x[1] += y[1];
     // lane (head, t) holds blocks 2 t and 2 t + 1 of the eight
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -408,9 +414,8 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_kernel(CacheView<T> c,
     __syncthreads();
     block_scores<T, D>(c, s_q, ng, b, h, lo, hi, scale, sg, stride, dev_status);
     __syncthreads();
-    // maxima and sums, 16 / heads warps a head (their order is fixed: equal inputs, equal bits)
-    const int heads = ng == 1 ? 1 : ng == 2 ? 2 : ng <= 4 ? 4 : 8, wph = kRouteWarps / heads;
-    const int g = warp / wph, first = lo + (warp % wph) * 32 + lane;
+    // maxima and sums, 16 / ng warps a head (their order is fixed: equal inputs, equal bits)
+    const int wph = kRouteWarps / ng, g = warp / wph, first = lo + (warp % wph) * 32 + lane;
     const double* s = sg + g * stride;
     double m = -INFINITY;
     bool nan = false;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_kernel(CacheView<T> c,
     m = warp_max_d(m);
     if (lane == 0) sm.part[0][warp] = m;
     __syncthreads();
-    for (int k = 0; k < wph; ++k) m = fmax(m, sm.part[0][g * wph + k]);
+    for (int k = 0; k < wph && g < ng; ++k) m = fmax(m, sm.part[0][g * wph + k]);
     double z = 0.0;
     if (g < ng)
       for (int i = first; i < hi; i += wph * 32) z += exp(s[i] - m);
@@ -721,11 +726,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
 
 // One CTA per (destination block, key head, sequence): gathers its 64 kept tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c, int keep,
+__global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(CacheView<T> c, int keep,
                                                                   const int32_t* __restrict__ dst_table, int dst_blocks,
                                                                   const int32_t* __restrict__ kept,
                                                                   int32_t* dev_status) {
-  using P = PageRows<T, D>;
+  using P = PageRows<T, D, kEvictCopyThreads>;
   const int b = blockIdx.z, h = blockIdx.y, block = blockIdx.x;
   grid_wait();
   const int len = seq_len(c, b, nullptr);
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
     }
   }
   bool clash = false;
-  for (int i = threadIdx.x; i * kBlock < len; i += kPageThreads)
+  for (int i = threadIdx.x; i * kBlock < len; i += kEvictCopyThreads)
     clash |= c.table[static_cast<int64_t>(b) * c.max_blocks + i] == dst;
   if (__syncthreads_or(clash) || dst < 0 || dst >= c.n_pages) {
     if (threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(kPageThreads) evict_copy_kernel(CacheView<T> c
       if (piece == 0) c.mass[to + r] = mass[i];
     }
   }
-  write_mean<T, D>(k, n, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * D);
+  write_mean<T, D, kEvictCopyThreads>(k, n, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * D);
 }
 
 // ---------------------------------------------------------------------------------
@@ -806,7 +811,7 @@ struct AppendCall {
     // a sequence's new tokens touch at most this many blocks
     const dim3 grid(static_cast<unsigned>((max_new + kBlock - 2) / kBlock + 1), static_cast<unsigned>(c->Hkv),
                     static_cast<unsigned>(s->B));
-    append_kernel<T, D><<<grid, kPageThreads, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(k_new),
+    append_kernel<T, D><<<grid, kAppendThreads, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(k_new),
                                                        static_cast<const T*>(v_new), stride, new_ptr, max_new, dev_status);
     return cudaGetLastError();
   }
@@ -833,13 +838,17 @@ struct RouteCall {
   template <typename T, int D>
   cudaError_t operator()() const {
     const int C = cluster_size(static_cast<int64_t>(s->B) * c->Hkv, s->max_blocks, 64);
-    const int per = (s->max_blocks + C - 1) / C, most = 60 * 1024 / 8;  // two CTAs an SM
+    // Two CTAs share an SM where there are many units. Clusters are made only where SMs are to
+    // spare: their CTAs ask for more than half of an SM's shared memory, or pairs of them would
+    // share one while others idle.
+    const int per = (s->max_blocks + C - 1) / C, most = (C > 1 ? 170 : 60) * 1024 / 8;
     const int cap = s->max_blocks + kHeads * per <= most ? per : 0;
+    size_t smem = static_cast<size_t>(s->max_blocks + kHeads * cap) * sizeof(double);
+    if (C > 1 && smem < 116 * 1024) smem = 116 * 1024;
     return launch_cluster(route_kernel<T, D>,
                           dim3(static_cast<unsigned>(C), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
-                          kRouteThreads, C, static_cast<size_t>(s->max_blocks + kHeads * cap) * sizeof(double), st,
-                          cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, scale, p, k_floor, n_recent, cap,
-                          scores, kept, n_kept, dev_status);
+                          kRouteThreads, C, smem, st, cache_view<T>(c, s), static_cast<const T*>(q), q_stride, H, scale, p,
+                          k_floor, n_recent, cap, scores, kept, n_kept, dev_status);
   }
 };
 
@@ -869,7 +878,7 @@ struct EvictCall {
                                    dev_status);
     if (e != cudaSuccess) return e;
     return launch_chained(evict_copy_kernel<T, D>, dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B),
-                          kPageThreads, 0, 0, st, v, keep, dst_table, dst_blocks, kept, dev_status);
+                          kEvictCopyThreads, 0, 0, st, v, keep, dst_table, dst_blocks, kept, dev_status);
   }
 };
 

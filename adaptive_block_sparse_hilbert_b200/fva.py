@@ -419,12 +419,28 @@ def _call(fn, device, stream, *args):
         raise FvaError(fn, rc)
 
 
-def _nbytes(ws):
-    return ws.numel() * ws.element_size()
+def _scratch(fn, workspace, dev_status, device):
+    """(bytes of the workspace, its pointer, dev_status' pointer), both on the call's device."""
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace is on {workspace.device} or not contiguous, expected {device}")
+    return workspace.numel() * workspace.element_size(), workspace.data_ptr(), _status(fn, dev_status, device)
+
+
+def _status(fn, dev_status, device):
+    if dev_status is None:
+        return None
+    if dev_status.device != device or dev_status.dtype is not torch.int32 or dev_status.numel() < 1:
+        raise ValueError(f"{fn}: dev_status is {dev_status.dtype} on {dev_status.device}, expected int32 on {device}")
+    return dev_status.data_ptr()
 
 
 def _shape_dtype(s):
     return torch.bfloat16 if s.dtype == FVA_BF16 else torch.float32
+
+
+def _mask_on(fn, mask, device):
+    if mask.row_ptr.device != device or mask.tile_col.device != device or mask.worklist.device != device:
+        raise ValueError(f"{fn}: the mask is on {mask.row_ptr.device}, expected {device}")
 
 
 def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=None, stream=None):
@@ -435,8 +451,9 @@ def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=No
         _expect(fn, what, t, four, _shape_dtype(s), dev)
     _expect(fn, "v", v, four, v.dtype if v.dtype in (torch.float16, torch.bfloat16) else _shape_dtype(s), dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _call(fn, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dtype_code(v), ctypes.byref(mask.c()), _ptr(o),
-          _ptr(lse), float(scale), _ptr(dev_status))
+    _mask_on(fn, mask, dev)
+    _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(v),
+          ctypes.byref(mask.c()), o.data_ptr(), lse.data_ptr(), float(scale), _status(fn, dev_status, dev))
 
 
 def fva_sparse_attn_bwd_workspace_bytes(s): return _lib.fva_sparse_attn_bwd_workspace_bytes(ctypes.byref(s))
@@ -451,9 +468,11 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
     for what, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
         _expect(fn, what, t, four, dt, dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _call(fn, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse),
-          ctypes.byref(mask.c()), _ptr(dq), _ptr(dk), _ptr(dv), float(scale), _ptr(workspace), _nbytes(workspace),
-          _ptr(dev_status))
+    _mask_on(fn, mask, dev)
+    size, ws, status = _scratch(fn, workspace, dev_status, dev)
+    _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+          lse.data_ptr(), ctypes.byref(mask.c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), float(scale), ws, size,
+          status)
 
 
 # ------------------------------------------------------------------------------ serving
@@ -511,8 +530,8 @@ def fva_cache_append(cache: Cache, table, length, k_new, v_new, new_ptr, max_new
     if k_new.stride(0) != v_new.stride(0) and shape[0] > 1:
         raise ValueError(f"{fn}: k_new and v_new have different token strides")
     stride = max(k_new.stride(0), c.Hkv * c.d) if shape[0] > 1 else c.Hkv * c.d
-    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), _ptr(k_new), _ptr(v_new), stride, _ptr(new_ptr),
-          int(max_new), _ptr(dev_status))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), k_new.data_ptr(), v_new.data_ptr(), stride,
+          new_ptr.data_ptr(), int(max_new), _status(fn, dev_status, dev))
 
 
 def fva_cache_route_workspace_bytes(cache, B, max_blocks, H):
@@ -534,8 +553,9 @@ def fva_cache_route(cache: Cache, table, length, q, p, k_floor, n_recent, kept, 
     H, q_stride = _query(fn, cache, sq.B, q)
     _expect(fn, "kept", kept, (sq.B, c.Hkv, sq.max_blocks), torch.int32, dev)
     _expect(fn, "n_kept", n_kept, (sq.B, c.Hkv), torch.int32, dev)
-    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, float(p), int(k_floor),
-          int(n_recent), float(scale), _ptr(kept), _ptr(n_kept), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
+    size, ws, status = _scratch(fn, workspace, dev_status, dev)
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), q.data_ptr(), H, q_stride, float(p), int(k_floor),
+          int(n_recent), float(scale), kept.data_ptr(), n_kept.data_ptr(), ws, size, status)
 
 
 def fva_cache_attn_workspace_bytes(cache, B, max_blocks, H, accumulate):
@@ -556,8 +576,9 @@ def fva_cache_attn(cache: Cache, table, length, q, kept, n_kept, o, workspace, l
     _expect(fn, "o", o, (sq.B, H, c.d), cache.k.dtype, dev)
     if lse is not None:
         _expect(fn, "lse", lse, (sq.B, H), torch.float32, dev)
-    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), _ptr(q), H, q_stride, _ptr(kept), _ptr(n_kept), _ptr(o),
-          _ptr(lse), float(scale), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
+    size, ws, status = _scratch(fn, workspace, dev_status, dev)
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), q.data_ptr(), H, q_stride, _ptr(kept), _ptr(n_kept),
+          o.data_ptr(), _ptr(lse), float(scale), int(bool(accumulate)), ws, size, status)
 
 
 def fva_cache_evict_workspace_bytes(cache, B, max_blocks):
@@ -573,8 +594,9 @@ def fva_cache_evict(cache: Cache, table, length, keep, n_sink, n_recent, dst_tab
     _expect(fn, "dst_table", dst_table, (sq.B, dst_table.shape[1]), torch.int32, dev)
     _expect(fn, "kept", kept, (sq.B, c.Hkv, int(keep)), torch.int32, dev)
     _expect(fn, "new_len", new_len, (sq.B,), torch.int32, dev)
-    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), int(keep), int(n_sink), int(n_recent), _ptr(dst_table),
-          dst_table.shape[1], _ptr(kept), _ptr(new_len), _ptr(workspace), _nbytes(workspace), _ptr(dev_status))
+    size, ws, status = _scratch(fn, workspace, dev_status, dev)
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(sq), int(keep), int(n_sink), int(n_recent), dst_table.data_ptr(),
+          dst_table.shape[1], kept.data_ptr(), new_len.data_ptr(), ws, size, status)
 
 
 def call_raw(name, *args):
