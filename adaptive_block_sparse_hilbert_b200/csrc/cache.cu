@@ -62,14 +62,15 @@ __device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D, kPage
 // tokens, 8 key heads, d = 128.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
-                                                              const T* __restrict__ v_new, int64_t token_stride,
+                                                              const T* __restrict__ v_new, int64_t n_tokens,
+                                                              int64_t token_stride,
                                                               const int32_t* __restrict__ new_ptr, int max_new,
                                                               int32_t* dev_status) {
   using P = PageRows<T, D, kAppendThreads>;
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = seq_len(c, b, dev_status);
-  const int from = new_ptr[b], n_new = new_ptr[b + 1] - from;
-  if (n_new <= 0 || n_new > max_new || n_new > len) {
+  const int from = new_ptr[b], to = new_ptr[b + 1], n_new = to - from;
+  if (n_new <= 0 || n_new > max_new || n_new > len || from < 0 || to > n_tokens) {
     if (n_new != 0 && threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
     return;
   }
@@ -801,7 +802,7 @@ struct AppendCall {
   const fva_cache* c;
   const fva_seqs* s;
   const void *k_new, *v_new;
-  int64_t stride;
+  int64_t n_tokens, stride;
   const int32_t* new_ptr;
   int max_new;
   int32_t* dev_status;
@@ -812,15 +813,16 @@ struct AppendCall {
     const dim3 grid(static_cast<unsigned>((max_new + kBlock - 2) / kBlock + 1), static_cast<unsigned>(c->Hkv),
                     static_cast<unsigned>(s->B));
     append_kernel<T, D><<<grid, kAppendThreads, 0, st>>>(cache_view<T>(c, s), static_cast<const T*>(k_new),
-                                                       static_cast<const T*>(v_new), stride, new_ptr, max_new, dev_status);
+                                                       static_cast<const T*>(v_new), n_tokens, stride, new_ptr, max_new,
+                                                       dev_status);
     return cudaGetLastError();
   }
 };
 
 cudaError_t launch_cache_append(const fva_cache* c, const fva_seqs* s, const void* k_new, const void* v_new,
-                                int64_t stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
-                                cudaStream_t st) {
-  return by_cache_type(c, AppendCall{c, s, k_new, v_new, stride, new_ptr, max_new, dev_status, st});
+                                int64_t n_tokens, int64_t stride, const int32_t* new_ptr, int max_new,
+                                int32_t* dev_status, cudaStream_t st) {
+  return by_cache_type(c, AppendCall{c, s, k_new, v_new, n_tokens, stride, new_ptr, max_new, dev_status, st});
 }
 
 struct RouteCall {

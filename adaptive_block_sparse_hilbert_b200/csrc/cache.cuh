@@ -66,7 +66,7 @@ inline cudaError_t by_cache_type(const fva_cache* c, const F& f) {
 }
 
 cudaError_t launch_cache_append(const fva_cache* c, const fva_seqs* q, const void* k_new, const void* v_new,
-                                int64_t token_stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
+                                int64_t n_tokens, int64_t token_stride, const int32_t* new_ptr, int max_new, int32_t* dev_status,
                                 cudaStream_t st);
 cudaError_t launch_cache_route(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride, double p,
                                int k_floor, int n_recent, double scale, int32_t* kept, int32_t* n_kept, double* scores,

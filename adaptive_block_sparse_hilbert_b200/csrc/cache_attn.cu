@@ -139,7 +139,7 @@ template <typename T, int D>
 __device__ __forceinline__ void put_stats(const AttnView<T>& a, bool whole, int share, int slot, int64_t row, int g,
                                           float mx, float sum) {
   if (whole) {
-    const float l2 = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
+    const float l2 = sum == 0.0f ? -INFINITY : mx + log2f(sum);
     if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
     if (a.ws.scores) a.ws.lse[row] = l2;
   } else {
@@ -482,10 +482,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       if (warp == 0 && r < ng) {
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sum += s_m[v][r] == -INFINITY ? 0.0f : s_l[v][r] * exp2f(s_m[v][r] - mx);
+        for (int v = 0; v < 4; ++v) sum += s_l[v][r] * (s_m[v][r] == -INFINITY ? 0.0f : exp2f(s_m[v][r] - mx));
         const int64_t row = row0 + r;
         if (whole) {
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           uint32_t* out = reinterpret_cast<uint32_t*>(a.o + row * D);
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) out[n * 4 + ct] = F::pack(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
           for (int k = 8; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
           const float m_new = fmaxf(m[g], mx);
           const float corr = m_new == -INFINITY ? 1.0f : exp2f(m[g] - m_new);
-          const float p = m_new == -INFINITY ? 0.0f : exp2f(s[g] - m_new);
+          const float p = exp2f(s[g] - (m_new == -INFINITY ? 0.0f : m_new));
           m[g] = m_new;
           l[g] = l[g] * corr + (part == 0 ? p : 0.0f);
 #pragma unroll
@@ -723,8 +723,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
         if (g >= ng) continue;
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sum += s_m[v][g] == -INFINITY ? 0.0f : s_l[v][g] * exp2f(s_m[v][g] - m[g]);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        for (int v = 0; v < 4; ++v) sum += s_l[v][g] * (s_m[v][g] == -INFINITY ? 0.0f : exp2f(s_m[v][g] - m[g]));
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         float* out = whole ? a.o + (row0 + g) * D
                            : a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + g) * (D + 2);
 #pragma unroll
@@ -822,15 +822,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
           for (int k = 0; k < 8; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = k0 + k < cnt && fk != 0.0f ? fmaf(fk, x[k][i], acc[i]) : acc[i];
+            for (int i = 0; i < V; ++i) acc[i] = k0 + k < cnt ? fmaf(fk, x[k][i], acc[i]) : acc[i];
           }
         }
       }
     }
-    const float l2 = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
+    // (a row without keys has a sum of 0; a NaN in its scores makes the sum one)
+    const float l2 = sum == 0.0f ? -INFINITY : mx + log2f(sum);
     if (joins) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) from_f32(sum > 0.0f ? acc[i] / sum : 0.0f, a.o + row * D + lane * V + i);
+      for (int i = 0; i < V; ++i) from_f32(sum == 0.0f ? 0.0f : acc[i] / sum, a.o + row * D + lane * V + i);
       if (lane == 0 && a.lse) a.lse[row] = l2 * 0.6931471805599453f;
     } else if (lane == 0) {
       s_lse[g] = l2;

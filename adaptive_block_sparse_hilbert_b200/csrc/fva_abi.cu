@@ -434,16 +434,16 @@ static int check_query(const fva_cache* c, const fva_seqs* q, const void* q_dev,
 }
 
 int fva_cache_append(const fva_cache* cache, const fva_seqs* seqs, const void* k_new_dev, const void* v_new_dev,
-                     int64_t token_stride, const int32_t* new_ptr_dev, int max_new, int32_t* dev_status,
-                     fva_stream_t stream) {
+                     int64_t n_tokens, int64_t token_stride, const int32_t* new_ptr_dev, int max_new,
+                     int32_t* dev_status, fva_stream_t stream) {
   const int rc = check_cache(cache, seqs);
   if (rc != FVA_OK) return rc;
-  if (!new_ptr_dev || max_new < 0 || max_new > kMaxCacheBlocks * kBlock) return FVA_ERR_INVALID_ARG;
+  if (!new_ptr_dev || n_tokens < 0 || max_new < 0 || max_new > kMaxCacheBlocks * kBlock) return FVA_ERR_INVALID_ARG;
   if (max_new == 0) return FVA_OK;
   if (!k_new_dev || !v_new_dev || token_stride < static_cast<int64_t>(cache->Hkv) * cache->d) return FVA_ERR_INVALID_ARG;
   if (!aligned16(k_new_dev) || !aligned16(v_new_dev) || token_stride * (cache->dtype == FVA_F32 ? 4 : 2) % 16 != 0)
     return FVA_ERR_ALIGNMENT;
-  return cuda_status(launch_cache_append(cache, seqs, k_new_dev, v_new_dev, token_stride, new_ptr_dev, max_new,
+  return cuda_status(launch_cache_append(cache, seqs, k_new_dev, v_new_dev, n_tokens, token_stride, new_ptr_dev, max_new,
                                          dev_status, stream));
 }
 

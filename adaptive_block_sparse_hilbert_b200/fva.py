@@ -120,7 +120,7 @@ def _load():
         "fva_sparse_attn_lse": (i32, [S, P, P, P, i32, M, P, P, flt, P, P]),
         "fva_sparse_attn_bwd_workspace_bytes": (sz, [S]),
         "fva_sparse_attn_bwd": (i32, [S, P, P, P, P, P, P, M, P, P, P, flt, P, sz, P, P]),
-        "fva_cache_append": (i32, [C, Q, P, P, i64, P, i32, P, P]),
+        "fva_cache_append": (i32, [C, Q, P, P, i64, i64, P, i32, P, P]),
         "fva_cache_route_workspace_bytes": (sz, [C, i32, i32, i32]),
         "fva_cache_route": (i32, [C, Q, P, i32, i64, dbl, i32, i32, flt, P, P, P, sz, P, P]),
         "fva_cache_attn_workspace_bytes": (sz, [C, i32, i32, i32, i32]),
@@ -530,8 +530,8 @@ def fva_cache_append(cache: Cache, table, length, k_new, v_new, new_ptr, max_new
     if k_new.stride(0) != v_new.stride(0) and shape[0] > 1:
         raise ValueError(f"{fn}: k_new and v_new have different token strides")
     stride = max(k_new.stride(0), c.Hkv * c.d) if shape[0] > 1 else c.Hkv * c.d
-    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), k_new.data_ptr(), v_new.data_ptr(), stride,
-          new_ptr.data_ptr(), int(max_new), _status(fn, dev_status, dev))
+    _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), k_new.data_ptr(), v_new.data_ptr(), shape[0],
+          stride, new_ptr.data_ptr(), int(max_new), _status(fn, dev_status, dev))
 
 
 def fva_cache_route_workspace_bytes(cache, B, max_blocks, H):

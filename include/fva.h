@@ -364,15 +364,17 @@ typedef struct fva_seqs {
  * sequence b, whose length AFTER the append is seqs->len[b]; the touched pages' key_mean (the
  * sum of the page's valid keys in float64, divided, rounded once) is rewritten, and the new
  * tokens' mass, if the cache has one, set to 0.
- *   k_new, v_new: rows [Hkv, d] of the cache's dtype, token_stride elements apart (>= Hkv*d;
- *     token_stride * element size a multiple of 16): slices of a fused projection's output fit;
- *   new_ptr_dev: int32 [B + 1], ascending from 0; max_new >= the largest count (a sequence with
- *     more, or with more than its length, sets FVA_DEVERR_BAD_LIST and is left unchanged).
+ *   k_new, v_new: n_tokens rows [Hkv, d] of the cache's dtype, token_stride elements apart
+ *     (>= Hkv*d; token_stride * element size a multiple of 16): slices of a fused projection's
+ *     output fit;
+ *   new_ptr_dev: int32 [B + 1], ascending from 0 to at most n_tokens; max_new >= the largest
+ *     count (a sequence with more, with more than its length, or with rows outside k_new sets
+ *     FVA_DEVERR_BAD_LIST and is left unchanged).
  * Two sequences of one call may not share a page that the call writes.
  */
 FVA_API int fva_cache_append(const fva_cache* cache, const fva_seqs* seqs, const void* k_new_dev,
-                             const void* v_new_dev, int64_t token_stride, const int32_t* new_ptr_dev, int max_new,
-                             int32_t* dev_status, fva_stream_t stream);
+                             const void* v_new_dev, int64_t n_tokens, int64_t token_stride,
+                             const int32_t* new_ptr_dev, int max_new, int32_t* dev_status, fva_stream_t stream);
 
 /*
  * Routing of single queries: Top-p with a Top-k floor, as fva_route does for query blocks, for

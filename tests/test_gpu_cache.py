@@ -205,6 +205,8 @@ def test_append_reports_and_skips():
     bad[1, 0], bad[3, 0] = s.cache.k.shape[0], -1
     assert go([70] * 4, bad) == [True, False, True, False]
     assert go([70] * 4, most=69) == [False] * 4
+    assert go([70] * 4, ptr=torch.tensor([0, 70, 140, 210, 281], dtype=torch.int32, device="cuda")) == [True] * 3 + [False]
+    assert go([70] * 4, ptr=torch.tensor([-1, 69, 140, 139, 200], dtype=torch.int32, device="cuda"))[0] is False
 
 
 # ------------------------------------------------------------------------------ routing
@@ -231,6 +233,17 @@ def test_route_many_blocks_and_wide_scores():
     kept, n = s.route(s.query(s.q), 0.7, 3000, 2)
     s.ok()
     s.check_route(kept, n, s.want_route(0.7, 3000, 2))
+
+
+def test_route_many_sequences_of_a_wide_table():
+    """More units than SMs and a table whose scores do not fit a shared SM's memory."""
+    lens = np.random.default_rng(2).integers(0, 700, 100).tolist()
+    lens[3] = 64 * 1100 - 3
+    s = Streams(lens, 8, 2, 64, "bf16", max_blocks=1200, scale_k=3.0).fill()
+    q = s.query()
+    kept, n = s.route(q, 0.8, 3, 1)
+    s.ok()
+    s.check_route(kept, n, s.want_route(0.8, 3, 1))
 
 
 def test_route_ties_take_the_lowest_blocks():
@@ -288,7 +301,7 @@ def test_attention(dtype, d, Hkv, G, every):
     assert s.torch.equal(o, o2) and s.torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("B,Hkv,G", [(300, 4, 2), (1, 1, 8), (2000, 1, 1)])
+@pytest.mark.parametrize("B,Hkv,G", [(300, 4, 2), (1, 1, 8), (2000, 1, 1), (3, 1, 128)])
 def test_attention_many_and_few_units(B, Hkv, G):
     """More sequences than CTAs and a single long one: shares that hold many units, units that
     cross many shares."""
@@ -300,6 +313,46 @@ def test_attention_many_and_few_units(B, Hkv, G):
     o, lse = s.attn(q, None, None, accumulate=True)
     s.ok()
     s.check_attn(o, lse, [[np.arange(-(-m // 64))] * Hkv for m in s.lens], before)
+
+
+def test_attention_of_empty_streams():
+    s = Streams([0, 0, 0], 4, 2, 128, "bf16", spare=1)
+    q = s.query()
+    kept, n = s.route(q, 0.5, 3, 2)
+    assert not n.any() and bool((kept == -1).all())
+    o, lse = s.attn(q, kept, n, accumulate=True)
+    s.ok()
+    assert not o.any() and bool(lse.isneginf().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_attention_nan_stays_in_its_head(dtype):
+    """A NaN in one query head makes that head's output and log-sum-exp NaN, over one share and
+    over many, and leaves its neighbours alone."""
+    for length in (100, 30000):
+        s = Streams([length, 300], 4, 2, 64, dtype).fill()
+        s.query()
+        clean = s.attn(s.dev(s.q), None, None)
+        s.q[0, 1, 5] = np.nan
+        o, lse = s.attn(s.dev(s.q), None, None)
+        s.ok()
+        assert bool(o[0, 1].isnan().all()) and bool(lse[0, 1].isnan())
+        rest = [(0, 0), (0, 2), (0, 3), (1, 0), (1, 1), (1, 2), (1, 3)]
+        assert all(s.torch.equal(o[i], clean[0][i]) and s.torch.equal(lse[i], clean[1][i]) for i in rest)
+
+
+def test_attention_without_masses():
+    s = Streams([500, 20], 4, 2, 64, "bf16").fill()
+    c = s.cache
+    s.cache = s.fva.Cache(c.k, c.v, c.key_mean)
+    q = s.query()
+    o, lse = s.attn(q, None, None)
+    s.ok()
+    s.cache = c
+    s.check_attn(o, lse, [[np.arange(8)] * 2, [np.arange(1)] * 2])
+    s.cache = s.fva.Cache(c.k, c.v, c.key_mean)
+    with pytest.raises(s.fva.FvaError):
+        s.attn(q, None, None, accumulate=True)
 
 
 def test_attention_large_scores():
@@ -435,6 +488,17 @@ def test_evict_long_stream():
     _evict(s, 12345, 4, 1000)
 
 
+@pytest.mark.parametrize("lens,max_blocks", [([40001] + [70] * 79, None), ([5000, 64, 3], 16384)])
+def test_evict_many_units_and_wide_tables(lens, max_blocks):
+    """A long stream in one CTA (more units than SMs), and tokens that are read again in every
+    pass (a table too wide for shared memory)."""
+    keep = 1234
+    s = Streams(lens, 1, 1, 64, "bf16", max_blocks=max_blocks, spare=len(lens) * -(-keep // 64)).fill()
+    s.cache.mass.uniform_(0, 1)
+    s.cache.mass *= (s.cache.mass > 0.4)
+    _evict(s, keep, 4, 100)
+
+
 def test_evict_reports_destinations_that_cannot_be():
     """A destination that is a source page of its sequence, or no page, is reported and not
     written; nothing else than the good destinations changes."""
@@ -467,6 +531,11 @@ def test_binding_refuses_mismatched_tensors():
         s.attn(q, kept[:, :, :1], n)
     with pytest.raises(ValueError):
         s.attn(q.cpu(), kept, n)
+    with pytest.raises(ValueError):
+        s.fva.fva_cache_attn(s.cache, s.table, s.length, q, kept, n, torch.empty_like(q), torch.empty(1 << 24, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        s.fva.fva_cache_attn(s.cache, s.table, s.length, q, kept, n, torch.empty_like(q), s.ws(1 << 24),
+                             dev_status=torch.zeros(1, dtype=torch.int32))
     with pytest.raises(s.fva.FvaError):
         s.fva.fva_cache_attn(s.cache, s.table, s.length, q, kept, None, torch.empty_like(q), s.ws(1 << 24))
     with pytest.raises(ValueError):

@@ -63,8 +63,8 @@ def _seqs(B=2, max_blocks=8, table=4096, length=8192):
 BIG = 1 << 50
 
 
-def _append(c=None, s=None, k=256, v=512, stride=512, ptr=64, most=10):
-    return fva.call_raw("fva_cache_append", ctypes.byref(c or _cache()), ctypes.byref(s or _seqs()), P(k), P(v), stride,
+def _append(c=None, s=None, k=256, v=512, tokens=20, stride=512, ptr=64, most=10):
+    return fva.call_raw("fva_cache_append", ctypes.byref(c or _cache()), ctypes.byref(s or _seqs()), P(k), P(v), tokens, stride,
                         P(ptr), most, None, None)
 
 
@@ -102,7 +102,7 @@ def test_append_refusals():
     assert _append(stride=511) == fva.FVA_ERR_INVALID_ARG    # narrower than a token's heads
     assert _append(stride=516) == fva.FVA_ERR_ALIGNMENT
     assert _append(k=260) == fva.FVA_ERR_ALIGNMENT
-    assert _append(most=-1) == fva.FVA_ERR_INVALID_ARG
+    assert _append(most=-1) == _append(tokens=-1) == fva.FVA_ERR_INVALID_ARG
     assert _append(most=0) == fva.FVA_OK                     # nothing to append
 
 
@@ -110,6 +110,7 @@ def test_append_refusals():
 def test_query_refusals(call):
     assert call(q=None) == fva.FVA_ERR_INVALID_ARG
     assert call(H=6) == call(H=0) == call(H=65536 * 4) == fva.FVA_ERR_UNSUPPORTED_SHAPE
+    assert call(H=516, stride=516 * 128) == fva.FVA_ERR_UNSUPPORTED_SHAPE  # 129 query heads per key head
     assert call(stride=1023) == fva.FVA_ERR_INVALID_ARG
     assert call(stride=1028) == fva.FVA_ERR_ALIGNMENT
     assert call(q=264) == fva.FVA_ERR_ALIGNMENT
