@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(512) order_kernel(const int32_t* __restrict__ 
 // ---------------------------------------------------------------------------------
 // CUDA-core gradient
 // ---------------------------------------------------------------------------------
-// A cluster of two CTAs owns 32 rows (half a block) and takes the blocks of its list in turn, so
-// that a small layer has CTAs for every SM and its longest list is halved; the second CTA's sums
-// are added to the first's at the end. Blocks stream through two shared-memory buffers.
+// A cluster of four CTAs owns 32 rows (half a block) and takes the blocks of its list in turn, so
+// that a small layer has CTAs for every SM and its longest list is a quarter as long; their sums
+// are added in the first's order at the end. Blocks stream through two shared-memory buffers.
 //   KV = false: owns query rows (a0 = Q, a1 = dO), streams K and V:  out0 = dQ = scale dS K
 //   KV = true:  owns key rows   (a0 = K, a1 = V), streams Q and dO:  out0 = dK = scale dS^T Q,
 //                                                                     out1 = dV = P^T dO
@@ -186,7 +186,7 @@ struct F32Args {
   const float *q, *k, *v, *d_o, *stats;
   float *dq, *dk, *dv;
 };
-constexpr int kF32Rows = 32;
+constexpr int kF32Rows = 32, kF32Split = 4;
 
 template <int D>
 struct F32Cfg {
@@ -230,7 +230,7 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   auto load_stats = [&](float* dst, int blk) {
     if (tid < 32) copy16(dst + 4 * tid, x.stats + (bh * nB + blk) * 128 + 4 * tid, true);
   };
-  int nth = 0;  // kept entries so far: this CTA takes those of its parity
+  int nth = 0;  // kept entries so far: this CTA takes every fourth
   auto next_of = [&](int e) {
     for (; e < n_list; ++e) {
       const int entry = list[e];
@@ -239,7 +239,7 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
         if (tid == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
         continue;
       }
-      if ((nth++ & 1) == rank) break;
+      if (nth++ % kF32Split == rank) break;
     }
     return e;
   };
@@ -280,7 +280,7 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) u[i][j] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < D; c += 4) {
       float4 a[4];
 #pragma unroll
@@ -317,7 +317,7 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     const float* px = (KV && group == 0 ? sP : sDS) + tr * LP;
     const float* pw = KV && group == 0 ? sB1 : sB0;
     const int s0 = KV ? 0 : group * (kBlock / 2), s1 = KV ? kBlock : s0 + kBlock / 2;
-#pragma unroll 2
+#pragma unroll 4
     for (int s = s0; s < s1; s += 4) {
       float4 d[4];
 #pragma unroll
@@ -344,32 +344,37 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  // the sums of the second CTA, and for dQ of the second group, go through the first's buffers
-  // [2][32][D]: KV: dV and dK of rank 1; else dQ of the groups
+  // the other CTAs' sums, and for dQ every CTA's second group's, through the stream's buffers as
+  // [2][32][D]: KV: dV and dK; else dQ of the groups
   float* sum = sB + group * kF32Rows * D;
   auto slot = [&](int i, int j) { return (tr + 8 * i) * D + ((j / kW) * 16 + tc) * kW + j % kW; };
-  if (rank == 1 || (!KV && group == 1)) {
-    float* to = sum;
+  if (rank > 0 || (!KV && group == 1)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < NC; ++j) to[slot(i, j)] = acc[i][j];
+      for (int j = 0; j < NC; ++j) sum[slot(i, j)] = acc[i][j];
   }
   cluster.sync();
-  if (rank == 0) {
-    const float* far = cluster.map_shared_rank(sB, 1);
+  if (rank == 0 && (KV || group == 0)) {
+    const float* far[kF32Split];
+#pragma unroll
+    for (int r = 0; r < kF32Split; ++r) far[r] = cluster.map_shared_rank(sB, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = r0 + tr + 8 * i;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int at = slot(i, j);
-        if (KV) {
-          const float v = acc[i][j] + far[group * kF32Rows * D + at];
-          if (n < N) (group == 0 ? x.dv : x.dk)[(base + r0) * D + at] = group == 0 ? v : v * scale;
-        } else if (group == 0) {
-          const float v = (acc[i][j] + sB[kF32Rows * D + at]) + (far[at] + far[kF32Rows * D + at]);
-          if (n < N) x.dq[(base + r0) * D + at] = v * scale;
+        float v = acc[i][j];
+        if (!KV) v += sB[kF32Rows * D + at];
+#pragma unroll
+        for (int r = 1; r < kF32Split; ++r)
+          v += KV ? far[r][group * kF32Rows * D + at] : far[r][at] + far[r][kF32Rows * D + at];
+        if (n < N) {
+          const int64_t to = (base + r0) * D + at;
+          if (!KV) x.dq[to] = v * scale;
+          else if (group == 0) x.dv[to] = v;
+          else x.dk[to] = v * scale;
         }
       }
     }
@@ -377,16 +382,16 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   cluster.sync();  // nobody leaves while its buffers are read
 }
 
-// CTAs of a head: pairs for the key rows, then pairs for the query rows.
+// Clusters of a head: those of the key rows, then those of the query rows.
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_bwd_f32_kernel(F32Args x, const int32_t* __restrict__ tile_ptr, const int32_t* __restrict__ tile_col,
                         BwdLists lists, int N, int nB, int nPairs, int owners, float scale, int32_t* dev_status) {
   extern __shared__ __align__(16) float smem_bwd[];
   grid_wait();
-  const int pair = static_cast<int>(blockIdx.x) / 2;
-  const bool kv = pair < owners;
-  const int own = pair - (kv ? 0 : owners);
+  const int at_x = static_cast<int>(blockIdx.x) / kF32Split;
+  const bool kv = at_x < owners;
+  const int own = at_x - (kv ? 0 : owners);
   const int64_t bh = blockIdx.y, tile = bh * nPairs + own / (2 * kBlock / kF32Rows);
   if (kv) {
     bwd_f32<D, true>(x, bh, own, lists.col + tile * nB, lists.cost[tile], N, nB, scale, smem_bwd, dev_status);
@@ -406,8 +411,8 @@ static cudaError_t launch_f32(const Dims& Dm, const BwdArgs& x, const fva_mask* 
                      static_cast<const float*>(x.d_o), ws.stats,                       static_cast<float*>(x.dq),
                      static_cast<float*>(x.dk),        static_cast<float*>(x.dv)};
   const int owners = static_cast<int>((Dm.N + kF32Rows - 1) / kF32Rows);
-  return launch_chained(attn_bwd_f32_kernel<D>, dim3(static_cast<unsigned>(4 * owners), static_cast<unsigned>(Dm.BH)), 256,
-                        2, F32Cfg<D>::kSmem, st, a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N),
+  return launch_chained(attn_bwd_f32_kernel<D>, dim3(static_cast<unsigned>(2 * kF32Split * owners), static_cast<unsigned>(Dm.BH)),
+                        256, kF32Split, F32Cfg<D>::kSmem, st, a, m->tile_ptr, m->tile_col, ws.lists, static_cast<int>(Dm.N),
                         static_cast<int>(Dm.nB), static_cast<int>(Dm.nPairs), owners, x.scale, dev_status);
 }
 
