@@ -61,7 +61,11 @@ class SparseAttentionLayer:
             self.vb = torch.empty(bhnd, dtype=dt, device=device) if self.v_fp16 else self.vh
             self.lse = torch.empty(bhnd[:3], dtype=torch.float32, device=device)
             self.doh, self.dqh, self.dkh, self.dvh = (torch.empty(bhnd, dtype=dt, device=device) for _ in range(4))
-            self.bwd_workspace = torch.empty(fva.fva_sparse_attn_bwd_workspace_bytes(s), dtype=torch.uint8, device=device)
+            size = fva.fva_sparse_attn_bwd_workspace_bytes(s)
+            if size == 0:
+                raise ValueError("SparseAttentionLayer: the gradient does not take this shape")
+            self.bwd_workspace = torch.empty(size, dtype=torch.uint8, device=device)
+            self.scale = None  # of the last attend(): the gradient's
         fva.fva_curve_perm(s, self.curve, self.perm, self.inv, self.dev_status)
 
     def reorder_inputs(self, q, k, v, stream=None):
@@ -78,9 +82,9 @@ class SparseAttentionLayer:
 
     def attend(self, stream=None, scale: float = 0.0):
         if self.train:
-            self.scale = scale
             fva.fva_sparse_attn_lse(self.shape, self.qh, self.kh, self.vh, self.mask, self.oh, self.lse, scale,
                                     self.dev_status, stream)
+            self.scale = scale
             return
         fva.fva_sparse_attn(self.shape, self.qh, self.kh, self.vh, self.mask, self.oh, scale, self.dev_status, stream)
 
@@ -99,6 +103,8 @@ class SparseAttentionLayer:
         [B, N, H, d] in raster order. The routed mask is a constant of the gradient."""
         if not self.train:
             raise RuntimeError("SparseAttentionLayer.backward: the layer was made without train=True")
+        if self.scale is None:
+            raise RuntimeError("SparseAttentionLayer.backward: no forward() to take the gradient of")
         s = self.shape
         fva.fva_reorder(s, do, self.doh, None, self.perm, fva.FVA_FWD, stream)
         fva.fva_sparse_attn_bwd(s, self.qh, self.kh, self.vb, self.oh, self.doh, self.lse, self.mask, self.dqh, self.dkh,
@@ -142,12 +148,14 @@ class CachedAttention:
         self.pages = [[] for _ in range(B)]   # host copies of the table's rows and the lengths
         self.lengths = [0] * B
 
-    def _publish(self, stream):
-        rows = torch.zeros((self.B, self.max_blocks), dtype=torch.int32)
-        for b, pages in enumerate(self.pages):
-            rows[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
+    def _publish(self, changed, stream):
+        """The lengths, and the table's rows of the streams in `changed`, to the device."""
         with torch.cuda.device(self.table.device), torch.cuda.stream(stream):
-            self.table.copy_(rows)
+            if changed:
+                rows = torch.zeros((len(changed), self.max_blocks), dtype=torch.int32)
+                for i, b in enumerate(changed):
+                    rows[i, :len(self.pages[b])] = torch.tensor(self.pages[b], dtype=torch.int32)
+                self.table[torch.tensor(changed, device=self.table.device)] = rows.to(self.table.device)
             self.length.copy_(torch.tensor(self.lengths, dtype=torch.int32))
 
     def _stream(self, stream):
@@ -164,15 +172,23 @@ class CachedAttention:
             raise ValueError("CachedAttention.append: a stream would outgrow max_blocks")
         if sum(need) > len(self.free):
             raise RuntimeError(f"CachedAttention.append: {sum(need)} pages needed, {len(self.free)} free")
+        grown = [b for b in range(self.B) if need[b]]
         for b, n in enumerate(need):
             self.pages[b] += [self.free.pop() for _ in range(n)]
             self.lengths[b] += counts[b]
-        self._publish(st)
+        self._publish(grown, st)
         ptr = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
-        with torch.cuda.device(self.table.device), torch.cuda.stream(st):
-            new_ptr = ptr.to(self.table.device)
-            fva.fva_cache_append(self.cache, self.table, self.length, k_new, v_new, new_ptr, max(counts), self.dev_status,
-                                 st)
+        try:
+            with torch.cuda.device(self.table.device), torch.cuda.stream(st):
+                new_ptr = ptr.to(self.table.device)
+                fva.fva_cache_append(self.cache, self.table, self.length, k_new, v_new, new_ptr, max(counts),
+                                     self.dev_status, st)
+        except (ValueError, fva.FvaError):  # refused: nothing ran
+            for b, n in reversed(list(enumerate(need))):
+                self.free += [self.pages[b].pop() for _ in range(n)]
+                self.lengths[b] -= counts[b]
+            self._publish([], st)
+            raise
 
     def attend(self, q, o, stream=None, scale: float = 0.0):
         """o [B, H, d] = attention of the query tokens q [B, H, d]; the choice is left in
@@ -187,6 +203,9 @@ class CachedAttention:
         """Cut every stream to at most `keep` tokens; returns the kept tokens' old positions
         (int32 [B, Hkv, keep], -1 behind them). Their old pages are free afterwards."""
         st = self._stream(stream)
+        if not 1 <= keep <= 1 << 20 or min(n_sink, n_recent) < 0 or n_sink + n_recent > keep:
+            raise ValueError(f"CachedAttention.evict: keep {keep}, first {n_sink}, last {n_recent}: expected 1 <= keep <= "
+                             f"2^20 and both ends within it")
         room = -(-int(keep) // fva.BLOCK)
         after = [min(n, int(keep)) for n in self.lengths]
         need = [-(-n // fva.BLOCK) for n in after]
@@ -205,7 +224,7 @@ class CachedAttention:
         for b, pages in enumerate(fresh):
             self.free += self.pages[b][::-1]
             self.pages[b], self.lengths[b] = pages, after[b]
-        self._publish(st)
+        self._publish(list(range(self.B)), st)
         return kept
 
 
