@@ -277,14 +277,14 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
       *abort_flag = 1;
     }
     __syncwarp();
-    if (*abort_flag) {  // wait (bounded) for the last load into every stage
-      volatile int never = 0;
-      if (Cfg::kOwnSmem && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
-      for (int j = n0 > Cfg::kS0 ? n0 - Cfg::kS0 : 0; j < n0; ++j)
-        mbar_wait(&bar.full0[j % Cfg::kS0], (j / Cfg::kS0) & 1, &never, 100000000ull);
-      for (int j = n1 > Cfg::kS1 ? n1 - Cfg::kS1 : 0; j < n1; ++j)
-        mbar_wait(&bar.full1[j % Cfg::kS1], (j / Cfg::kS1) & 1, &never, 100000000ull);
-    }
+    // wait (bounded) for the last load into every stage: whichever warp gives up, no load
+    // outlives the CTA
+    volatile int never = 0;
+    if (Cfg::kOwnSmem && !withhold && n_iter > 0) mbar_wait(&bar.own_full, 0, &never, 100000000ull);
+    for (int j = n0 > Cfg::kS0 ? n0 - Cfg::kS0 : 0; j < n0; ++j)
+      mbar_wait(&bar.full0[j % Cfg::kS0], (j / Cfg::kS0) & 1, &never, 100000000ull);
+    for (int j = n1 > Cfg::kS1 ? n1 - Cfg::kS1 : 0; j < n1; ++j)
+      mbar_wait(&bar.full1[j % Cfg::kS1], (j / Cfg::kS1) & 1, &never, 100000000ull);
   } else if (warp >= 17) {
     // ------------------------------------------------------------------ products
     // An elected lane, not `lane == 0`: the compiler keeps the descriptors in uniform registers
@@ -314,7 +314,6 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
           mma_ts(tmem + out_col, tmem + x_col + (kk >> 1) * 32 + (kk & 1) * 8,
                  sdesc_sw128(b_base + kk * 2048, 64 * 128, 1024), idesc_second, add || kk > 0);
       };
-      bool issued = false;
       bool ok = Cfg::kOwnSmem ? mbar_wait(&bar.own_full, 0, abort_flag, wait_limit_ns) : true;
       if (warp == 17) {
         RingPos<Cfg::kSBufs> buf;
@@ -326,7 +325,6 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
           tc_fence_after();
           first(Cfg::kSCol + buf.i * 64, Cfg::kOwn0Col, smem_u32(s_own), smem_u32(s_ring0) + r.i * Cfg::kTile);
           tc_commit(&bar.s_full[buf.i]);
-          issued = true;
           buf.next();
           r.next();
         }
@@ -344,7 +342,6 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
                   smem_u32(s_ring1) + r1.i * Cfg::kTile);
             tc_commit(&bar.dp_full[db.i]);
             if (!KV) tc_commit(&bar.empty1[r1.i]);
-            issued = true;
             db.next();
             r1.next();
           }
@@ -367,11 +364,6 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
       if (!ok) {
         report(dev_status, FVA_DEVERR_TIMEOUT);
         *abort_flag = 1;
-        if (issued) {
-          volatile int never = 0;
-          tc_commit(&bar.drain[warp - 17]);
-          mbar_wait(&bar.drain[warp - 17], 0, &never, 100000000ull);
-        }
       }
     }
   } else {
@@ -517,6 +509,14 @@ __device__ __forceinline__ void bwd_tile(const BwdTcArgs& x, const CUtensorMap& 
 
   tc_fence_before();
   __syncthreads();
+  if (bar.abort) {  // products may be in flight that nobody waited for
+    if (warp >= 17 && n_iter > 0 && elect_one()) {
+      volatile int never = 0;
+      tc_commit(&bar.drain[warp - 17]);
+      mbar_wait(&bar.drain[warp - 17], 0, &never, 100000000ull);
+    }
+    __syncthreads();
+  }
   if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, kBwdTmemCols);

@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(CacheView<T> c, 
   const int b = blockIdx.z, h = blockIdx.y;
   const int len = seq_len(c, b, dev_status);
   const int from = new_ptr[b], to = new_ptr[b + 1], n_new = to - from;
-  if (n_new <= 0 || n_new > max_new || n_new > len || from < 0 || to > n_tokens) {
-    if (n_new != 0 && threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
+  if (from < 0 || to <= from || to > n_tokens || n_new > max_new || n_new > len) {
+    if (to != from && threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
     return;
   }
   const int first = len - n_new;  // position of the first new token

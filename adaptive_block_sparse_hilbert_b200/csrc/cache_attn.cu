@@ -149,13 +149,19 @@ __device__ __forceinline__ void put_stats(const AttnView<T>& a, bool whole, int 
   }
 }
 
+struct SplitWaits {
+  uint64_t limit_ns;
+  uint32_t diag_flags;
+};
+
 // The loading warp of a split kernel: walks its share's lists and the page table 32 entries at
 // a time and has `load(stage, page, head)` request the pages, as the ring's stages come free.
 // `valid` of a stage: its keys that count, 0 for a page that is skipped.
 template <typename T, typename Load>
 __device__ __forceinline__ void feed_pages(const AttnView<T>& a, Walk<T>& w, uint64_t* full, uint64_t* empty, int* valid_of,
-                                           volatile int* abort_flag, uint64_t wait_limit_ns, int stages,
+                                           volatile int* abort_flag, const SplitWaits& waits, int stages,
                                            const Load& load) {
+  if (waits.diag_flags & FVA_DIAG_WITHHOLD_Q) return;  // nothing ever arrives: the waits run out
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   int stage = 0, phase = 0, issued = 0;
@@ -172,7 +178,7 @@ __device__ __forceinline__ void feed_pages(const AttnView<T>& a, Walk<T>& w, uin
       }
       for (int k = 0; k < cnt; ++k) {
         const int pg = __shfl_sync(0xffffffffu, page, k), va = __shfl_sync(0xffffffffu, valid, k);
-        if (!warp_wait_spin(&empty[stage], phase ^ 1, abort_flag, wait_limit_ns)) {
+        if (!warp_wait_spin(&empty[stage], phase ^ 1, abort_flag, waits.limit_ns)) {
           ok = false;
           break;
         }
@@ -272,7 +278,7 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, AttnView<T> a,
-                 uint64_t wait_limit_ns) {
+                 SplitWaits waits) {
   using Cfg = SplitCfg<D>;
   using F = Frag<T>;
   extern __shared__ uint8_t smem_raw[];
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   Walk<T> w(sh, share);
   volatile int* abort_flag = &s_abort;
   if (warp == 4) {
-    feed_pages(a, w, full, empty, s_valid, abort_flag, wait_limit_ns, Cfg::kStages, [&](int stage, int page, int h) {
+    feed_pages(a, w, full, empty, s_valid, abort_flag, waits, Cfg::kStages, [&](int stage, int page, int h) {
       uint8_t* dst = ring + stage * 2 * Cfg::kTile;
       mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTile);
 #pragma unroll
@@ -309,11 +315,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
 
   // -------------------------------------------------------------------- products and softmax
+  // A warp whose wait runs out takes no further data but goes through its units' joins: the
+  // four warps meet at barriers there.
   bool ok = true;
   int stage = 0, phase = 0;
   const int rg = lane >> 2, ct = lane & 3;  // fragment rows rg, rg + 8; columns 2 ct, 2 ct + 1
   const int lm = lane >> 3, lr = lane & 7;  // ldmatrix: matrix and row of this lane's address
-  while (ok && w.next(a)) {
+  while (w.next(a)) {
     const int bh = w.u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
     const int g0 = (w.u - bh * a.GS) * kGroup, ng = min(a.G - g0, kGroup);
     const int64_t row0 = static_cast<int64_t>(b) * a.H + h * a.G + g0;
@@ -338,8 +346,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int64_t stop = w.stop();
     const int first_pos = static_cast<int>(w.at - w.start), n_pos = static_cast<int>(stop - w.at);
     for (int j = 0; j < n_pos; ++j) {
-      if (!warp_wait_spin(&full[stage], phase, abort_flag, wait_limit_ns)) {
-        ok = false;
+      ok = ok && warp_wait_spin(&full[stage], phase, abort_flag, waits.limit_ns);
+      if (!ok) {
+        *abort_flag = 1;
         break;
       }
       const int nk = s_valid[stage] - warp * 16;  // this warp's keys that count
@@ -438,7 +447,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         phase ^= 1;
       }
     }
-    if (!ok) break;
     // ---- join the four warps: 2 and 3 hand over to 0 and 1, then 1 to 0, eight rows at a time
     auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
 #pragma unroll
@@ -501,10 +509,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     if (tid == 0) a.ws.start[w.u] = w.start;
     w.at = stop;
   }
-  if (!ok) {
-    report(a.dev_status, FVA_DEVERR_TIMEOUT);
-    *abort_flag = 1;
-  }
+  if (!ok) report(a.dev_status, FVA_DEVERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------------
@@ -543,7 +548,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&x)[V]) {
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float> a, uint64_t wait_limit_ns) {
+__global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float> a, SplitWaits waits) {
   using Cfg = SplitF32Cfg<D>;
   constexpr int V = D / 32, kHalf = D / 8;  // kHalf: 16-byte pieces of half a row
   extern __shared__ uint8_t smem_raw[];
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
   Walk<float> w(sh, share);
   volatile int* abort_flag = &s_abort;
   if (warp == 4) {
-    feed_pages(a, w, full, empty, s_valid, abort_flag, wait_limit_ns, Cfg::kStages, [&](int stage, int page, int h) {
+    feed_pages(a, w, full, empty, s_valid, abort_flag, waits, Cfg::kStages, [&](int stage, int page, int h) {
       const int64_t at = (static_cast<int64_t>(page) * a.c.Hkv + h) * kBlock * D;
       mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTile);
       bulk_load(ring + stage * 2 * Cfg::kTile, a.c.k + at, Cfg::kTile, &full[stage]);
@@ -578,11 +583,11 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
     return;
   }
 
-  bool ok = true;
+  bool ok = true;  // (a warp whose wait runs out still meets the others at the joins' barriers)
   int stage = 0, phase = 0;
   const int key = lane & 15, part = lane >> 4;
   auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-  while (ok && w.next(a)) {
+  while (w.next(a)) {
     const int bh = w.u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
     const int g0 = (w.u - bh * a.GS) * kGroup, ng = min(a.G - g0, kGroup);
     const int64_t row0 = static_cast<int64_t>(b) * a.H + h * a.G + g0;
@@ -600,8 +605,9 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
     const int64_t stop = w.stop();
     const int first_pos = static_cast<int>(w.at - w.start), n_pos = static_cast<int>(stop - w.at);
     for (int j = 0; j < n_pos; ++j) {
-      if (!warp_wait_spin(&full[stage], phase, abort_flag, wait_limit_ns)) {
-        ok = false;
+      ok = ok && warp_wait_spin(&full[stage], phase, abort_flag, waits.limit_ns);
+      if (!ok) {
+        *abort_flag = 1;
         break;
       }
       const int nk = min(s_valid[stage] - warp * 16, 16);  // this warp's keys that count
@@ -676,7 +682,6 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
         phase ^= 1;
       }
     }
-    if (!ok) break;
     // ---- join the four warps: 2 and 3 hand over to 0 and 1, then 1 to 0
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -736,10 +741,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
     sync4();  // the next unit rewrites what was read here
     w.at = stop;
   }
-  if (!ok) {
-    report(a.dev_status, FVA_DEVERR_TIMEOUT);
-    *abort_flag = 1;
-  }
+  if (!ok) report(a.dev_status, FVA_DEVERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------------
@@ -777,13 +779,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
     }
   };
   if (!joins) find_pages(first);
+  // A head without a finite score weighs nothing: exp2(-inf - inf) is 0, -inf - -inf is NaN.
+  auto weightless = [](float l2) { return l2 == -INFINITY ? INFINITY : l2; };
   const int64_t per = n ? *a.ws.per : 1;
   for (int g = warp; g < a.G; g += kJoinThreads / 32) {
     const int64_t row = static_cast<int64_t>(b) * a.H + h * a.G + g;
     const int64_t start = n ? a.ws.start[bh * a.GS + g / kGroup] : 0;
     const int c0 = static_cast<int>(start / per), c1 = n ? static_cast<int>((start + n - 1) / per) : c0;
+    if (c0 < 0 || c1 < c0 || c1 >= kShares) continue;  // (never: whatever the workspace holds, no access leaves it)
     if (n && c0 == c1) {  // finished by the split kernel
-      if (!joins && lane == 0) s_lse[g] = a.ws.lse[row];
+      if (!joins && lane == 0) s_lse[g] = weightless(a.ws.lse[row]);
       continue;
     }
     constexpr int V = D / 32;
@@ -834,7 +839,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
       for (int i = 0; i < V; ++i) from_f32(sum == 0.0f ? 0.0f : acc[i] / sum, a.o + row * D + lane * V + i);
       if (lane == 0 && a.lse) a.lse[row] = l2 * 0.6931471805599453f;
     } else if (lane == 0) {
-      s_lse[g] = l2;
+      s_lse[g] = weightless(l2);
     }
   }
   if (joins) return;
@@ -885,7 +890,7 @@ static cudaError_t launch_f32(const AttnView<float>& a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(split_f32_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   if (e != cudaSuccess) return e;
   return launch_chained(split_f32_kernel<D, G>, dim3(Cfg::kUseShares), kSplitThreads, 0, Cfg::kSmem, st, a,
-                        attn_wait_limit_ns());
+                        SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
 }
 
 template <typename T, int D>
@@ -897,7 +902,7 @@ static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaSt
                                                SplitCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     return launch_chained(split_kernel<T, D>, dim3(kShares), kSplitThreads, 0, SplitCfg<D>::kSmem, st, mk, mv, a,
-                          attn_wait_limit_ns());
+                          SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
   } else {
     const int g = a.G < kGroup ? a.G : kGroup;
     return g <= 1   ? launch_f32<D, 1>(a, st)

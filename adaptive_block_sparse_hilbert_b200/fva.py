@@ -438,7 +438,10 @@ def _shape_dtype(s):
     return torch.bfloat16 if s.dtype == FVA_BF16 else torch.float32
 
 
-def _mask_on(fn, mask, device):
+def _mask_on(fn, s, N, mask, device):
+    nB = -(-N // BLOCK)
+    if mask.row_ptr.numel() <= s.B * s.H * nB or mask.worklist.numel() < s.B * s.H * ((nB + 1) // 2):
+        raise ValueError(f"{fn}: the mask is one of another shape")
     if mask.row_ptr.device != device or mask.tile_col.device != device or mask.worklist.device != device:
         raise ValueError(f"{fn}: the mask is on {mask.row_ptr.device}, expected {device}")
 
@@ -451,7 +454,7 @@ def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=No
         _expect(fn, what, t, four, _shape_dtype(s), dev)
     _expect(fn, "v", v, four, v.dtype if v.dtype in (torch.float16, torch.bfloat16) else _shape_dtype(s), dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _mask_on(fn, mask, dev)
+    _mask_on(fn, s, N, mask, dev)
     _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(v),
           ctypes.byref(mask.c()), o.data_ptr(), lse.data_ptr(), float(scale), _status(fn, dev_status, dev))
 
@@ -468,7 +471,7 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
     for what, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
         _expect(fn, what, t, four, dt, dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _mask_on(fn, mask, dev)
+    _mask_on(fn, s, N, mask, dev)
     size, ws, status = _scratch(fn, workspace, dev_status, dev)
     _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
           lse.data_ptr(), ctypes.byref(mask.c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), float(scale), ws, size,
@@ -529,7 +532,7 @@ def fva_cache_append(cache: Cache, table, length, k_new, v_new, new_ptr, max_new
     _expect(fn, "new_ptr", new_ptr, (q.B + 1,), torch.int32, dev)
     if k_new.stride(0) != v_new.stride(0) and shape[0] > 1:
         raise ValueError(f"{fn}: k_new and v_new have different token strides")
-    stride = max(k_new.stride(0), c.Hkv * c.d) if shape[0] > 1 else c.Hkv * c.d
+    stride = k_new.stride(0) if shape[0] > 1 else c.Hkv * c.d
     _call(fn, dev, stream, ctypes.byref(c), ctypes.byref(q), k_new.data_ptr(), v_new.data_ptr(), shape[0],
           stride, new_ptr.data_ptr(), int(max_new), _status(fn, dev_status, dev))
 

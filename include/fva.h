@@ -139,9 +139,9 @@ FVA_API int fva_version(void);
  * wait_limit_ns: time limit of every mbarrier wait (default 2 s; 0 restores it). A wait
  *   that runs out sets FVA_DEVERR_TIMEOUT in dev_status, and its CTA drains its own loads
  *   and MMAs, frees TMEM and exits; the device stays usable.
- * flags: FVA_DIAG_WITHHOLD_Q makes each CTA skip its Q tile load (the gradient kernels: all
- *   loads; the cache attention has no such load), so the waits behind it can never complete
- *   and run out after wait_limit_ns (a wait on a flag nothing sets).
+ * flags: FVA_DIAG_WITHHOLD_Q makes each CTA skip its Q tile load (the tensor-core gradient and
+ *   the cache attention: all loads), so the waits behind it can never complete and run out
+ *   after wait_limit_ns (a wait on a flag nothing sets).
  * fva_set_diagnostics(0, 0) restores normal operation. */
 enum { FVA_DIAG_WITHHOLD_Q = 1 };
 FVA_API void fva_set_diagnostics(uint64_t wait_limit_ns, int flags);
@@ -346,6 +346,8 @@ FVA_API int fva_sparse_attn_bwd(const fva_shape* s, const void* q_dev, const voi
  * page may hold anything, NaN included. A page id outside [0, n_pages), or a length outside
  * its range, sets FVA_DEVERR_BAD_LIST in dev_status; the page is then skipped, the length
  * clamped. 1 <= B <= 65535, 1 <= max_blocks <= 16384 (2^20 tokens).
+ * Calls that may overlap (two streams, captured graphs that may run at once) need a workspace
+ * each, and must not write pages that another one reads or writes.
  */
 typedef struct fva_cache {
   void* k;
@@ -403,7 +405,8 @@ FVA_API int fva_cache_route(const fva_cache* cache, const fva_seqs* seqs, const 
  * fva_cache_route writes them, or both NULL: every block):
  *   o_h = sum_j softmax_j(scale * q_h . k_j) v_j   over the valid tokens j of the kept blocks.
  * o [B, H, d] contiguous, of the cache's dtype; lse_dev, optional: float32 [B, H], the natural
- * logarithm of the softmax denominator. An empty sequence or list gives o = 0, lse = -infinity.
+ * logarithm of the softmax denominator. An empty sequence or list, or one whose every score is
+ * -infinity, gives o = 0, lse = -infinity and adds nothing to the masses.
  * accumulate != 0 adds every token's attention weight, summed over the query heads of its key
  * head, to cache->mass (sequences of one call that share pages add atomically: the sum is then
  * right but its rounding order is not fixed; otherwise equal inputs give equal bits).
@@ -426,7 +429,8 @@ FVA_API int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const v
  * kept_dev: int32 [B, Hkv, keep], the kept tokens' old positions, -1 behind them; new_len_dev:
  * int32 [B], min(len, keep). n_sink + n_recent <= keep, 1 <= keep <= 2^20. A destination page
  * must not be a source page of the call (of its own sequence: FVA_DEVERR_BAD_LIST, and the
- * page is not written) nor be named twice.
+ * page is not written) nor be named twice. The workspace is reserved: what the selection keeps
+ * between its passes fits on the chip.
  */
 FVA_API size_t fva_cache_evict_workspace_bytes(const fva_cache* cache, int B, int max_blocks);
 FVA_API int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int n_sink, int n_recent,

@@ -270,3 +270,34 @@ def test_bad_list_entries_are_reported(d, dtype):
         c.mask.worklist[1] = good
         c.st.zero_()
     c.check(c.backward())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_wait_limits_end(d):
+    """Whatever waits run out, in some of the warps or none, the calls end and the next is right."""
+    c = Case(1, 2, 3, 12, 17, d, "bf16", "random")
+    for limit in (1, 2000, 20000):
+        c.fva.fva_set_diagnostics(limit, 0)
+        try:
+            for _ in range(10):
+                c.backward()
+                assert int(c.st.item()) in (0, c.fva.FVA_DEVERR_TIMEOUT)
+        finally:
+            c.fva.fva_set_diagnostics(0, 0)
+    c.st.zero_()
+    c.check(c.backward())
+
+
+def test_training_layer_refusals():
+    """A gradient before any forward, and a forward with the mask of another shape."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import fva, pipeline
+    s = fva.make_shape(1, 1, 64, 1, 8, 16)
+    layer = pipeline.SparseAttentionLayer(s, 0.9, 2, train=True)
+    x = torch.zeros(1, 128, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(RuntimeError):
+        layer.backward(x, x, x, x)
+    small = fva.Mask.allocate(fva.make_shape(1, 1, 64, 1, 8, 8))
+    t = [torch.zeros(1, 1, 128, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    with pytest.raises(ValueError):
+        fva.fva_sparse_attn_lse(s, *t[:3], small, t[3], torch.zeros(1, 1, 128, device="cuda"))

@@ -636,3 +636,146 @@ def test_streams_served_together():
         add([64 * 15 - 6, 700, 700])
     with pytest.raises(ValueError):
         add([64 * 16, 0, 0])
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(8, 2, 128, "bf16"), (20, 1, 64, "f16"), (3, 3, 32, "f32"), (8, 2, 128, "f32")])
+def test_wait_that_runs_out_is_reported(H, Hkv, d, dtype):
+    """With the loads withheld and a 20 ms limit the attention reports a timeout, ends and leaves
+    the device usable; the next call is right."""
+    s = Streams([700, 64, 0, 5000], H, Hkv, d, dtype).fill()
+    q = s.query()
+    s.fva.fva_set_diagnostics(20_000_000, s.fva.FVA_DIAG_WITHHOLD_Q)
+    try:
+        s.attn(q, None, None, accumulate=True)
+        s.ok(s.fva.FVA_DEVERR_TIMEOUT)
+    finally:
+        s.fva.fva_set_diagnostics(0, 0)
+    s.cache.mass.zero_()
+    before = s.cache.mass.double().cpu().numpy()
+    o, lse = s.attn(q, None, None, accumulate=True)
+    s.ok()
+    s.check_attn(o, lse, [[np.arange(-(-n // 64))] * Hkv for n in s.lens], before)
+
+
+@pytest.mark.parametrize("limit", [1, 2000, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_short_wait_limits_end(dtype, limit):
+    """Whatever waits run out, in some of the warps or none, the calls end and the next is right."""
+    s = Streams([3000, 1000, 1, 20000], 8, 2, 128, dtype).fill()
+    q = s.query()
+    want = s.attn(q, None, None)
+    s.ok()
+    s.fva.fva_set_diagnostics(limit, 0)
+    try:
+        for _ in range(20):
+            s.attn(q, None, None, accumulate=True)
+            assert int(s.st.item()) in (0, s.fva.FVA_DEVERR_TIMEOUT)
+    finally:
+        s.fva.fva_set_diagnostics(0, 0)
+    s.st.zero_()
+    got = s.attn(q, None, None)
+    s.ok()
+    assert all(bool((a == b).all()) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[70], [40000]])  # one CTA, and a unit that crosses shares
+def test_scores_of_minus_infinity_weigh_nothing(dtype, lens):
+    """Heads whose every score is -infinity give 0 and -infinity and add nothing to the masses."""
+    import torch
+    s = Streams(lens, 2, 1, 64, dtype)
+    inf = float("-inf")
+    s.k[0][:, 0, 0] = inf
+    s.fill()
+    q = np.abs(s.draw(1, 2, 64))
+    q[:, 0, 0], q[:, 1, 0] = 1.0, 1.0
+    o, lse = s.attn(s.query(q), None, None, accumulate=True)
+    s.ok()
+    pages = torch.from_numpy(s.table_np[0, :-(-lens[0] // 64)].astype(np.int64)).cuda()
+    assert bool((o == 0).all()) and bool((lse == inf).all()) and bool((s.cache.mass[pages] == 0).all())
+
+
+def test_append_refuses_overlapping_rows_and_wrapped_ranges():
+    import torch
+    s = Streams([100, 80], 2, 1, 64, "bf16")
+    one = torch.zeros((1, 1, 64), dtype=s.dt, device="cuda")
+    ptr = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
+    with pytest.raises(s.fva.FvaError):  # an expanded row has stride 0
+        s.fva.fva_cache_append(s.cache, s.table, s.length, one.expand(40, 1, 64), one.expand(40, 1, 64), ptr, 20, s.st)
+    x = torch.zeros((40, 1, 64), dtype=s.dt, device="cuda")
+    for a, b in ((2 ** 31 - 1, -2 ** 31), (30, 10), (-5, 10)):  # differences of 1 (wrapped), -20 and 15
+        ptr = torch.tensor([a, b, b], dtype=torch.int32, device="cuda")
+        s.fva.fva_cache_append(s.cache, s.table, s.length, x, x, ptr, 20, s.st)
+        s.ok(s.fva.FVA_DEVERR_BAD_LIST)
+    assert bool(s.cache.k.isnan().all()) and bool(s.cache.key_mean.isnan().all())
+
+
+def test_refused_calls_leave_the_streams_as_they_were():
+    """CachedAttention: a refused append or eviction takes no page and changes no length."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import pipeline
+    att = pipeline.CachedAttention(2, 4, 2, 64, n_pages=12, max_blocks=8)
+    x = torch.randn(100, 2, 64, device="cuda").bfloat16()
+    att.append(x, x, [70, 30])
+    state = lambda: (sorted(att.free), [list(p) for p in att.pages], list(att.lengths), att.length.tolist(),  # noqa: E731
+                     att.table[0, :2].tolist(), att.table[1, :1].tolist())
+    before = state()
+    with pytest.raises(ValueError):
+        att.append(x.float(), x.float(), [60, 40])
+    with pytest.raises(ValueError):
+        att.append(x, x[:, :1], [60, 40])
+    with pytest.raises(ValueError):
+        att.append(x, x, [60, 30])
+    wide = torch.randn(100 * 130 + 8, device="cuda").bfloat16()[:100 * 130].view(100, 130)[:, :128].unflatten(1, (2, 64))
+    with pytest.raises(RuntimeError):  # rows that start on 4-byte boundaries
+        att.append(wide, wide, [60, 40])
+    for keep, sink, recent in ((0, 0, 0), (-1, 0, 0), (10, 6, 5), (10, -1, 0), ((1 << 20) + 1, 0, 0)):
+        with pytest.raises(ValueError):
+            att.evict(keep, sink, recent)
+    assert state() == before
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    first = att.attend(q, torch.empty_like(q))
+    att.append(x[:0], x[:0], [0, 0])
+    assert torch.equal(att.attend(q, torch.empty_like(q)), first)
+    assert int(att.dev_status.item()) == 0
+    att.evict(1 << 20, 0, 0)  # a budget above every length moves the tokens and keeps them all
+    assert att.lengths == before[2] and torch.equal(att.attend(q, torch.empty_like(q)), first)
+
+
+def test_captured_eviction_and_append_are_replayed():
+    """Append and eviction captured into one graph: every replay does what the calls would."""
+    import torch
+    s = Streams([500, 130], 2, 2, 64, "bf16", spare=12).fill()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    dst = torch.tensor([s.free[:2], s.free[2:4]], **i32)
+    kept, new_len, ws = torch.empty((2, 2, 100), **i32), torch.empty(2, **i32), s.ws(256)
+    x = torch.zeros((2, 2, 64), dtype=s.dt, device="cuda")
+    ptr = torch.tensor([0, 1, 2], **i32)
+    after = torch.tensor([101, 101], **i32)
+
+    def step():
+        s.fva.fva_cache_evict(s.cache, s.table, s.length, 100, 2, 10, dst, kept, new_len, ws, dev_status=s.st)
+        s.fva.fva_cache_append(s.cache, dst, after, x, x, ptr, 1, s.st)
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    pages = torch.from_numpy(s.table_np[0, :8].astype(np.int64)).cuda()
+    for seed in range(3):
+        torch.manual_seed(seed)
+        s.cache.mass[pages] = torch.rand(8, 2, 64, device="cuda")
+        x.copy_(torch.randn(2, 2, 64, device="cuda"))
+        step()
+        want = [t.clone() for t in (kept, new_len, s.cache.k[dst[0].long()], s.cache.key_mean[dst[1].long()])]
+        for t in (kept, new_len):
+            t.zero_()
+        s.cache.k[dst.flatten().long()] = 0
+        g.replay()
+        got = [kept, new_len, s.cache.k[dst[0].long()], s.cache.key_mean[dst[1].long()]]
+        rows = [slice(None), slice(None), slice(None), slice(None)]
+        for a, b, r in zip(got, want, rows):
+            a, b = a[r].reshape(-1), b[r].reshape(-1)
+            if a.dtype.is_floating_point:  # the slots behind the 101 tokens are nobody's
+                a, b = a[:64 * 64], b[:64 * 64]
+            assert torch.equal(a, b)
+    s.ok()
