@@ -530,9 +530,12 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // A cluster of CTAs per (key head, sequence), each with a contiguous share of the tokens. The
 // threshold among the middle tokens is found in three digits (11, 11, 10 bits) from the
 // cluster-wide histograms; then the shares' counts place every share's kept tokens. The
-// patterns stay in shared memory between the passes while a share fits (`hold` tokens).
+// patterns stay in shared memory between the passes while a share fits (`hold` tokens); a
+// thread takes four consecutive tokens at a time, since what bounds the passes is the number of
+// instructions a token.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr uint32_t kAlways = ~0u;  // a token of either end, above every pattern; or none, behind the share
 
 template <typename T>
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T> c, int keep, int n_sink, int n_recent,
@@ -540,12 +543,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
                                                                      int32_t* __restrict__ new_len,
                                                                      int32_t* dev_status) {
   extern __shared__ __align__(16) uint32_t held[];  // [hold]
-  __shared__ __align__(16) uint32_t bins[2048];
+  __shared__ __align__(16) uint32_t bins[3][2048];  // of each pass
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need, warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
+  __shared__ int s_need, warp_n[3][kEvictWarps], warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 3 * 2048 / 4; i += kEvictThreads)
+    reinterpret_cast<uint4*>(&bins[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
   grid_wait();
   grid_release();
   const int len = seq_len(c, b, dev_status);
@@ -555,84 +560,93 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
     for (int i = rank * kEvictThreads + tid; i < keep; i += C * kEvictThreads) out[i] = i < len ? i : -1;
     return;
   }
-  // shares end on block borders, so a warp's 32 tokens lie in one page
+  auto sync_all = [&] {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
+  // shares end on block borders, so a warp's loads lie in one page
   const int per = ((len + C - 1) / C + kBlock - 1) / kBlock * kBlock, t0 = min(rank * per, len), t1 = min(t0 + per, len);
   const bool fits = per <= hold;
+  const int lo = n_sink, hi = min(len - n_recent, t1);  // the middle, as far as this share goes
   auto load_key = [&](int t) -> uint32_t {
+    if (t < lo || t >= hi) return kAlways;
     const int page = page_of(c, b, t / kBlock, dev_status);
     return page < 0 ? 0u : mass_key(c.mass[(static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock]);
   };
-  if (fits) {  // a warp takes whole pages, eight on their way at a time
+  if (fits) {  // a warp takes whole pages, 16 on their way at a time
     const int nb = (t1 - t0 + kBlock - 1) / kBlock, b0 = t0 / kBlock;
     for (int base = warp; base < nb; base += 32 * kEvictWarps) {
       const int mine_at = base + lane * kEvictWarps;
       const int pages = mine_at < nb ? page_of(c, b, b0 + mine_at, dev_status) : -1;
       const int cnt = min(32, (nb - base + kEvictWarps - 1) / kEvictWarps);
-      for (int k0 = 0; k0 < cnt; k0 += 8) {
-        float2 x[8];
+      for (int k0 = 0; k0 < cnt; k0 += 16) {
+        float2 x[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
           const int page = __shfl_sync(0xffffffffu, pages, min(k0 + k, cnt - 1));
           x[k] = page < 0 ? make_float2(NAN, NAN)
                           : reinterpret_cast<const float2*>(c.mass + (static_cast<int64_t>(page) * c.Hkv + h) * kBlock)[lane];
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k0 + k < cnt)
-            *reinterpret_cast<uint2*>(held + (base + (k0 + k) * kEvictWarps) * kBlock + 2 * lane) =
-                make_uint2(mass_key(x[k].x), mass_key(x[k].y));
+        for (int k = 0; k < 16; ++k)
+          if (k0 + k < cnt) {
+            const int at = (base + (k0 + k) * kEvictWarps) * kBlock + 2 * lane, t = t0 + at;
+            *reinterpret_cast<uint2*>(held + at) = make_uint2(t < lo || t >= hi ? kAlways : mass_key(x[k].x),
+                                                              t + 1 < lo || t + 1 >= hi ? kAlways : mass_key(x[k].y));
+          }
       }
     }
-    __syncthreads();
   }
-  auto key = [&](int t) -> uint32_t { return fits ? held[t - t0] : load_key(t); };
-  const int lo = n_sink, hi = len - n_recent;  // the middle, of which `need` tokens stay
-  int need = keep - n_sink - n_recent;
+  __syncthreads();
+  // patterns of t .. t + 3 (t - t0 a multiple of 4, t < t1: the share's last block is held whole)
+  auto four = [&](int t, uint32_t (&u)[4]) {
+    if (fits) {
+      const uint4 x = *reinterpret_cast<const uint4*>(held + (t - t0));
+      u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = load_key(t + k);
+    }
+  };
+  int need = keep - n_sink - n_recent;  // of the middle tokens so many stay
   const bool some = need > 0;
-  uint32_t prefix = 0;
+  uint32_t prefix = 0, same = 0;  // the digits found so far, and their bits
   int shift = 32;
   for (int pass = 0; pass < 3 && some; ++pass) {
-    const int up = shift, width = pass < 2 ? 11 : 10;
+    const int width = pass < 2 ? 11 : 10;
     shift -= width;
-    for (int i = tid; i < 2048; i += kEvictThreads) bins[i] = 0u;
-    __syncthreads();
     uint32_t zeros = 0;  // tokens that were never attended to, often many: counted aside
     const uint32_t mask = (1u << width) - 1u;
-    const int end = min(hi, t1);
+#pragma unroll 2
     for (int t = t0 + 4 * tid; t < t1; t += 4 * kEvictThreads) {
       uint32_t u[4];
-      if (fits) {
-        const uint4 x = *reinterpret_cast<const uint4*>(held + (t - t0));
-        u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = t + k < t1 ? load_key(t + k) : 0u;
-      }
-      const bool inner = t >= lo && t + 4 <= end;
+      four(t, u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (!inner && (t + k < lo || t + k >= end)) continue;
-        if (pass > 0 && (u[k] >> up) != (prefix >> up)) continue;
+        if (((u[k] ^ prefix) & same) != 0u || u[k] == kAlways) continue;
         if (u[k] == kZeroMass) ++zeros;
-        else atomicAdd(&bins[(u[k] >> shift) & mask], 1u);
+        else atomicAdd(&bins[pass][(u[k] >> shift) & mask], 1u);
       }
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
-    if (lane == 0 && zeros) atomicAdd(&bins[(kZeroMass >> shift) & ((1u << width) - 1u)], zeros);
-    cluster.sync();
+    if (lane == 0 && zeros) atomicAdd(&bins[pass][(kZeroMass >> shift) & mask], zeros);
+    sync_all();
     // two bins a thread, from the highest down; every CTA finds the same one
-    uint32_t n0 = 0, n1 = 0;
     const int d0 = 2047 - 2 * tid;
-    for (int r0 = 0; r0 < C; r0 += 8) {
-      uint2 x[8];
+    uint32_t n0 = 0, n1 = 0;
+    if (C > 1) {
+      uint2 x[kMaxCluster];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        x[r] = r0 + r < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(bins, r0 + r) + d0 - 1) : make_uint2(0u, 0u);
+      for (int r = 0; r < kMaxCluster; ++r)
+        x[r] = r < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&bins[pass][0], r) + d0 - 1) : make_uint2(0u, 0u);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < kMaxCluster; ++r) {
         n1 += x[r].x;
         n0 += x[r].y;
       }
+    } else {
+      n1 = bins[pass][d0 - 1];
+      n0 = bins[pass][d0];
     }
     int inc = static_cast<int>(n0 + n1);
 #pragma unroll
@@ -640,89 +654,100 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
       const int x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    if (lane == 31) warp_a[warp] = inc;
+    if (lane == 31) warp_n[pass][warp] = inc;
     __syncthreads();
-    int before = inc - static_cast<int>(n0 + n1);
-    for (int w = 0; w < warp; ++w) before += warp_a[w];
+    const int before = inc - static_cast<int>(n0 + n1) + __reduce_add_sync(0xffffffffu, lane < warp ? warp_n[pass][lane] : 0);
     if (before < need && need <= before + static_cast<int>(n0 + n1)) {
       const bool first = need <= before + static_cast<int>(n0);
       s_prefix = prefix | (static_cast<uint32_t>(first ? d0 : d0 - 1) << shift);
       s_need = need - before - (first ? 0 : static_cast<int>(n0));
     }
-    cluster.sync();  // the bins have been read everywhere
+    __syncthreads();
     prefix = s_prefix;
     need = s_need;
+    same |= mask << shift;
   }
-  // keys above the threshold and both ends stay, and the first `need` of the equal ones
-  const int piece = (per / kEvictWarps + 31) / 32 * 32, w0 = t0 + warp * piece, w1 = min(w0 + piece, t1);
-  auto classify = [&](int t, bool& above, bool& equal) {
-    const bool in = t < w1, middle = t >= lo && t < hi;
-    const uint32_t u = in && middle && some ? key(t) : 0u;
-    above = in && (!middle || (some && u > prefix));
-    equal = in && middle && some && u == prefix;
+  // patterns above the threshold and both ends stay, and the first `need` of the equal ones. A
+  // warp takes a contiguous piece, a lane four tokens of each 128.
+  const uint32_t border = some ? prefix : kAlways - 1u;  // (no token has the pattern kAlways - 1)
+  const int piece = (per / kEvictWarps + 127) / 128 * 128, w0 = t0 + warp * piece, w1 = min(w0 + piece, t1);
+  auto classify = [&](int t, unsigned& above, unsigned& equal) {  // a bit a token
+    above = equal = 0u;
+    if (t >= w1) return;
+    uint32_t u[4];
+    four(t, u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      above |= u[k] > border ? 1u << k : 0u;
+      equal |= u[k] == border ? 1u << k : 0u;
+    }
+    if (t + 4 > w1) above &= (1u << (w1 - t)) - 1u;  // (behind the share: kAlways, never equal)
   };
   int na = 0, ne = 0;
-  unsigned held_a = 0, held_e = 0;  // lane i: the ballots of the piece's i-th 32 tokens
-  for (int base = w0; base < w1; base += 32) {
-    bool a, e;
-    if (fits && some && base >= lo && base + 32 <= min(hi, w1)) {
-      const uint32_t u = held[base - t0 + lane];
-      a = u > prefix;
-      e = u == prefix;
-    } else {
-      classify(base + lane, a, e);
+  unsigned held_a = 0, held_e = 0;  // the bits of the first 1024 tokens of the piece
+  for (int base = w0; base < w1; base += 128) {
+    unsigned a, e;
+    classify(base + 4 * lane, a, e);
+    const int at = (base - w0) / 32;
+    if (at < 32) {
+      held_a |= a << at;
+      held_e |= e << at;
     }
-    const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
-    if (lane == (base - w0) / 32) {
-      held_a = am;
-      held_e = em;
-    }
-    na += __popc(am);
-    ne += __popc(em);
+    na += __popc(a);
+    ne += __popc(e);
   }
+  na = __reduce_add_sync(0xffffffffu, na);
+  ne = __reduce_add_sync(0xffffffffu, ne);
   if (lane == 0) {
     warp_a[warp] = na;
     warp_e[warp] = ne;
   }
   __syncthreads();
-  int above = 0, equal = 0;
-  if (tid == 0) {
-    for (int w = 0; w < kEvictWarps; ++w) {
-      above += warp_a[w];
-      equal += warp_e[w];
+  if (warp == 0) {
+    const int all_a = __reduce_add_sync(0xffffffffu, warp_a[lane]), all_e = __reduce_add_sync(0xffffffffu, warp_e[lane]);
+    if (lane == 0) {
+      mine[0] = all_a;
+      mine[1] = all_e;
     }
-    mine[0] = above;
-    mine[1] = equal;
   }
-  cluster.sync();
-  above = equal = 0;
-  for (int r = 0; r < rank; ++r) {
-    above += cluster.map_shared_rank(mine, r)[0];
-    equal += cluster.map_shared_rank(mine, r)[1];
+  if (C > 1) cluster.sync();
+  int above = lane < warp ? warp_a[lane] : 0, equal = lane < warp ? warp_e[lane] : 0;
+  if (lane < rank) {
+    const int* theirs = cluster.map_shared_rank(mine, lane);
+    above += theirs[0];
+    equal += theirs[1];
   }
-  for (int w = 0; w < warp; ++w) {
-    above += warp_a[w];
-    equal += warp_e[w];
-  }
-  const unsigned below = (1u << lane) - 1u;
-  for (int base = w0; base < w1; base += 32) {
-    unsigned am, em;
-    if (piece <= 1024) {
-      am = __shfl_sync(0xffffffffu, held_a, (base - w0) / 32);
-      em = __shfl_sync(0xffffffffu, held_e, (base - w0) / 32);
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  for (int base = w0; base < w1; base += 128) {
+    const int at = (base - w0) / 32, t = base + 4 * lane;
+    unsigned a, e;
+    if (at < 32) {
+      a = (held_a >> at) & 15u;
+      e = (held_e >> at) & 15u;
     } else {
-      bool a, e;
-      classify(base + lane, a, e);
-      am = __ballot_sync(0xffffffffu, a);
-      em = __ballot_sync(0xffffffffu, e);
+      classify(t, a, e);
     }
-    const int rank_e = equal + __popc(em & below);
-    if (((am >> lane) & 1u) || (((em >> lane) & 1u) && rank_e < need))
-      out[above + __popc(am & below) + min(rank_e, need)] = base + lane;
-    above += __popc(am);
-    equal += __popc(em);
+    const int count = __popc(a) | (__popc(e) << 16);
+    int inc = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int total = __shfl_sync(0xffffffffu, inc, 31), before = inc - count;
+    int pa = above + (before & 0xffff), pe = equal + (before >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool is_a = (a >> k) & 1u, is_e = (e >> k) & 1u;
+      if (is_a || (is_e && pe < need)) out[pa + min(pe, need)] = t + k;
+      pa += is_a;
+      pe += is_e;
+    }
+    above += total & 0xffff;
+    equal += total >> 16;
   }
-  cluster.sync();  // nobody leaves while its counts are read
+  if (C > 1) cluster.sync();  // nobody leaves while its counts are read
 }
 
 // One CTA per (destination block, key head, sequence): gathers its 64 kept tokens.
