@@ -196,11 +196,6 @@ struct F32Cfg {
   static_assert(2 * kF32Rows * D <= 4 * kB, "the sums of both groups fit the stream's buffers");
 };
 
-__device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 template <int D, bool KV>
 __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, const int32_t* list, int n_list, int N,
                                         int nB, float scale, float* smem, int32_t* dev_status) {

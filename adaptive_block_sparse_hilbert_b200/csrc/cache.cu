@@ -2,6 +2,8 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.cuh"
 
 namespace fva {
@@ -14,7 +16,8 @@ namespace cg = cooperative_groups;
 // A CTA holds the 64 rows of one (page, key head), 16 bytes a thread and row: thread = (row
 // lane, 16-byte piece), rows row lane, row lane + kLanes, ... All of a thread's loads are issued
 // before its first store, so a CTA has up to 32 KB in flight. (16 prompts, d = 128, on 128 / 256
-// / 512 threads: 41 / 44 / 50 us; eviction of 62500 of 250 thousand tokens: 136 / 113 / 120 us.)
+// / 512 threads: 41 / 44 / 50 us; eviction of 62500 of 250 thousand tokens, selection included: 134
+// / 130 / 136 us.)
 constexpr int kAppendThreads = 128, kEvictCopyThreads = 256;
 
 template <typename T, int D, int kPageThreads>
@@ -532,17 +535,44 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // cluster-wide histograms; then the shares' counts place every share's kept tokens. The
 // patterns stay in shared memory between the passes while a share fits (`hold` tokens); a
 // thread takes four consecutive tokens at a time, since what bounds the passes is the number of
-// instructions a token.
+// instructions a token. One further cluster a sequence (blockIdx.y = Hkv) marks the destination
+// pages that are pages of the sequence itself.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kClashWords = kMaxCacheBlocks / 32;
 constexpr uint32_t kAlways = ~0u;  // a token of either end, above every pattern; or none, behind the share
 
+// Bit i of `clash`: destination i is one of the sequence's own pages. The pages' bits stand in
+// `bits`, as many of them at a time as `words` hold.
 template <typename T>
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T> c, int keep, int n_sink, int n_recent,
-                                                                     int hold, int32_t* __restrict__ kept,
-                                                                     int32_t* __restrict__ new_len,
-                                                                     int32_t* dev_status) {
-  extern __shared__ __align__(16) uint32_t held[];  // [hold]
+__device__ void mark_clashes(const CacheView<T>& c, int b, int nB, const int32_t* __restrict__ dst, int n_dst, uint32_t* bits,
+                             int words, uint32_t* __restrict__ clash) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < (n_dst + 31) / 32; i += kEvictThreads) clash[i] = 0u;
+  const int64_t most = static_cast<int64_t>(words) * 32;
+  for (int64_t first = 0; first < c.n_pages; first += most) {
+    const int n = static_cast<int>(min(most, c.n_pages - first));
+    for (int i = tid; i < (n + 31) / 32; i += kEvictThreads) bits[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < nB; i += kEvictThreads) {
+      const int64_t at = c.table[static_cast<int64_t>(b) * c.max_blocks + i] - first;
+      if (at >= 0 && at < n) atomicOr(&bits[at >> 5], 1u << (at & 31));
+    }
+    __syncthreads();
+    for (int i = tid; i < n_dst; i += kEvictThreads) {
+      const int64_t at = dst[i] - first;
+      if (at >= 0 && at < n && ((bits[at >> 5] >> (at & 31)) & 1u)) atomicOr(&clash[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kEvictThreads)
+    evict_select_kernel(CacheView<T> c, int keep, int n_sink, int n_recent, int hold, int words,
+                        const int32_t* __restrict__ dst_table, int dst_blocks, uint32_t* __restrict__ clash,
+                        int32_t* __restrict__ kept, int32_t* __restrict__ new_len, int32_t* dev_status) {
+  extern __shared__ __align__(16) uint32_t held[];  // [words], hold of them for patterns
   __shared__ __align__(16) uint32_t bins[3][2048];  // of each pass
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, warp_n[3][kEvictWarps], warp_a[kEvictWarps], warp_e[kEvictWarps], mine[2];
@@ -554,8 +584,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
   grid_wait();
   grid_release();
   const int len = seq_len(c, b, dev_status);
+  if (h == c.Hkv) {
+    if (rank > 0) return;
+    if (tid == 0) new_len[b] = min(len, keep);
+    mark_clashes(c, b, (len + kBlock - 1) / kBlock, dst_table + static_cast<int64_t>(b) * dst_blocks,
+                 (min(len, keep) + kBlock - 1) / kBlock, held, words, clash + static_cast<int64_t>(b) * kClashWords);
+    return;
+  }
   int32_t* out = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep;
-  if (h == 0 && rank == 0 && tid == 0) new_len[b] = min(len, keep);
   if (len <= keep) {
     for (int i = rank * kEvictThreads + tid; i < keep; i += C * kEvictThreads) out[i] = i < len ? i : -1;
     return;
@@ -750,13 +786,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(CacheView<T
   if (C > 1) cluster.sync();  // nobody leaves while its counts are read
 }
 
-// One CTA per (destination block, key head, sequence): gathers its 64 kept tokens.
+// One CTA per (destination block, key head, sequence): gathers its 64 kept tokens. What bounds it
+// are the rows in flight, so a CTA holds little: the keys pass through registers, for their mean,
+// the values through shared memory, and six CTAs fit an SM. (62500 of 250 thousand tokens, 8 key
+// heads, d = 128: 91 us, 5.9 TB/s; with the values in registers too, four CTAs an SM, 95.)
 template <typename T, int D>
-__global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(CacheView<T> c, int keep,
-                                                                  const int32_t* __restrict__ dst_table, int dst_blocks,
-                                                                  const int32_t* __restrict__ kept,
-                                                                  int32_t* dev_status) {
+__global__ void __launch_bounds__(kEvictCopyThreads, sizeof(T) == 2 ? 6 : 4)
+    evict_copy_kernel(CacheView<T> c, int keep, const int32_t* __restrict__ dst_table, int dst_blocks,
+                      const uint32_t* __restrict__ clash, const int32_t* __restrict__ kept, int32_t* dev_status) {
   using P = PageRows<T, D, kEvictCopyThreads>;
+  __shared__ __align__(128) uint4 s_v[kBlock * P::kPieces];
   const int b = blockIdx.z, h = blockIdx.y, block = blockIdx.x;
   grid_wait();
   const int len = seq_len(c, b, nullptr);
@@ -765,29 +804,26 @@ __global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(CacheView
   const int lane = threadIdx.x / P::kPieces, piece = threadIdx.x % P::kPieces;
   const int32_t* src_at = kept + (static_cast<int64_t>(b) * c.Hkv + h) * keep + block * kBlock;
   const int dst = dst_table[static_cast<int64_t>(b) * dst_blocks + block];
-  uint4 k[P::kRows], v[P::kRows];
+  const bool own = (clash[static_cast<int64_t>(b) * kClashWords + block / 32] >> (block % 32)) & 1u;
+  uint4 k[P::kRows];
   float mass[P::kRows];
 #pragma unroll
   for (int i = 0; i < P::kRows; ++i) {
     const int r = lane + i * P::kLanes;
-    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    k[i] = make_uint4(0u, 0u, 0u, 0u);
     mass[i] = 0.0f;
-    if (r < n) {
-      const int t = src_at[r];
-      const int page = page_of(c, b, t / kBlock, dev_status);
-      if (page >= 0) {
-        const int64_t from = (static_cast<int64_t>(page) * c.Hkv + h) * kBlock + t % kBlock;
-        k[i] = __ldcs(reinterpret_cast<const uint4*>(c.k + from * D) + piece);
-        v[i] = __ldcs(reinterpret_cast<const uint4*>(c.v + from * D) + piece);
-        if (piece == 0) mass[i] = c.mass[from];
-      }
+    const int t = r < n ? src_at[r] : -1;
+    const int page = t >= 0 ? page_of(c, b, t / kBlock, dev_status) : -1;
+    const int64_t from = (static_cast<int64_t>(max(page, 0)) * c.Hkv + h) * kBlock + (t & (kBlock - 1));
+    copy16(s_v + r * P::kPieces + piece, reinterpret_cast<const uint4*>(c.v + from * D) + piece, page >= 0);
+    if (page >= 0) {
+      k[i] = __ldcs(reinterpret_cast<const uint4*>(c.k + from * D) + piece);
+      if (piece == 0) mass[i] = c.mass[from];
     }
   }
-  bool clash = false;
-  for (int i = threadIdx.x; i * kBlock < len; i += kEvictCopyThreads)
-    clash |= c.table[static_cast<int64_t>(b) * c.max_blocks + i] == dst;
-  if (__syncthreads_or(clash) || dst < 0 || dst >= c.n_pages) {
+  if (own || dst < 0 || dst >= c.n_pages) {
     if (threadIdx.x == 0) report(dev_status, FVA_DEVERR_BAD_LIST);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
   const int64_t to = (static_cast<int64_t>(dst) * c.Hkv + h) * kBlock;
@@ -796,11 +832,12 @@ __global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(CacheView
     const int r = lane + i * P::kLanes;
     if (r < n) {
       __stcs(reinterpret_cast<uint4*>(c.k + (to + r) * D) + piece, k[i]);
-      __stcs(reinterpret_cast<uint4*>(c.v + (to + r) * D) + piece, v[i]);
       if (piece == 0) c.mass[to + r] = mass[i];
     }
   }
-  write_mean<T, D, kEvictCopyThreads>(k, n, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * D);
+  asm volatile("cp.async.wait_all;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+  write_mean<T, D, kEvictCopyThreads>(k, n, c.key_mean + (static_cast<int64_t>(dst) * c.Hkv + h) * D);  // (a barrier in it)
+  if (threadIdx.x == kEvictCopyThreads - 1) bulk_store(c.v + to * D, s_v, n * D * static_cast<int>(sizeof(T)));
 }
 
 // ---------------------------------------------------------------------------------
@@ -891,7 +928,9 @@ struct EvictCall {
   int keep, n_sink, n_recent;
   const int32_t* dst_table;
   int dst_blocks;
-  int32_t *kept, *new_len, *dev_status;
+  int32_t *kept, *new_len;
+  uint32_t* clash;
+  int32_t* dev_status;
   cudaStream_t st;
   template <typename T, int D>
   cudaError_t operator()() const {
@@ -899,20 +938,23 @@ struct EvictCall {
     const unsigned Hkv = static_cast<unsigned>(c->Hkv), B = static_cast<unsigned>(s->B);
     const int tokens = s->max_blocks * kBlock, C = cluster_size(static_cast<int64_t>(B) * Hkv, tokens, 4096);
     const int per = ((tokens + C - 1) / C + kBlock - 1) / kBlock * kBlock, most = 200 * 1024 / 4;
-    const int hold = per <= most ? per : 0;
-    cudaError_t e = launch_cluster(evict_select_kernel<T>, dim3(static_cast<unsigned>(C), Hkv, B), kEvictThreads, C,
-                                   static_cast<size_t>(hold) * 4, st, v, keep, n_sink, n_recent, hold, kept, new_len,
-                                   dev_status);
+    const int hold = per <= most ? per : 0, page_words = (c->n_pages - 1) / 32 + 1;
+    const int words = std::max(hold, std::min(page_words, 16384));
+    cudaError_t e = launch_cluster(evict_select_kernel<T>, dim3(static_cast<unsigned>(C), Hkv + 1, B), kEvictThreads, C,
+                                   static_cast<size_t>(words) * 4, st, v, keep, n_sink, n_recent, hold, words, dst_table,
+                                   dst_blocks, clash, kept, new_len, dev_status);
     if (e != cudaSuccess) return e;
     return launch_chained(evict_copy_kernel<T, D>, dim3(static_cast<unsigned>((keep + kBlock - 1) / kBlock), Hkv, B),
-                          kEvictCopyThreads, 0, 0, st, v, keep, dst_table, dst_blocks, kept, dev_status);
+                          kEvictCopyThreads, 0, 0, st, v, keep, dst_table, dst_blocks, clash, kept, dev_status);
   }
 };
 
 cudaError_t launch_cache_evict(const fva_cache* c, const fva_seqs* s, int keep, int n_sink, int n_recent,
                                const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len,
-                               int32_t* dev_status, cudaStream_t st) {
-  return by_cache_type(c, EvictCall{c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, dev_status, st});
+                               uint32_t* clash, int32_t* dev_status, cudaStream_t st) {
+  return by_cache_type(c, EvictCall{c, s, keep, n_sink, n_recent, dst_table, dst_blocks, kept, new_len, clash, dev_status, st});
 }
+
+size_t cache_evict_clash_words(int B) { return static_cast<size_t>(B) * kClashWords; }
 
 }  // namespace fva

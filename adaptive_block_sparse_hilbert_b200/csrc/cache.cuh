@@ -82,8 +82,10 @@ size_t cache_attn_part_floats(int d);
 cudaError_t launch_cache_attn(const fva_cache* c, const fva_seqs* s, const void* q, int H, int64_t q_stride,
                               const int32_t* kept, const int32_t* n_kept, void* o, float* lse, float scale,
                               int accumulate, const CacheAttnScratch& ws, int32_t* dev_status, cudaStream_t st);
+// clash: cache_evict_clash_words(B) words of workspace.
+size_t cache_evict_clash_words(int B);
 cudaError_t launch_cache_evict(const fva_cache* c, const fva_seqs* s, int keep, int n_sink, int n_recent,
-                               const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len,
+                               const int32_t* dst_table, int dst_blocks, int32_t* kept, int32_t* new_len, uint32_t* clash,
                                int32_t* dev_status, cudaStream_t st);
 
 }  // namespace fva

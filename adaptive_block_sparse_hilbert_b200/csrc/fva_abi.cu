@@ -514,7 +514,7 @@ int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const void* q_d
 }
 
 size_t fva_cache_evict_workspace_bytes(const fva_cache* cache, int B, int max_blocks) {
-  return batch_sizes_ok(cache, B, max_blocks) ? 256 : 0;
+  return batch_sizes_ok(cache, B, max_blocks) ? cache_evict_clash_words(B) * sizeof(uint32_t) : 0;
 }
 
 int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int n_sink, int n_recent,
@@ -522,6 +522,7 @@ int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int 
                     void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, fva_stream_t stream) {
   const int rc = check_cache(cache, seqs);
   if (rc != FVA_OK) return rc;
+  if (cache->Hkv > 65534) return FVA_ERR_UNSUPPORTED_SHAPE;
   if (!cache->mass || !dst_table_dev || !kept_dev || !new_len_dev || !workspace_dev) return FVA_ERR_INVALID_ARG;
   if (keep < 1 || keep > kMaxCacheBlocks * kBlock || n_sink < 0 || n_recent < 0 ||
       static_cast<int64_t>(n_sink) + n_recent > keep)
@@ -530,7 +531,7 @@ int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int 
   if (workspace_bytes < fva_cache_evict_workspace_bytes(cache, seqs->B, seqs->max_blocks)) return FVA_ERR_WORKSPACE;
   if (!aligned16(workspace_dev)) return FVA_ERR_ALIGNMENT;
   return cuda_status(launch_cache_evict(cache, seqs, keep, n_sink, n_recent, dst_table_dev, dst_max_blocks, kept_dev,
-                                        new_len_dev, dev_status, stream));
+                                        new_len_dev, static_cast<uint32_t*>(workspace_dev), dev_status, stream));
 }
 
 }  // extern "C"

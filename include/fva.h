@@ -427,10 +427,9 @@ FVA_API int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const v
  * (int32 [B, dst_max_blocks], dst_max_blocks >= ceil(keep / 64)), whose key_mean is written;
  * the source pages are left as they were, and so are the slots behind the last token.
  * kept_dev: int32 [B, Hkv, keep], the kept tokens' old positions, -1 behind them; new_len_dev:
- * int32 [B], min(len, keep). n_sink + n_recent <= keep, 1 <= keep <= 2^20. A destination page
+ * int32 [B], min(len, keep). n_sink + n_recent <= keep, 1 <= keep <= 2^20, Hkv <= 65534. A destination page
  * must not be a source page of the call (of its own sequence: FVA_DEVERR_BAD_LIST, and the
- * page is not written) nor be named twice. The workspace is reserved: what the selection keeps
- * between its passes fits on the chip.
+ * page is not written) nor be named twice.
  */
 FVA_API size_t fva_cache_evict_workspace_bytes(const fva_cache* cache, int B, int max_blocks);
 FVA_API int fva_cache_evict(const fva_cache* cache, const fva_seqs* seqs, int keep, int n_sink, int n_recent,

@@ -748,7 +748,7 @@ def test_captured_eviction_and_append_are_replayed():
     s = Streams([500, 130], 2, 2, 64, "bf16", spare=12).fill()
     i32 = dict(dtype=torch.int32, device="cuda")
     dst = torch.tensor([s.free[:2], s.free[2:4]], **i32)
-    kept, new_len, ws = torch.empty((2, 2, 100), **i32), torch.empty(2, **i32), s.ws(256)
+    kept, new_len, ws = torch.empty((2, 2, 100), **i32), torch.empty(2, **i32), s.ws(s.fva.fva_cache_evict_workspace_bytes(s.cache, 2, s.max_blocks))
     x = torch.zeros((2, 2, 64), dtype=s.dt, device="cuda")
     ptr = torch.tensor([0, 1, 2], **i32)
     after = torch.tensor([101, 101], **i32)

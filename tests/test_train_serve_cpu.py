@@ -130,6 +130,7 @@ def test_route_attn_evict_refusals():
     assert _evict(keep=0) == _evict(keep=(1 << 20) + 1) == _evict(sink=-1) == _evict(recent=-1) == fva.FVA_ERR_INVALID_ARG
     assert _evict(sink=60, recent=41) == fva.FVA_ERR_INVALID_ARG
     assert _evict(sink=2 ** 31 - 1, recent=2 ** 31 - 1) == fva.FVA_ERR_INVALID_ARG
+    assert _evict(c=_cache(Hkv=65535)) == fva.FVA_ERR_UNSUPPORTED_SHAPE
     assert _evict(blocks=1) == fva.FVA_ERR_CAPACITY
     assert _evict(dst=None) == _evict(kept=None) == _evict(n=None) == _evict(ws=None) == fva.FVA_ERR_INVALID_ARG
     assert _evict(size=0) == fva.FVA_ERR_WORKSPACE
