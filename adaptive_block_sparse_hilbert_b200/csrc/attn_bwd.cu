@@ -247,6 +247,8 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  int e = next_of(0);
+  if (rank > 0 && e >= n_list) return;  // nothing to add: its SM takes another CTA
   load(sA0, a0, r0, kF32Rows);
   load(sA1, a1, r0, kF32Rows);
   if (!KV) load_stats(sStat, block);
@@ -257,7 +259,6 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
     for (int j = 0; j < NC; ++j) acc[i][j] = 0.0f;
   const float scale_log2 = scale * 1.4426950408889634f;
 
-  int e = next_of(0);
   fetch(e, 0);
   for (int buf = 0; e < n_list; buf ^= 1) {
     const int blk = list[e] >> 2;
@@ -339,40 +340,38 @@ __device__ __forceinline__ void bwd_f32(const F32Args& x, int64_t bh, int own, c
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  // the other CTAs' sums, and for dQ every CTA's second group's, through the stream's buffers as
-  // [2][32][D]: KV: dV and dK; else dQ of the groups
+  // every CTA leaves its sums in the stream's buffers as [2][32][D] (KV: dV and dK; else dQ of the
+  // groups), and the CTAs add a share of them each
   float* sum = sB + group * kF32Rows * D;
-  auto slot = [&](int i, int j) { return (tr + 8 * i) * D + ((j / kW) * 16 + tc) * kW + j % kW; };
-  if (rank > 0 || (!KV && group == 1)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < NC; ++j) sum[slot(i, j)] = acc[i][j];
-  }
+    for (int j = 0; j < NC; ++j) sum[(tr + 8 * i) * D + ((j / kW) * 16 + tc) * kW + j % kW] = acc[i][j];
   cluster.sync();
-  if (rank == 0 && (KV || group == 0)) {
-    const float* far[kF32Split];
+  const int active = min(max(nth, 1), kF32Split);  // the list has been read to its end
+  constexpr int kHalf = kF32Rows * D / 4;          // 16-byte pieces of a group
+  for (int at = rank * 256 + tid; at < (KV ? 2 : 1) * kHalf; at += active * 256) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float4 x) {
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+    };
 #pragma unroll
-    for (int r = 0; r < kF32Split; ++r) far[r] = cluster.map_shared_rank(sB, r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = r0 + tr + 8 * i;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int at = slot(i, j);
-        float v = acc[i][j];
-        if (!KV) v += sB[kF32Rows * D + at];
-#pragma unroll
-        for (int r = 1; r < kF32Split; ++r)
-          v += KV ? far[r][group * kF32Rows * D + at] : far[r][at] + far[r][kF32Rows * D + at];
-        if (n < N) {
-          const int64_t to = (base + r0) * D + at;
-          if (!KV) x.dq[to] = v * scale;
-          else if (group == 0) x.dv[to] = v;
-          else x.dk[to] = v * scale;
-        }
+    for (int r = 0; r < kF32Split; ++r) {
+      if (r < active) {
+        const float4* far = reinterpret_cast<const float4*>(cluster.map_shared_rank(sB, r));
+        add(far[at]);
+        if (!KV) add(far[kHalf + at]);
       }
     }
+    const bool second = KV && at >= kHalf;
+    const int in = second ? at - kHalf : at;
+    const float f = KV && !second ? 1.0f : scale;
+    float* out = KV ? (second ? x.dk : x.dv) : x.dq;
+    if (r0 + in / (D / 4) < N)
+      reinterpret_cast<float4*>(out + (base + r0) * D)[in] = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
   }
   cluster.sync();  // nobody leaves while its buffers are read
 }
