@@ -6,15 +6,21 @@
 // SM reads the same amount. A unit inside one CTA's share is finished there; one that crosses
 // shares leaves each share's unnormalised O with its running maximum and sum in the workspace,
 // and a second kernel joins them in share order (a fixed order: equal inputs, equal bits) and
-// accumulates the weights.
+// accumulates the weights. Small calls have a cluster of CTAs per unit instead, a part of its list
+// each, that joins through shared memory: the second launch then only accumulates, if at all.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "cache.cuh"
 
 namespace fva {
 
+namespace cg = cooperative_groups;
+
 constexpr int kShares = 296;  // CTAs of the split kernels at most: two per SM
 constexpr int kGroup = 16;    // query heads of a unit at most
+constexpr int kMaxParts = 8;  // CTAs of a cluster at most
+constexpr int kPartBlocks = 24;  // blocks that a CTA of a cluster takes at most
 
 template <typename T>
 struct AttnView {
@@ -134,19 +140,86 @@ struct Walk {
   __device__ int slot() const { return at == first_at ? 0 : 1; }
 };
 
-// A row's statistics: the log-sum-exp of a finished row, or maximum and sum for the join.
-template <typename T, int D>
-__device__ __forceinline__ void put_stats(const AttnView<T>& a, bool whole, int share, int slot, int64_t row, int g,
-                                          float mx, float sum) {
-  if (whole) {
-    const float l2 = sum == 0.0f ? -INFINITY : mx + log2f(sum);
-    if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
-    if (a.ws.scores) a.ws.lse[row] = l2;
-  } else {
-    float* part = a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + g) * (D + 2);
-    part[D] = mx;
-    part[D + 1] = sum;
+// A cluster's walk: its one unit, this CTA's part of the list, which may be empty.
+template <typename T>
+struct PartWalk {
+  int64_t at, end, start = 0;
+  int u, n;
+  bool taken = false;
+  __device__ PartWalk(const AttnView<T>& a, int rank, int parts) {
+    u = static_cast<int>(blockIdx.x) / parts;
+    n = unit_count(a, u, a.dev_status);
+    const int per = (n + parts - 1) / parts;
+    at = min(rank * per, n);
+    end = min(static_cast<int>(at) + per, n);
   }
+  __device__ bool next(const AttnView<T>&) {
+    const bool first = !taken;
+    taken = true;
+    return first;
+  }
+  __device__ int64_t stop() const { return end; }
+};
+
+template <typename T, bool kCluster>
+__device__ __forceinline__ auto make_walk(const AttnView<T>& a) {
+  if constexpr (kCluster) {
+    cg::cluster_group cluster = cg::this_cluster();
+    __syncthreads();  // publishes the mbarriers
+    return PartWalk<T>(a, static_cast<int>(cluster.block_rank()), static_cast<int>(cluster.num_blocks()));
+  } else {
+    const Share sh = find_share(a, blockIdx.x);  // (its barriers publish the mbarriers too)
+    return Walk<T>(sh, blockIdx.x);
+  }
+}
+
+// The log-sum-exp of a finished row.
+template <typename T>
+__device__ __forceinline__ void put_lse(const AttnView<T>& a, int64_t row, float mx, float sum) {
+  const float l2 = sum == 0.0f ? -INFINITY : mx + log2f(sum);
+  if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+  if (a.ws.scores) a.ws.lse[row] = l2;
+}
+
+// Rows of a unit from its cluster's parts ([row][D + 2] in every CTA's `part`: unnormalised O,
+// maximum, sum), in their order; a warp per row. Every thread of the CTA calls this.
+template <typename T, int D>
+__device__ void join_cluster(const AttnView<T>& a, int u, float* part) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), parts = static_cast<int>(cluster.num_blocks());
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int bh = u / a.GS, b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
+  const int g0 = (u - bh * a.GS) * kGroup, ng = min(a.G - g0, kGroup);
+  cluster.sync();
+  for (int r = rank + parts * warp; r < ng; r += parts * warps) {
+    constexpr int V = D / 32;
+    float m[kMaxParts], l[kMaxParts], x[kMaxParts][V];
+#pragma unroll
+    for (int c = 0; c < kMaxParts; ++c) {
+      const float* from = c < parts ? cluster.map_shared_rank(part, c) + r * (D + 2) : nullptr;
+      m[c] = from ? from[D] : -INFINITY;
+      l[c] = from ? from[D + 1] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[c][i] = from ? from[lane * V + i] : 0.0f;
+    }
+    float mx = -INFINITY, sum = 0.0f, acc[V];
+#pragma unroll
+    for (int c = 0; c < kMaxParts; ++c) mx = fmaxf(mx, m[c]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kMaxParts; ++c) {
+      const float f = m[c] == -INFINITY ? 0.0f : exp2f(m[c] - mx);
+      sum = fmaf(f, l[c], sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(f, x[c][i], acc[i]);
+    }
+    const int64_t row = static_cast<int64_t>(b) * a.H + h * a.G + g0 + r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) from_f32(sum == 0.0f ? 0.0f : acc[i] / sum, a.o + row * D + lane * V + i);
+    if (lane == 0) put_lse(a, row, mx, sum);
+  }
+  cluster.sync();  // nobody leaves while its part is read
 }
 
 struct SplitWaits {
@@ -157,8 +230,8 @@ struct SplitWaits {
 // The loading warp of a split kernel: walks its share's lists and the page table 32 entries at
 // a time and has `load(stage, page, head)` request the pages, as the ring's stages come free.
 // `valid` of a stage: its keys that count, 0 for a page that is skipped.
-template <typename T, typename Load>
-__device__ __forceinline__ void feed_pages(const AttnView<T>& a, Walk<T>& w, uint64_t* full, uint64_t* empty, int* valid_of,
+template <typename T, typename W, typename Load>
+__device__ __forceinline__ void feed_pages(const AttnView<T>& a, W& w, uint64_t* full, uint64_t* empty, int* valid_of,
                                            volatile int* abort_flag, const SplitWaits& waits, int stages,
                                            const Load& load) {
   if (waits.diag_flags & FVA_DIAG_WITHHOLD_Q) return;  // nothing ever arrives: the waits run out
@@ -275,7 +348,7 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return static_cast<uint32_t>((piece >> 3) * (kBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kCluster>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, AttnView<T> a,
                  SplitWaits waits) {
@@ -298,8 +371,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   grid_wait();
   grid_release();
-  const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
-  Walk<T> w(sh, share);
+  auto w = make_walk<T, kCluster>(a);
+  const int unit = w.u;
   volatile int* abort_flag = &s_abort;
   if (warp == 4) {
     feed_pages(a, w, full, empty, s_valid, abort_flag, waits, Cfg::kStages, [&](int stage, int page, int h) {
@@ -311,6 +384,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         tma_load_3d(dst + Cfg::kTile + c * (kBlock * 128), &tmv, &full[stage], c * 64, h * kBlock, page);
       }
     });
+    if constexpr (kCluster) join_cluster<T, D>(a, unit, reinterpret_cast<float*>(ring));
     return;
   }
 
@@ -460,8 +534,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       }
     }
     sync4();
-    const bool whole = w.whole();
-    const int slot = w.slot();
+    bool whole = false;  // finished here; else the sums go to `parts`, rows of D + 2
+    float* parts = reinterpret_cast<float*>(ring);
+    if constexpr (!kCluster) {
+      whole = w.whole();
+      parts = a.ws.part + (static_cast<int64_t>(share) * 2 + w.slot()) * kGroup * (D + 2);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // fragment rows rg, then rg + 8
       if (i * 8 >= ng) break;
@@ -498,18 +576,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) out[n * 4 + ct] = F::pack(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
         } else {
-          float2* part = reinterpret_cast<float2*>(a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + r) * (D + 2));
+          float2* part = reinterpret_cast<float2*>(parts + r * (D + 2));
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) part[n * 4 + ct] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
         }
-        if (ct == 0) put_stats<T, D>(a, whole, share, slot, row, r, mx, sum);
+        if (ct == 0 && whole) put_lse(a, row, mx, sum);
+        if (ct == 0 && !whole) parts[r * (D + 2) + D] = mx, parts[r * (D + 2) + D + 1] = sum;
       }
       sync4();  // the buffers are rewritten by the next rows, s_m and s_l by the next unit
     }
-    if (tid == 0) a.ws.start[w.u] = w.start;
+    if (!kCluster && tid == 0) a.ws.start[w.u] = w.start;
     w.at = stop;
   }
   if (!ok) report(a.dev_status, FVA_DEVERR_TIMEOUT);
+  if constexpr (kCluster) join_cluster<T, D>(a, unit, reinterpret_cast<float*>(ring));
 }
 
 // ---------------------------------------------------------------------------------
@@ -547,7 +627,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&x)[V]) {
   else p[0] = x[0];
 }
 
-template <int D, int G>
+template <int D, int G, bool kCluster>
 __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float> a, SplitWaits waits) {
   using Cfg = SplitF32Cfg<D>;
   constexpr int V = D / 32, kHalf = D / 8;  // kHalf: 16-byte pieces of half a row
@@ -570,8 +650,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
   }
   grid_wait();
   grid_release();
-  const Share sh = find_share(a, share);  // (its barriers publish the mbarriers too)
-  Walk<float> w(sh, share);
+  auto w = make_walk<float, kCluster>(a);
+  const int unit = w.u;
   volatile int* abort_flag = &s_abort;
   if (warp == 4) {
     feed_pages(a, w, full, empty, s_valid, abort_flag, waits, Cfg::kStages, [&](int stage, int page, int h) {
@@ -580,6 +660,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
       bulk_load(ring + stage * 2 * Cfg::kTile, a.c.k + at, Cfg::kTile, &full[stage]);
       bulk_load(ring + stage * 2 * Cfg::kTile + Cfg::kTile, a.c.v + at, Cfg::kTile, &full[stage]);
     });
+    if constexpr (kCluster) join_cluster<float, D>(a, unit, reinterpret_cast<float*>(ring));
     return;
   }
 
@@ -694,8 +775,12 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
       }
     }
     sync4();
-    const bool whole = w.whole();
-    const int slot = w.slot();
+    bool whole = false;  // finished here; else the sums go to `parts`, rows of D + 2
+    float* parts = reinterpret_cast<float*>(ring);
+    if constexpr (!kCluster) {
+      whole = w.whole();
+      parts = a.ws.part + (static_cast<int64_t>(share) * 2 + w.slot()) * kGroup * (D + 2);
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const float mx = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
@@ -730,18 +815,19 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
 #pragma unroll
         for (int v = 0; v < 4; ++v) sum += s_l[v][g] * (s_m[v][g] == -INFINITY ? 0.0f : exp2f(s_m[v][g] - m[g]));
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        float* out = whole ? a.o + (row0 + g) * D
-                           : a.ws.part + ((static_cast<int64_t>(share) * 2 + slot) * kGroup + g) * (D + 2);
+        float* out = whole ? a.o + (row0 + g) * D : parts + g * (D + 2);
 #pragma unroll
         for (int i = 0; i < V; ++i) out[lane * V + i] = whole ? acc[g][i] * inv : acc[g][i];
-        if (lane == 0) put_stats<float, D>(a, whole, share, slot, row0 + g, g, m[g], sum);
+        if (lane == 0 && whole) put_lse(a, row0 + g, m[g], sum);
+        if (lane == 0 && !whole) out[D] = m[g], out[D + 1] = sum;
       }
     }
-    if (tid == 0) a.ws.start[w.u] = w.start;
+    if (!kCluster && tid == 0) a.ws.start[w.u] = w.start;
     sync4();  // the next unit rewrites what was read here
     w.at = stop;
   }
   if (!ok) report(a.dev_status, FVA_DEVERR_TIMEOUT);
+  if constexpr (kCluster) join_cluster<float, D>(a, unit, reinterpret_cast<float*>(ring));
 }
 
 // ---------------------------------------------------------------------------------
@@ -750,11 +836,12 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
 // CTA (x, key head, sequence), 0 < x: forms the heads' log-sum-exp from the shares' maxima and
 // sums and adds exp(s - lse), summed over the heads, to the masses of pieces x - 1, x - 1 + (the
 // grid's x less one), .. of 16 listed blocks. x = 0 joins the shares' O, a warp per head. Little
-// is moved: what such a CTA takes is its chain of dependent loads.
+// is moved: what such a CTA takes is its chain of dependent loads. `joined`: the clusters of the
+// split kernel have finished every row.
 constexpr int kJoinThreads = 256, kMassBlocks = 16;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a, bool joined) {
   __shared__ float s_lse[kMaxCacheGroup];
   __shared__ int s_page[kMassBlocks], s_valid[kMassBlocks];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -764,7 +851,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
   grid_release();
   const int len = seq_len(a.c, b, nullptr), n = unit_count(a, bh * a.GS, nullptr);
   const int first = joins ? 0 : (blockIdx.x - 1) * kMassBlocks;
-  if (!joins && first >= n) return;
+  if (joins ? joined : first >= n) return;
   auto find_pages = [&](int pos0) {
     if (tid < kMassBlocks) {
       const int pos = pos0 + tid;
@@ -781,9 +868,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnView<T> a) {
   if (!joins) find_pages(first);
   // A head without a finite score weighs nothing: exp2(-inf - inf) is 0, -inf - -inf is NaN.
   auto weightless = [](float l2) { return l2 == -INFINITY ? INFINITY : l2; };
-  const int64_t per = n ? *a.ws.per : 1;
+  const int64_t per = n && !joined ? *a.ws.per : 1;
   for (int g = warp; g < a.G; g += kJoinThreads / 32) {
     const int64_t row = static_cast<int64_t>(b) * a.H + h * a.G + g;
+    if (joined) {
+      if (lane == 0) s_lse[g] = weightless(a.ws.lse[row]);
+      continue;
+    }
     const int64_t start = n ? a.ws.start[bh * a.GS + g / kGroup] : 0;
     const int c0 = static_cast<int>(start / per), c1 = n ? static_cast<int>((start + n - 1) / per) : c0;
     if (c0 < 0 || c1 < c0 || c1 >= kShares) continue;  // (never: whatever the workspace holds, no access leaves it)
@@ -884,32 +975,49 @@ static bool make_page_map(CUtensorMap* map, const void* base, const fva_cache* c
   return make_rows_map(map, base, c->n_pages, static_cast<int64_t>(c->Hkv) * kBlock, c->d, c->dtype == FVA_F16);
 }
 
-template <int D, int G>
-static cudaError_t launch_f32(const AttnView<float>& a, cudaStream_t st) {
-  using Cfg = SplitF32Cfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(split_f32_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_chained(split_f32_kernel<D, G>, dim3(Cfg::kUseShares), kSplitThreads, 0, Cfg::kSmem, st, a,
-                        SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
+// CTAs of a unit's cluster, or 0: shares and a second launch. A cluster saves the launch and the
+// trip through global memory, but leaves CTAs unused where there are few units and balances
+// nothing between them. Routing and attention of one sequence (bf16, d = 128, 8 key heads of 4
+// query heads, all blocks kept) take, with clusters / shares, 28 / 29 us at 119 blocks, 35 / 36 at
+// 172, 42 / 39 at 235; of 8 sequences (fp32, d = 64, 12 heads, all kept) 25 / 30 us at 24 blocks,
+// 37 / 42 at 47.
+static int cluster_parts(int units, int max_blocks, int resident) {
+  int parts = 1;
+  while (parts < kMaxParts && units * parts * 2 <= resident) parts *= 2;
+  return units * parts <= resident && (max_blocks + parts - 1) / parts <= kPartBlocks ? parts : 0;
 }
 
+template <typename... Params, typename... Args>
+static cudaError_t launch_split_grid(void (*kernel)(Params...), int grid, int parts, size_t smem, cudaStream_t st,
+                                     const Args&... args) {
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_chained(kernel, dim3(static_cast<unsigned>(grid)), kSplitThreads, parts, smem, st, args...);
+}
+
+template <int D, int G>
+static cudaError_t launch_f32(const AttnView<float>& a, int parts, cudaStream_t st) {
+  using Cfg = SplitF32Cfg<D>;
+  return launch_split_grid(parts ? split_f32_kernel<D, G, true> : split_f32_kernel<D, G, false>,
+                           parts ? a.units * parts : Cfg::kUseShares, parts, Cfg::kSmem, st, a,
+                           SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
+}
+
+// parts: of a cluster per unit; 0: shares.
 template <typename T, int D>
-static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, cudaStream_t st) {
+static cudaError_t launch_split(const fva_cache* c, const AttnView<T>& a, int parts, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     CUtensorMap mk, mv;
     if (!make_page_map(&mk, c->k, c) || !make_page_map(&mv, c->v, c)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(split_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               SplitCfg<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_chained(split_kernel<T, D>, dim3(kShares), kSplitThreads, 0, SplitCfg<D>::kSmem, st, mk, mv, a,
-                          SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
+    return launch_split_grid(parts ? split_kernel<T, D, true> : split_kernel<T, D, false>, parts ? a.units * parts : kShares,
+                             parts, SplitCfg<D>::kSmem, st, mk, mv, a, SplitWaits{attn_wait_limit_ns(), attn_diag_flags()});
   } else {
     const int g = a.G < kGroup ? a.G : kGroup;
-    return g <= 1   ? launch_f32<D, 1>(a, st)
-           : g <= 2 ? launch_f32<D, 2>(a, st)
-           : g <= 4 ? launch_f32<D, 4>(a, st)
-           : g <= 8 ? launch_f32<D, 8>(a, st)
-                    : launch_f32<D, 16>(a, st);
+    return g <= 1   ? launch_f32<D, 1>(a, parts, st)
+           : g <= 2 ? launch_f32<D, 2>(a, parts, st)
+           : g <= 4 ? launch_f32<D, 4>(a, parts, st)
+           : g <= 8 ? launch_f32<D, 8>(a, parts, st)
+                    : launch_f32<D, 16>(a, parts, st);
   }
 }
 
@@ -932,8 +1040,10 @@ struct AttnCall {
     const int G = H / c->Hkv, GS = (G + kGroup - 1) / kGroup;
     const AttnView<T> a = {cache_view<T>(c, s), static_cast<const T*>(q), q_stride, kept, n_kept, H, G, GS,
                            s->B * c->Hkv * GS, scale * 1.4426950408889634f, ws, static_cast<T*>(o), lse, dev_status};
-    const cudaError_t e = launch_split<T, D>(c, a, st);
-    if (e != cudaSuccess) return e;
+    const int resident = sizeof(T) == 4 && D == 128 ? kShares / 2 : kShares;
+    const int parts = cluster_parts(a.units, s->max_blocks, resident);
+    const cudaError_t e = launch_split<T, D>(c, a, parts, st);
+    if (e != cudaSuccess || (parts && !accumulate)) return e;
     // pieces of the accumulation: about eight CTAs an SM, were every list of full length
     unsigned chunks = 0;
     if (accumulate) {
@@ -942,7 +1052,7 @@ struct AttnCall {
       chunks = static_cast<unsigned>(pieces < most ? pieces : most);
     }
     return launch_chained(join_kernel<T, D>, dim3(1 + chunks, static_cast<unsigned>(c->Hkv), static_cast<unsigned>(s->B)),
-                          kJoinThreads, 0, 0, st, a);
+                          kJoinThreads, 0, 0, st, a, parts > 0);
   }
 };
 

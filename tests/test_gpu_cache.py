@@ -638,23 +638,24 @@ def test_streams_served_together():
         add([64 * 16, 0, 0])
 
 
+@pytest.mark.parametrize("accumulate", [True, False])
 @pytest.mark.parametrize("H,Hkv,d,dtype", [(8, 2, 128, "bf16"), (20, 1, 64, "f16"), (3, 3, 32, "f32"), (8, 2, 128, "f32")])
-def test_wait_that_runs_out_is_reported(H, Hkv, d, dtype):
+def test_wait_that_runs_out_is_reported(H, Hkv, d, dtype, accumulate):
     """With the loads withheld and a 20 ms limit the attention reports a timeout, ends and leaves
     the device usable; the next call is right."""
     s = Streams([700, 64, 0, 5000], H, Hkv, d, dtype).fill()
     q = s.query()
     s.fva.fva_set_diagnostics(20_000_000, s.fva.FVA_DIAG_WITHHOLD_Q)
     try:
-        s.attn(q, None, None, accumulate=True)
+        s.attn(q, None, None, accumulate=accumulate)
         s.ok(s.fva.FVA_DEVERR_TIMEOUT)
     finally:
         s.fva.fva_set_diagnostics(0, 0)
     s.cache.mass.zero_()
     before = s.cache.mass.double().cpu().numpy()
-    o, lse = s.attn(q, None, None, accumulate=True)
+    o, lse = s.attn(q, None, None, accumulate=accumulate)
     s.ok()
-    s.check_attn(o, lse, [[np.arange(-(-n // 64))] * Hkv for n in s.lens], before)
+    s.check_attn(o, lse, [[np.arange(-(-n // 64))] * Hkv for n in s.lens], before if accumulate else None)
 
 
 @pytest.mark.parametrize("limit", [1, 2000, 20000])
@@ -779,3 +780,28 @@ def test_captured_eviction_and_append_are_replayed():
                 a, b = a[:64 * 64], b[:64 * 64]
             assert torch.equal(a, b)
     s.ok()
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(4, 4, 64, "bf16"), (16, 2, 128, "bf16"), (33, 1, 64, "f16"), (6, 2, 32, "f32"),
+                                           (20, 1, 128, "f32"), (2, 2, 64, "f32")])
+@pytest.mark.parametrize("lens", [[0], [1], [64, 0, 65], [1023, 200, 1], [1024] * 5, [63 + 64 * i for i in range(16)]])
+def test_small_calls_in_one_launch(H, Hkv, d, dtype, lens):
+    """Calls that accumulate nothing and whose lists are short: parts of a list may be empty, and a
+    sequence longer or shorter than its cluster has CTAs. Also with a kept list, and captured."""
+    import torch
+    s = Streams(lens, H, Hkv, d, dtype, seed=len(lens)).fill()
+    q = s.query()
+    o, lse = s.attn(q, None, None)
+    s.ok()
+    s.check_attn(o, lse, [[np.arange(-(-n // 64))] * Hkv for n in lens])
+    kept, n = s.route(q, 0.5, 1, 1)
+    o, lse = s.attn(q, kept, n)
+    s.ok()
+    s.check_attn(o, lse, s.want_route(0.5, 1, 1))
+    out = torch.full_like(o, float("nan"))
+    ws = s.ws(s.fva.fva_cache_attn_workspace_bytes(s.cache, s.B, s.max_blocks, H, False))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.fva.fva_cache_attn(s.cache, s.table, s.length, q, kept, n, out, ws)
+    g.replay()
+    assert torch.equal(out, o)
