@@ -805,3 +805,30 @@ def test_small_calls_in_one_launch(H, Hkv, d, dtype, lens):
         s.fva.fva_cache_attn(s.cache, s.table, s.length, q, kept, n, out, ws)
     g.replay()
     assert torch.equal(out, o)
+
+
+def test_evict_among_very_many_pages():
+    """More pages than the destination check holds at a time: a clash among the last ones is
+    found, and the rows of far pages (offsets beyond 32 bits) arrive where they should."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import fva
+    n_pages, d = 600_000, 64
+    cache = fva.Cache.allocate(n_pages, 1, d)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[599_999, 10, 530_000, 524_288]], **i32)
+    length, st = torch.tensor([200], **i32), torch.zeros(1, **i32)
+    x = torch.randn(200, 1, d, device="cuda").bfloat16()
+    y = torch.randn(200, 1, d, device="cuda").bfloat16()
+    fva.fva_cache_append(cache, table, length, x, y, torch.tensor([0, 200], **i32), 200, st)
+    cache.mass[table[0].long()] = torch.rand(4, 1, 64, device="cuda")
+    before = cache.k[524_288].clone()
+    kept, new_len = torch.empty((1, 1, 128), **i32), torch.empty(1, **i32)
+    ws = torch.empty(fva.fva_cache_evict_workspace_bytes(cache, 1, 4), dtype=torch.uint8, device="cuda")
+    for dst, code in (([524_288, 599_998], fva.FVA_DEVERR_BAD_LIST), ([524_287, 599_998], 0)):
+        fva.fva_cache_evict(cache, table, length, 128, 2, 8, torch.tensor([dst], **i32), kept, new_len, ws, dev_status=st)
+        assert int(st.item()) == code
+        st.zero_()
+        at = kept[0, 0].long()
+        assert torch.equal(cache.k[599_998, 0], x[at[64:], 0]) and torch.equal(cache.v[599_998, 0], y[at[64:], 0])
+        assert torch.equal(cache.k[524_288], before)
+    assert torch.equal(cache.k[524_287, 0], x[at[:64], 0]) and torch.equal(cache.v[524_287, 0], y[at[:64], 0])
