@@ -27,6 +27,10 @@
 //   * The statistics of a 64-row block, -lse2 and -D, are one 512-byte piece (see
 //     prepare_kernel): the key kernel streams it with Q and dO. Rows without keys and rows
 //     past N have -lse2 = -infinity, so their P is 0.
+//   * Measured: 21 x 30 x 52 tokens, 16 heads, d = 128, a quarter of the blocks: 9.0 ms in a
+//     stream of calls, 1.35 PFLOP/s of executed products under the power cap, 7.8 alone (tensor
+//     pipe 72% of a small case's cycles); 13 x 30 x 45 tokens, 32 heads, d = 64: 4.0 and 3.5 ms,
+//     bound by the warps that form P and dS (issue 52%).
 //   * Every wait is bounded; on expiry the CTA reports FVA_DEVERR_TIMEOUT, drains its own
 //     loads and products, frees TMEM and exits.
 #include <math.h>
