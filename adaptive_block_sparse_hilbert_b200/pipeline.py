@@ -19,6 +19,8 @@ token by token from a paged cache:
 """
 from __future__ import annotations
 
+import itertools
+
 import torch
 
 from . import fva
@@ -172,23 +174,26 @@ class CachedAttention:
             raise ValueError("CachedAttention.append: a stream would outgrow max_blocks")
         if sum(need) > len(self.free):
             raise RuntimeError(f"CachedAttention.append: {sum(need)} pages needed, {len(self.free)} free")
-        grown = [b for b in range(self.B) if need[b]]
-        for b, n in enumerate(need):
-            self.pages[b] += [self.free.pop() for _ in range(n)]
-            self.lengths[b] += counts[b]
-        self._publish(grown, st)
-        ptr = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
-        try:
-            with torch.cuda.device(self.table.device), torch.cuda.stream(st):
-                new_ptr = ptr.to(self.table.device)
-                fva.fva_cache_append(self.cache, self.table, self.length, k_new, v_new, new_ptr, max(counts),
-                                     self.dev_status, st)
-        except (ValueError, fva.FvaError):  # refused: nothing ran
-            for b, n in reversed(list(enumerate(need))):
-                self.free += [self.pages[b].pop() for _ in range(n)]
-                self.lengths[b] -= counts[b]
-            self._publish([], st)
-            raise
+        # What can fail comes before what the streams are known by: a failed call leaves them as
+        # they were (table entries behind a stream's last block are not read).
+        total = sum(need)
+        fresh = self.free[len(self.free) - total:][::-1]
+        lengths = [n + c for n, c in zip(self.lengths, counts)]
+        ptr = [0, *itertools.accumulate(counts)]
+        with torch.cuda.device(self.table.device), torch.cuda.stream(st):
+            ints = torch.tensor(lengths + ptr, dtype=torch.int32).to(self.table.device)
+            if total:
+                at = [b * self.max_blocks + len(p) + i for b, (p, n) in enumerate(zip(self.pages, need)) for i in range(n)]
+                both = torch.tensor([at, fresh]).to(self.table.device)
+                self.table.view(-1)[both[0]] = both[1].to(torch.int32)
+            fva.fva_cache_append(self.cache, self.table, ints[:self.B], k_new, v_new, ints[self.B:], max(counts),
+                                 self.dev_status, st)
+            self.length.copy_(ints[:self.B])
+        self.lengths = lengths
+        del self.free[len(self.free) - total:]
+        pages = iter(fresh)
+        for held, n in zip(self.pages, need):
+            held += itertools.islice(pages, n)
 
     def attend(self, q, o, stream=None, scale: float = 0.0):
         """o [B, H, d] = attention of the query tokens q [B, H, d]; the choice is left in

@@ -1,0 +1,95 @@
+"""CachedAttention's host side: page and length bookkeeping, with the entry points replaced by
+host versions over CPU tensors (what they compute is tested on the GPU)."""
+import contextlib
+
+import pytest
+import torch
+
+from adaptive_block_sparse_hilbert_b200 import fva, pipeline
+
+HKV, D = 2, 64
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """make(B, n_pages, max_blocks) -> a CachedAttention on the CPU; make.calls: its appends."""
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
+    calls = []
+
+    def append(cache, table, length, k_new, v_new, new_ptr, max_new, dev_status=None, stream=None):
+        calls.append((table.clone(), length.tolist(), new_ptr.tolist(), max_new))
+        for b, n in enumerate(length.tolist()):
+            lo, hi = new_ptr[b].item(), new_ptr[b + 1].item()
+            for t in range(lo, hi):
+                at = n - (hi - t)
+                page = int(table[b, at // 64])
+                cache.k[page, :, at % 64], cache.v[page, :, at % 64] = k_new[t], v_new[t]
+                cache.mass[page, :, at % 64] = 0.0
+    monkeypatch.setattr(fva, "fva_cache_append", append)
+
+    def make(B=2, n_pages=12, max_blocks=8):
+        return pipeline.CachedAttention(B, 2 * HKV, HKV, D, n_pages, max_blocks, device="cpu")
+    make.calls = calls
+    return make
+
+
+def tokens(n, seed=0):
+    return torch.randn(n, HKV, D, generator=torch.Generator().manual_seed(seed)).bfloat16()
+
+
+def state(att):
+    """What a caller can see: free pages, every stream's pages and length, on host and device."""
+    used = [att.table[b, :len(p)].tolist() for b, p in enumerate(att.pages)]
+    return sorted(att.free), [list(p) for p in att.pages], list(att.lengths), att.length.tolist(), used
+
+
+def check(att):
+    """Every page belongs to one stream or is free, and the device's copies say the same."""
+    _, pages, lengths, length, used = state(att)
+    assert sorted(att.free + sum(pages, [])) == list(range(att.cache.k.shape[0]))
+    assert lengths == length and used == pages
+    assert [len(p) for p in pages] == [-(-n // 64) for n in lengths]
+
+
+def held(att, b):
+    """A stream's keys in order, read through the device's table."""
+    at = torch.arange(att.lengths[b])
+    return att.cache.k[att.table[b, at // 64].long(), :, at % 64]
+
+
+def test_append_books_pages_and_lengths(streams):
+    att = streams()
+    x = tokens(300)
+    att.append(x[:100], x[:100], [70, 30])
+    att.append(x[100:230], x[100:230], [0, 130])
+    att.append(x[230:231], x[230:231], [1, 0])
+    check(att)
+    assert att.lengths == [71, 160] and len(att.free) == 12 - 2 - 3
+    assert torch.equal(held(att, 0), torch.cat([x[:70], x[230:231]]))
+    assert torch.equal(held(att, 1), torch.cat([x[70:100], x[100:230]]))
+    assert streams.calls[1][1:] == ([70, 160], [0, 0, 130], 130)
+
+
+@pytest.mark.parametrize("where", ["copy", "call"])
+@pytest.mark.parametrize("error", [RuntimeError, MemoryError, KeyboardInterrupt])
+def test_append_that_fails_changes_nothing(streams, monkeypatch, where, error):
+    """An error of any kind, in the copies to the device (memory, a capture in progress) or in the
+    call itself, takes no page and counts no token that was not stored."""
+    att = streams()
+    x = tokens(200)
+    att.append(x[:100], x[:100], [70, 30])
+    before = state(att)
+
+    def fails(*a, **k):
+        raise error("no")
+    with monkeypatch.context() as m:
+        m.setattr(*((torch.Tensor, "to") if where == "copy" else (fva, "fva_cache_append")), fails)
+        for counts in ([60, 40], [1, 1]):  # new pages, and none
+            with pytest.raises(error):
+                att.append(x[:sum(counts)], x[:sum(counts)], counts)
+            assert state(att) == before
+    att.append(x[100:], x[100:], [60, 40])
+    check(att)
+    assert torch.equal(held(att, 0), torch.cat([x[:70], x[100:160]]))
