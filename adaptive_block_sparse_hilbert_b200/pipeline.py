@@ -150,16 +150,6 @@ class CachedAttention:
         self.pages = [[] for _ in range(B)]   # host copies of the table's rows and the lengths
         self.lengths = [0] * B
 
-    def _publish(self, changed, stream):
-        """The lengths, and the table's rows of the streams in `changed`, to the device."""
-        with torch.cuda.device(self.table.device), torch.cuda.stream(stream):
-            if changed:
-                rows = torch.zeros((len(changed), self.max_blocks), dtype=torch.int32)
-                for i, b in enumerate(changed):
-                    rows[i, :len(self.pages[b])] = torch.tensor(self.pages[b], dtype=torch.int32)
-                self.table[torch.tensor(changed, device=self.table.device)] = rows.to(self.table.device)
-            self.length.copy_(torch.tensor(self.lengths, dtype=torch.int32))
-
     def _stream(self, stream):
         return torch.cuda.current_stream(self.table.device) if stream is None else stream
 
@@ -216,20 +206,26 @@ class CachedAttention:
         need = [-(-n // fva.BLOCK) for n in after]
         if sum(need) > len(self.free):
             raise RuntimeError(f"CachedAttention.evict: {sum(need)} pages needed, {len(self.free)} free")
-        fresh = [[self.free.pop() for _ in range(n)] for n in need]
+        pool = iter(self.free[::-1])
+        fresh = [list(itertools.islice(pool, n)) for n in need]
         rows = torch.full((self.B, room), -1, dtype=torch.int32)
         for b, pages in enumerate(fresh):
             rows[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
+        # As in append(): what can fail comes before what the streams are known by.
         with torch.cuda.device(self.table.device), torch.cuda.stream(st):
             dst = rows.to(self.table.device)
             kept = torch.empty((self.B, self.cache.k.shape[1], int(keep)), dtype=torch.int32, device=dst.device)
-            new_len = torch.empty_like(self.length)
+            new_len, table = torch.empty_like(self.length), torch.zeros_like(self.table)
+            width = min(room, self.max_blocks)
+            table[:, :width] = dst[:, :width].clamp(min=0)
             fva.fva_cache_evict(self.cache, self.table, self.length, keep, n_sink, n_recent, dst, kept, new_len,
                                 self.evict_ws, self.dev_status, st)
-        for b, pages in enumerate(fresh):
-            self.free += self.pages[b][::-1]
-            self.pages[b], self.lengths[b] = pages, after[b]
-        self._publish(list(range(self.B)), st)
+            self.table.copy_(table)
+            self.length.copy_(new_len)
+        del self.free[len(self.free) - sum(need):]
+        for pages in self.pages:
+            self.free += pages[::-1]
+        self.pages, self.lengths = fresh, after
         return kept
 
 

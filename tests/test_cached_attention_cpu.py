@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from adaptive_block_sparse_hilbert_b200 import fva, pipeline
+from oracle import cache_oracle as CO
 
 HKV, D = 2, 64
 
@@ -28,6 +29,20 @@ def streams(monkeypatch):
                 cache.k[page, :, at % 64], cache.v[page, :, at % 64] = k_new[t], v_new[t]
                 cache.mass[page, :, at % 64] = 0.0
     monkeypatch.setattr(fva, "fva_cache_append", append)
+
+    def evict(cache, table, length, keep, n_sink, n_recent, dst_table, kept, new_len, workspace, dev_status=None,
+              stream=None):
+        kept.fill_(-1)
+        for b, n in enumerate(length.tolist()):
+            at, m = torch.arange(n), min(n, keep)
+            rows = [x[table[b, at // 64].long(), :, at % 64] for x in (cache.k, cache.v, cache.mass)]
+            new_len[b] = m
+            to = torch.arange(m)
+            for g in range(HKV):
+                kept[b, g, :m] = torch.from_numpy(CO.evict(rows[2][:, g].numpy(), keep, n_sink, n_recent))
+                for x, r in zip((cache.k, cache.v, cache.mass), rows):
+                    x[dst_table[b, to // 64].long(), g, to % 64] = r[kept[b, g, :m].long(), g]
+    monkeypatch.setattr(fva, "fva_cache_evict", evict)
 
     def make(B=2, n_pages=12, max_blocks=8):
         return pipeline.CachedAttention(B, 2 * HKV, HKV, D, n_pages, max_blocks, device="cpu")
@@ -93,3 +108,27 @@ def test_append_that_fails_changes_nothing(streams, monkeypatch, where, error):
     att.append(x[100:], x[100:], [60, 40])
     check(att)
     assert torch.equal(held(att, 0), torch.cat([x[:70], x[100:160]]))
+
+
+@pytest.mark.parametrize("where", ["copy", "memory", "call"])
+@pytest.mark.parametrize("error", [RuntimeError, MemoryError, KeyboardInterrupt])
+def test_evict_that_fails_changes_nothing(streams, monkeypatch, where, error):
+    """An error of any kind before or in the call loses no page and cuts no stream."""
+    att = streams()
+    x = tokens(300)
+    att.append(x, x, [200, 100])
+    before, keys = state(att), held(att, 0)
+
+    def fails(*a, **k):
+        raise error("no")
+    at = {"copy": (torch.Tensor, "to"), "memory": (torch, "empty"), "call": (fva, "fva_cache_evict")}[where]
+    with monkeypatch.context() as m:
+        m.setattr(*at, fails)
+        for _ in range(3):
+            with pytest.raises(error):
+                att.evict(128, 2, 8)
+            assert state(att) == before
+    assert torch.equal(held(att, 0), keys)
+    kept = att.evict(128, 2, 8)
+    check(att)
+    assert att.lengths == [128, 100] and torch.equal(held(att, 0)[:, 1], keys[kept[0, 1].long(), 1])
