@@ -196,36 +196,50 @@ class CachedAttention:
 
     def evict(self, keep: int, n_sink: int = 4, n_recent: int = 64, stream=None):
         """Cut every stream to at most `keep` tokens; returns the kept tokens' old positions
-        (int32 [B, Hkv, keep], -1 behind them). Their old pages are free afterwards."""
+        (int32 [B, Hkv, keep], -1 behind them). A stream within the budget is left where it is. The
+        others move to new pages and give back their old ones, as many at a time as there are
+        pages free: those of one (ceil(keep / 64)) are enough."""
         st = self._stream(stream)
         if not 1 <= keep <= 1 << 20 or min(n_sink, n_recent) < 0 or n_sink + n_recent > keep:
             raise ValueError(f"CachedAttention.evict: keep {keep}, first {n_sink}, last {n_recent}: expected 1 <= keep <= "
                              f"2^20 and both ends within it")
-        room = -(-int(keep) // fva.BLOCK)
-        after = [min(n, int(keep)) for n in self.lengths]
-        need = [-(-n // fva.BLOCK) for n in after]
-        if sum(need) > len(self.free):
-            raise RuntimeError(f"CachedAttention.evict: {sum(need)} pages needed, {len(self.free)} free")
-        pool = iter(self.free[::-1])
-        fresh = [list(itertools.islice(pool, n)) for n in need]
-        rows = torch.full((self.B, room), -1, dtype=torch.int32)
-        for b, pages in enumerate(fresh):
-            rows[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
-        # As in append(): what can fail comes before what the streams are known by.
+        keep, room = int(keep), -(-int(keep) // fva.BLOCK)
+        cut = [b for b, n in enumerate(self.lengths) if n > keep]
+        if cut and room > len(self.free):
+            raise RuntimeError(f"CachedAttention.evict: {room} pages needed, {len(self.free)} free")
+        free, fresh, groups = list(self.free), [], []  # (a group: its range of `cut`)
+        while len(fresh) < len(cut):
+            first = len(fresh)
+            end = min(len(cut), first + len(free) // room)
+            fresh += [[free.pop() for _ in range(room)] for _ in range(first, end)]
+            for b in cut[first:end]:
+                free += self.pages[b][::-1]
+            groups.append(slice(first, end))
+        # As in append(): what can fail comes before what the streams are known by, and before the
+        # first group's old pages may be written.
         with torch.cuda.device(self.table.device), torch.cuda.stream(st):
-            dst = rows.to(self.table.device)
-            kept = torch.empty((self.B, self.cache.k.shape[1], int(keep)), dtype=torch.int32, device=dst.device)
-            new_len, table = torch.empty_like(self.length), torch.zeros_like(self.table)
-            width = min(room, self.max_blocks)
-            table[:, :width] = dst[:, :width].clamp(min=0)
-            fva.fva_cache_evict(self.cache, self.table, self.length, keep, n_sink, n_recent, dst, kept, new_len,
-                                self.evict_ws, self.dev_status, st)
-            self.table.copy_(table)
-            self.length.copy_(new_len)
-        del self.free[len(self.free) - sum(need):]
-        for pages in self.pages:
-            self.free += pages[::-1]
-        self.pages, self.lengths = fresh, after
+            every = torch.arange(keep, dtype=torch.int32, device=self.table.device)
+            kept = torch.empty((self.B, self.cache.k.shape[1], keep), dtype=torch.int32, device=self.table.device)
+            some = len(cut) < self.B
+            if some:
+                kept.copy_(torch.where(every < self.length[:, None], every, -1)[:, None])
+            if cut:
+                both = torch.tensor([[b, *pages] for b, pages in zip(cut, fresh)]).to(self.table.device)
+                at, dst = both[:, 0], both[:, 1:].to(torch.int32)
+                # the streams that are cut, side by side
+                table, length, out = (x[at] if some else x for x in (self.table, self.length, kept))
+                new_len, new_table = torch.empty_like(length), torch.zeros_like(table)
+                new_table[:, :room] = dst
+                for g in groups:
+                    fva.fva_cache_evict(self.cache, table[g], length[g], keep, n_sink, n_recent, dst[g], out[g], new_len[g],
+                                        self.evict_ws, self.dev_status, st)
+                self.table[at], self.length[at] = new_table, new_len
+        self.free = free
+        for b, pages in zip(cut, fresh):
+            self.pages[b], self.lengths[b] = pages, keep
+        if cut and some:
+            with torch.cuda.device(self.table.device), torch.cuda.stream(st):
+                kept[at] = out
         return kept
 
 

@@ -132,3 +132,50 @@ def test_evict_that_fails_changes_nothing(streams, monkeypatch, where, error):
     kept = att.evict(128, 2, 8)
     check(att)
     assert att.lengths == [128, 100] and torch.equal(held(att, 0)[:, 1], keys[kept[0, 1].long(), 1])
+
+
+def evicted(att, keep, sink, recent):
+    """Evict with random masses and compare every stream with what it held before."""
+    att.cache.mass.uniform_(0, 1)
+    pages, lengths = [list(p) for p in att.pages], list(att.lengths)
+    read = lambda x, b: x[att.table[b, torch.arange(att.lengths[b]) // 64].long(), :, torch.arange(att.lengths[b]) % 64]  # noqa: E731
+    old = [[read(x, b) for x in (att.cache.k, att.cache.v, att.cache.mass)] for b in range(att.B)]
+    kept = att.evict(keep, sink, recent)
+    check(att)
+    for b, n in enumerate(lengths):
+        m = min(n, keep)
+        assert att.lengths[b] == m and (n > keep or att.pages[b] == pages[b])  # no need to move: not moved
+        new = [read(x, b) for x in (att.cache.k, att.cache.v, att.cache.mass)]
+        for g in range(HKV):
+            want = CO.evict(old[b][2][:, g].numpy(), keep, sink, recent)
+            assert kept[b, g].tolist() == want.tolist() + [-1] * (keep - m)
+            assert all(torch.equal(x[:, g], y[want, g]) for x, y in zip(new, old[b]))
+    return kept
+
+
+@pytest.mark.parametrize("n_pages,lens,keep", [
+    (12, [200, 100, 0, 64], 64),          # room for all that are cut
+    (9, [200, 100, 64, 1], 200),          # nothing to cut, and a single page free
+    (9, [200, 64, 64, 64], 100),          # one of four, and just the two pages for it
+    (15, [200, 130, 190, 140], 70),       # all are cut, one at a time: two pages are free
+    (18, [128, 320, 100, 321], 130),      # two of four, one at a time, out of order with the others
+    (9, [65, 129, 63, 65], 64),           # a page is enough
+])
+def test_evict_needs_pages_only_for_what_it_cuts(streams, n_pages, lens, keep):
+    att = streams(B=4, n_pages=n_pages)
+    x = tokens(sum(lens))
+    att.append(x, x.flip(0), lens)
+    evicted(att, keep, 3, 10)
+    att.append(x[:4], x[:4], [1] * 4)
+    check(att)
+
+
+def test_evict_without_a_page_is_refused(streams):
+    att = streams(B=2, n_pages=6)
+    x = tokens(300)
+    att.append(x, x, [200, 100])
+    before = state(att)
+    with pytest.raises(RuntimeError):
+        att.evict(64, 2, 8)
+    assert state(att) == before
+    evicted(att, 200, 2, 8)
