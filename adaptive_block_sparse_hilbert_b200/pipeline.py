@@ -102,12 +102,14 @@ class SparseAttentionLayer:
 
     def backward(self, do, dq, dk, dv, stream=None):
         """Gradients of the last forward() (train=True) for the output gradient `do`; all
-        [B, N, H, d] in raster order. The routed mask is a constant of the gradient."""
+        [B, N, H, d] in raster order, contiguous. The routed mask is a constant of the gradient."""
         if not self.train:
             raise RuntimeError("SparseAttentionLayer.backward: the layer was made without train=True")
         if self.scale is None:
             raise RuntimeError("SparseAttentionLayer.backward: no forward() to take the gradient of")
         s = self.shape
+        for what, t in (("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
+            fva._expect("SparseAttentionLayer.backward", what, t, (s.B, self.N, s.H, s.d), self.dtype, self.perm.device)
         fva.fva_reorder(s, do, self.doh, None, self.perm, fva.FVA_FWD, stream)
         fva.fva_sparse_attn_bwd(s, self.qh, self.kh, self.vb, self.oh, self.doh, self.lse, self.mask, self.dqh, self.dkh,
                                 self.dvh, self.bwd_workspace, self.scale, self.dev_status, stream)
