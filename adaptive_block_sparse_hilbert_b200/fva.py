@@ -439,11 +439,15 @@ def _shape_dtype(s):
 
 
 def _mask_on(fn, s, N, mask, device):
+    """The mask as fva_mask; one of tensors is checked for its size and device."""
+    if not isinstance(mask, Mask):
+        return mask
     nB = -(-N // BLOCK)
     if mask.row_ptr.numel() <= s.B * s.H * nB or mask.worklist.numel() < s.B * s.H * ((nB + 1) // 2):
         raise ValueError(f"{fn}: the mask is one of another shape")
     if mask.row_ptr.device != device or mask.tile_col.device != device or mask.worklist.device != device:
         raise ValueError(f"{fn}: the mask is on {mask.row_ptr.device}, expected {device}")
+    return mask.c()
 
 
 def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=None, stream=None):
@@ -454,9 +458,9 @@ def fva_sparse_attn_lse(s, q, k, v, mask: Mask, o, lse, scale=0.0, dev_status=No
         _expect(fn, what, t, four, _shape_dtype(s), dev)
     _expect(fn, "v", v, four, v.dtype if v.dtype in (torch.float16, torch.bfloat16) else _shape_dtype(s), dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _mask_on(fn, s, N, mask, dev)
+    m = _mask_on(fn, s, N, mask, dev)
     _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(v),
-          ctypes.byref(mask.c()), o.data_ptr(), lse.data_ptr(), float(scale), _status(fn, dev_status, dev))
+          ctypes.byref(m), o.data_ptr(), lse.data_ptr(), float(scale), _status(fn, dev_status, dev))
 
 
 def fva_sparse_attn_bwd_workspace_bytes(s): return _lib.fva_sparse_attn_bwd_workspace_bytes(ctypes.byref(s))
@@ -471,10 +475,10 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
     for what, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do), ("dq", dq), ("dk", dk), ("dv", dv)):
         _expect(fn, what, t, four, dt, dev)
     _expect(fn, "lse", lse, four[:3], torch.float32, dev)
-    _mask_on(fn, s, N, mask, dev)
+    m = _mask_on(fn, s, N, mask, dev)
     size, ws, status = _scratch(fn, workspace, dev_status, dev)
     _call(fn, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-          lse.data_ptr(), ctypes.byref(mask.c()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), float(scale), ws, size,
+          lse.data_ptr(), ctypes.byref(m), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), float(scale), ws, size,
           status)
 
 
