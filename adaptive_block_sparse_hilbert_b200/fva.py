@@ -484,9 +484,10 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
 
 # ------------------------------------------------------------------------------ serving
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class Cache:
-    """Device buffers of one paged key/value cache (owned by torch; passed to libfva as fva_cache)."""
+    """Device buffers of one paged key/value cache (owned by torch; passed to libfva as fva_cache).
+    Frozen: the struct is filled once, so other buffers need another Cache."""
 
     k: torch.Tensor         # [n_pages, Hkv, 64, d]
     v: torch.Tensor
@@ -503,8 +504,9 @@ class Cache:
         _expect("Cache", "key_mean", self.key_mean, (n, Hkv, d), torch.float32, dev)
         if self.mass is not None:
             _expect("Cache", "mass", self.mass, (n, Hkv, BLOCK), torch.float32, dev)
-        self._c = fva_cache(self.k.data_ptr(), self.v.data_ptr(), self.key_mean.data_ptr(),
-                            None if self.mass is None else self.mass.data_ptr(), n, Hkv, d, _dtype_code(self.k))
+        c = fva_cache(self.k.data_ptr(), self.v.data_ptr(), self.key_mean.data_ptr(),
+                      None if self.mass is None else self.mass.data_ptr(), n, Hkv, d, _dtype_code(self.k))
+        object.__setattr__(self, "_c", c)
 
     @staticmethod
     def allocate(n_pages, Hkv, d, dtype=torch.bfloat16, device="cuda", mass=True) -> "Cache":

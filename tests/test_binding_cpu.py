@@ -21,3 +21,13 @@ def test_masks_as_tensors_or_as_the_struct(backward):
     small = fva.Mask.allocate(fva.make_shape(1, 1, 64, 1, 8, 8), "cpu")
     with pytest.raises(ValueError, match="another shape"):
         fva.fva_sparse_attn_lse(s, *x[:3], small, x[3], lse)
+
+
+def test_a_cache_keeps_to_its_buffers():
+    """The struct that the calls pass on names the buffers the object shows: others need another object."""
+    c = fva.Cache.allocate(4, 2, 64, device="cpu")
+    for name in ("k", "v", "key_mean", "mass"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, torch.zeros_like(getattr(c, name)))
+        assert getattr(c.c(), name) == getattr(c, name).data_ptr()
+    assert fva.Cache(c.k, c.v, c.key_mean).c().mass is None
