@@ -484,10 +484,10 @@ def fva_sparse_attn_bwd(s, q, k, v, o, do, lse, mask: Mask, dq, dk, dv, workspac
 
 # ------------------------------------------------------------------------------ serving
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass
 class Cache:
     """Device buffers of one paged key/value cache (owned by torch; passed to libfva as fva_cache).
-    Frozen: the struct is filled once, so other buffers need another Cache."""
+    A buffer may be replaced by one of the same sizes; other sizes need another Cache."""
 
     k: torch.Tensor         # [n_pages, Hkv, 64, d]
     v: torch.Tensor
@@ -504,9 +504,18 @@ class Cache:
         _expect("Cache", "key_mean", self.key_mean, (n, Hkv, d), torch.float32, dev)
         if self.mass is not None:
             _expect("Cache", "mass", self.mass, (n, Hkv, BLOCK), torch.float32, dev)
-        c = fva_cache(self.k.data_ptr(), self.v.data_ptr(), self.key_mean.data_ptr(),
-                      None if self.mass is None else self.mass.data_ptr(), n, Hkv, d, _dtype_code(self.k))
-        object.__setattr__(self, "_c", c)
+        self._c = fva_cache(self.k.data_ptr(), self.v.data_ptr(), self.key_mean.data_ptr(),
+                            None if self.mass is None else self.mass.data_ptr(), n, Hkv, d, _dtype_code(self.k))
+
+    def __setattr__(self, name, value):
+        made, old = "_c" in self.__dict__, self.__dict__.get(name)
+        object.__setattr__(self, name, value)
+        if made and name != "_c":  # the struct follows, or the buffer stays
+            try:
+                self.__post_init__()
+            except Exception:
+                object.__setattr__(self, name, old)
+                raise
 
     @staticmethod
     def allocate(n_pages, Hkv, d, dtype=torch.bfloat16, device="cuda", mass=True) -> "Cache":

@@ -23,11 +23,19 @@ def test_masks_as_tensors_or_as_the_struct(backward):
         fva.fva_sparse_attn_lse(s, *x[:3], small, x[3], lse)
 
 
-def test_a_cache_keeps_to_its_buffers():
-    """The struct that the calls pass on names the buffers the object shows: others need another object."""
-    c = fva.Cache.allocate(4, 2, 64, device="cpu")
+def test_a_cache_passes_on_the_buffers_it_shows():
+    """The struct names the buffers that the object holds, also after one was replaced; one that does
+    not fit the others is refused and changes nothing."""
+    c = fva.Cache.allocate(4, 2, 64, device="cpu", mass=False)
+    assert c.c().mass is None
+    c.mass = torch.zeros(4, 2, 64)
+    c.mass *= 2
     for name in ("k", "v", "key_mean", "mass"):
-        with pytest.raises(AttributeError):
-            setattr(c, name, torch.zeros_like(getattr(c, name)))
-        assert getattr(c.c(), name) == getattr(c, name).data_ptr()
-    assert fva.Cache(c.k, c.v, c.key_mean).c().mass is None
+        setattr(c, name, torch.zeros_like(getattr(c, name)))
+        for bad in (getattr(c, name)[:3], getattr(c, name).to("meta")):
+            with pytest.raises(ValueError):
+                setattr(c, name, bad)
+        assert all(getattr(c.c(), n) == getattr(c, n).data_ptr() for n in ("k", "v", "key_mean", "mass"))
+        assert c.c().n_pages == 4
+    c.mass = None
+    assert c.c().mass is None
