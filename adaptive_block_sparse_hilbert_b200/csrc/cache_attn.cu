@@ -572,10 +572,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         for (int v = 0; v < 4; ++v) sum += s_l[v][r] * (s_m[v][r] == -INFINITY ? 0.0f : exp2f(s_m[v][r] - mx));
         const int64_t row = row0 + r;
         if (whole) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const float inv = 1.0f / sum;  // (a row without weight is 0 even where 0 times its values is NaN)
           uint32_t* out = reinterpret_cast<uint32_t*>(a.o + row * D);
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) out[n * 4 + ct] = F::pack(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+          for (int n = 0; n < D / 8; ++n)
+            out[n * 4 + ct] = sum == 0.0f ? 0u : F::pack(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
         } else {
           float2* part = reinterpret_cast<float2*>(parts + r * (D + 2));
 #pragma unroll
@@ -816,10 +817,10 @@ __global__ void __launch_bounds__(kSplitThreads) split_f32_kernel(AttnView<float
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < 4; ++v) sum += s_l[v][g] * (s_m[v][g] == -INFINITY ? 0.0f : exp2f(s_m[v][g] - m[g]));
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = 1.0f / sum;  // (a row without weight is 0 even where 0 times its values is NaN)
         float* out = whole ? a.o + (row0 + g) * D : parts + g * (D + 2);
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[lane * V + i] = whole ? acc[g][i] * inv : acc[g][i];
+        for (int i = 0; i < V; ++i) out[lane * V + i] = !whole ? acc[g][i] : sum == 0.0f ? 0.0f : acc[g][i] * inv;
         if (lane == 0 && whole) put_lse(a, row0 + g, m[g], sum);
         if (lane == 0 && !whole) out[D] = m[g], out[D + 1] = sum;
       }

@@ -69,6 +69,26 @@ def test_large_scores_by_shares(dtype, d):
     s.check_attn(o, lse, [[np.arange(-(-m // 64))] for m in s.lens])
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f16", 64), ("f32", 32), ("f32", 128)])
+@pytest.mark.parametrize("streams", ["long", "many"])
+def test_weightless_rows_are_zero_whatever_their_values(dtype, d, streams):
+    """Heads whose every score is -infinity give 0 and -infinity also where the values are
+    infinite or NaN, in units inside a share and in those that cross several."""
+    s = Streams(lengths(streams), 2, 1, d, dtype, max_blocks=WIDE)
+    for k, v in zip(s.k, s.v):
+        k[:, 0, 0] = -np.inf
+        v[::3, 0, 1], v[1::3, 0, 2] = np.inf, np.nan
+    s.fill()
+    q = np.abs(s.draw(s.B, 2, d))
+    q[:, :, 0] = 1.0
+    q = s.query(q)
+    assert by_shares(s, q)
+    for accumulate in (False, True):
+        o, lse = s.attn(q, None, None, accumulate=accumulate)
+        s.ok()
+        assert bool((o == 0).all()) and bool(lse.isneginf().all())
+
+
 @pytest.mark.parametrize("accumulate", [True, False])
 @pytest.mark.parametrize("H,Hkv,d,dtype", [(8, 2, 128, "bf16"), (20, 1, 64, "f16"), (3, 3, 32, "f32"), (8, 2, 128, "f32")])
 def test_wait_that_runs_out_is_reported(H, Hkv, d, dtype, accumulate):
