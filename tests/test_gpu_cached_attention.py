@@ -37,3 +37,49 @@ def test_evict_with_few_pages_left():
             ow, _, w, _ = CO.attention(q[b, 2 * h:2 * h + 2].double().cpu().numpy(), kh, vh, np.arange(-(-len(want) // 64)))
             # eps / 2 of a bf16 output, and 2^-14 of the values for the weights
             assert (np.abs(o[b, 2 * h:2 * h + 2] - ow) <= 2.0 ** -8 * np.abs(ow) + 2.0 ** -14 * (w @ np.abs(vh))).all()
+
+
+def test_attend_captured_once_and_replayed_between_changes():
+    """One captured attend() serves the streams through appends (new pages among them) and evictions,
+    the partial kind too: every replay gives what the call would."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import pipeline
+    att = pipeline.CachedAttention(3, 8, 2, 128, n_pages=40, max_blocks=16, p=0.7, accumulate=False)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = lambda n: torch.randn(n, 2, 128, device="cuda", generator=g).bfloat16()  # noqa: E731
+    att.append(rows(700), rows(700), [0, 100, 600])
+    q = torch.randn(3, 8, 128, device="cuda", generator=g).bfloat16()
+    o, want = torch.empty_like(q), torch.empty_like(q)
+    att.attend(q, o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        att.attend(q, o)
+    changes = [lambda: att.append(rows(3), rows(3), [1, 1, 1]), lambda: att.append(rows(300), rows(300), [130, 170, 0]),
+               lambda: att.evict(200, 4, 20), lambda: att.append(rows(65), rows(65), [64, 0, 1]), lambda: att.evict(64, 4, 20),
+               lambda: att.append(rows(3), rows(3), [1, 1, 1])]
+    for change in changes:
+        change()
+        q.copy_(torch.randn(3, 8, 128, device="cuda", generator=g))
+        o.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(o, att.attend(q, want)) and not bool(o.isnan().any())
+    assert att.lengths == [65, 65, 65] and int(att.dev_status.item()) == 0
+
+
+def test_append_refused_while_a_stream_is_captured():
+    """append() reads host memory and may not be captured: it raises, and the streams stay as they were."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import pipeline
+    att = pipeline.CachedAttention(1, 2, 1, 64, n_pages=4, max_blocks=4)
+    x = torch.ones(70, 1, 64, dtype=torch.bfloat16, device="cuda")
+    att.append(x[:60], x[:60], [60])
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(graph):
+            att.append(x[:10], x[:10], [10])
+    torch.cuda.synchronize()
+    assert att.lengths == [60] and att.length.tolist() == [60] and len(att.free) == 3
+    att.append(x[:10], x[:10], [10])
+    q = torch.ones(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert bool((att.attend(q, torch.empty_like(q)) == 1).all()) and int(att.dev_status.item()) == 0
