@@ -74,7 +74,8 @@ class Large:
         assert int(self.st.item()) == 0
         return out
 
-    def check(self, lse_got, out):
+    def check(self, lse_got, out, p_rel=None):
+        """p_rel: o and lse are the forward's own, whose weights have this rounding (0: fp32)."""
         import torch
         bf, scale = self.dt == torch.bfloat16, 1 / self.d ** 0.5
         for h in range(self.H):
@@ -98,6 +99,13 @@ class Large:
                 e_p = p * (2 * e_s + 4 * n)
                 e_ds = e_p * (dp - delta).abs() + p * n * (self.d + 8) * (adp + 2 * ad) + 4 * n * ds.abs()
                 n_out = n * (self.N + 8)
+            if p_rel is not None:
+                # lse is off by `limit` at most, which scales a row's P; o by its weights' roundings, their scores'
+                # errors and a sum of N: both enter D
+                e_w = p * ((p_rel + 2 * limit)[:, None] + 2.0 ** -24 * (2 * (self.d + 8) * score + self.N + 64))
+                e_d = (e_w * adp).sum(1, keepdim=True)
+                e_ds = e_ds + p * (2 * limit[:, None] * (dp - delta).abs() + 2 * e_d)
+                e_p = e_p + 2 * p * limit[:, None]
             want = (scale * ds @ k, scale * ds.T @ q, p.T @ do)
             bounds = (scale * e_ds @ k.abs(), scale * e_ds.T @ q.abs(), e_p.T @ do.abs())
             sums = (scale * ds.abs() @ k.abs(), scale * ds.abs().T @ q.abs(), p.T @ do.abs())
@@ -114,3 +122,34 @@ def test_gradient_of_a_large_layer(case):
     out = c.backward()
     c.check(c.forward(), out)
     assert all(torch.equal(a, b) for a, b in zip(out, c.backward()))
+
+
+@pytest.mark.parametrize("B,H,T,Hg,Wg,d,dtype,v_fp16,curve", [
+    (2, 2, 3, 10, 13, 64, "bf16", True, 0), (1, 3, 3, 10, 13, 128, "bf16", False, 0), (1, 2, 4, 16, 17, 128, "bf16", True, 1),
+    (2, 2, 3, 10, 13, 64, "f32", True, 0), (1, 2, 3, 11, 12, 32, "f32", False, 1), (1, 2, 3, 10, 13, 128, "f32", True, 0),
+    (1, 1, 1, 1, 1, 64, "bf16", True, 0)])
+def test_layers_of_every_kind_train(B, H, T, Hg, Wg, d, dtype, v_fp16, curve):
+    """SparseAttentionLayer(train=True): both types, V kept as fp16 or not, both token orders, batches;
+    forward and gradients in raster order, the mask as routed."""
+    import torch
+    from adaptive_block_sparse_hilbert_b200 import fva, pipeline
+    s = fva.make_shape(B, H, d, T, Hg, Wg, dtype)
+    layer = pipeline.SparseAttentionLayer(s, 0.6, 1, v_fp16=v_fp16, curve=curve, train=True)
+    N, nB = layer.N, layer.nB
+    g = torch.Generator(device="cuda").manual_seed(N + d)
+    q, k, v, do = (torch.randn(B, N, H, d, device="cuda", generator=g).to(layer.dtype) for _ in range(4))
+    grads = [torch.full_like(q, float("nan")) for _ in range(3)]
+    o = layer.forward(2 * q, k, v, torch.empty_like(q))
+    layer.backward(do, *grads)
+    assert int(layer.dev_status.item()) == 0
+    along = lambda x: x[:, layer.perm.long()].transpose(1, 2).reshape(1, B * H, N, d)  # noqa: E731
+    assert torch.equal(along(2 * q), layer.qh.view(1, B * H, N, d)) and torch.equal(along(o), layer.oh.view(1, B * H, N, d))
+    c = object.__new__(Large)
+    c.H, c.N, c.d, c.dt, c.keep = B * H, N, d, layer.dtype, np.zeros((B * H, nB, nB), dtype=bool)
+    c.q, c.k, c.v, c.do, c.o = along(2 * q), along(k), along(v), along(do), layer.oh.view(1, B * H, N, d)
+    rp, ci = layer.mask.row_ptr.cpu().numpy(), layer.mask.col_idx.cpu().numpy()
+    for r in range(B * H * nB):
+        c.keep[r // nB, r % nB, ci[rp[r]:rp[r + 1]]] = True
+    assert nB == 1 or not c.keep.all()
+    p_rel = 0.0 if dtype == "f32" else 2.0 ** -11 if v_fp16 else 2.0 ** -8
+    c.check(layer.lse.view(1, B * H, N), [along(x) for x in grads], p_rel)
