@@ -30,7 +30,9 @@ namespace cg = cooperative_groups;
 //
 // Statistics: -lse in log2 units and -D, D_i = sum_c dO_ic O_ic, 64 rows as one 512-byte piece.
 // d * sizeof(T) / 16 lanes per row, 16 bytes each; a row without keys (lse = -inf) and the rows
-// past N of the last block get -infinity and 0, so that their P is 0.
+// past N of the last block get -infinity and 0, so that their P is 0. O is the stored one, of a
+// bf16 layer rounded to bf16: that moves dQ and dK by 2e-4 of their norm, the rounding of dS by
+// 1.7e-3.
 //
 // Bound by the CSR's reads, once per 64 key blocks: 77 us of 9 ms (21 x 30 x 52 tokens, 16 heads,
 // a quarter of the blocks), 7 us at 2 x 6 heads of 612 tokens.
@@ -184,9 +186,10 @@ __global__ void __launch_bounds__(512) order_kernel(const int32_t* __restrict__ 
 // Warps 0-3 form X = a0 b0^T and P, warps 4-7 Y = a1 b1^T and dS (scores and dP, transposed when
 // KV), 4 x 4 values a thread; then the two groups accumulate P b1 and dS b0 (KV) or half of the
 // block's rows of dS b0 each, 4 rows x D / 16 channels a thread. Measured (4 x 16 x 16 tokens, 2
-// heads, d = 64, 0.4 of the blocks): 47 us, FMA pipes 31% and shared memory 40% of the time; what
-// bounds it are a step's three barriers with two CTAs an SM, and the last CTAs. 8 x 8 values a
-// thread (128 registers): 51; one stream buffer and three CTAs: 51; packed FMAs: the same.
+// heads, d = 64, 0.4 of the blocks): 47 us, 49 with the preparation; FMA pipes 31% and shared memory
+// 40% of the time; what bounds it are a step's three barriers with two CTAs an SM, and the last CTAs.
+// Tried, with the preparation: 8 x 8 values a thread 53; one stream buffer and three CTAs 53; packed
+// FMAs the same.
 struct F32Args {
   const float *q, *k, *v, *d_o, *stats;
   float *dq, *dk, *dv;

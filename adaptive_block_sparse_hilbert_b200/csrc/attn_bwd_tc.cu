@@ -6,8 +6,10 @@
 //   KV = true   owns key rows; streams Q, dO.    S^T = K Q^T, dP^T = V dO^T,
 //                                                dV += P^T dO, dK += dS^T Q
 // with P = 2^(scale log2(e) S - lse2) and dS = P (dP - D), both rounded to bf16 as operands of
-// the second products (their relative error, 2^-9 on average, is the size of the gradients'
-// own rounding); sums stay in fp32 in TMEM. One owner per output row: no atomics.
+// the second products. That moves the gradients by 1.7e-3 of their norm, as much as their own
+// rounding does, so the two together by 2.4e-3; two parts of 16 bits, as the decoding attention keeps
+// its weights in, would make two products of each second one. Sums stay in fp32 in TMEM. One
+// owner per output row: no atomics.
 //
 //   * Warp 16 issues TMA loads into two rings of stages, warp 17 the products S, warp 18 dP and
 //     the second products. (One thread's waits and commits for all three took longer than the

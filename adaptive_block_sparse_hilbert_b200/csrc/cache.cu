@@ -16,8 +16,8 @@ namespace cg = cooperative_groups;
 // A CTA holds the 64 rows of one (page, key head), 16 bytes a thread and row: thread = (row
 // lane, 16-byte piece), rows row lane, row lane + kLanes, ... All of a thread's loads are issued
 // before its first store, so a CTA has up to 32 KB in flight. (16 prompts, d = 128, on 128 / 256
-// / 512 threads: 41 / 44 / 50 us; eviction of 62500 of 250 thousand tokens, selection included: 134
-// / 130 / 136 us.)
+// / 512 threads: 41 / 44 / 50 us of kernel. The gather of an eviction, while values still went through
+// registers, took 3% longer on 128 and 5% longer on 512 threads than on 256.)
 constexpr int kAppendThreads = 128, kEvictCopyThreads = 256;
 
 template <typename T, int D, int kPageThreads>
@@ -62,7 +62,7 @@ __device__ __forceinline__ void write_mean(const uint4 (&k)[PageRows<T, D, kPage
 // Append
 // ---------------------------------------------------------------------------------
 // One CTA per (touched block, key head, sequence). Bound by the copy: 16 prompts of 1 to 4001
-// tokens, 8 key heads, d = 128, take 41 us, the copy rate.
+// tokens, 8 key heads, d = 128, take 41 us of kernel, the copy rate (a call among others 48).
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(CacheView<T> c, const T* __restrict__ k_new,
                                                               const T* __restrict__ v_new, int64_t n_tokens,
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(CacheView<T> c, 
 // and sums joined over the cluster, then every block's share P_b, gathered in the shared
 // memory of the cluster's first CTA, which selects. Bound by latencies: 32 sequences of 2 to 9
 // thousand tokens, 32 query on 8 key heads, d = 128, take 23 us, of which the scores are a fifth;
-// 131 and 250 thousand tokens, 40 on 8 heads, 34 us: scores 9, softmaxes 6, selection 6, emission 3.
+// 131 and 250 thousand tokens, 40 on 8 heads, 35 us: scores 9, softmaxes 6, selection 6, emission 3.
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRankMost = 256;    // this many blocks are ranked against one another (4 us)
@@ -847,8 +847,8 @@ __global__ void __launch_bounds__(kEvictCopyThreads, sizeof(T) == 2 ? 6 : 4)
 // host side
 // ---------------------------------------------------------------------------------
 // CTAs of a unit's cluster: doubled while the units leave SMs idle and every CTA keeps at
-// least `least` items, up to 8 (clusters of 16 found too few places at a time: the eviction's
-// selection over 250 thousand tokens and 8 key heads took 135 us with them, 53 with 8).
+// least `least` items, up to 8 (clusters of 16 found too few places at a time: an earlier version of
+// the eviction's selection, over 250 thousand tokens and 8 key heads, took 2.5 times as long with them).
 static int cluster_size(int64_t units, int64_t items, int64_t least) {
   int n = 1;
   while (n < 8 && units * n * 2 <= 148 && items / (2 * n) >= least) n *= 2;

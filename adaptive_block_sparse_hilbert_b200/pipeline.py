@@ -127,7 +127,7 @@ class CachedAttention:
 
     append() and evict() change the page table and lengths on the host and copy them to the
     device; attend() touches only device state and may be captured into a CUDA graph and
-    replayed between them.
+    replayed between them. An append() or evict() that raises leaves the streams as they were.
     """
 
     def __init__(self, B: int, H: int, Hkv: int, d: int, n_pages: int, max_blocks: int, dtype=torch.bfloat16,

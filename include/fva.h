@@ -307,7 +307,8 @@ FVA_API int fva_dense_attn(const fva_shape* s, const void* q_dev, const void* k_
  * All of q, k, v, o, d_o, dq, dk, dv are [B, H, N, d] in Hilbert order, dtype s->dtype (V too:
  * a bf16 layer gives its V as bf16 here even when its forward read an fp16 V); lse as above.
  *   FVA_BF16 (tensor cores, d in {64, 128}): fp32 accumulation; P and dS are rounded to bf16
- *     for their products, the gradients to bf16 once.
+ *     for their products, the gradients to bf16 once: together 2.4e-3 of a gradient's norm, where
+ *     the last rounding alone makes 1.7e-3.
  *   FVA_F32 (CUDA cores, d in {32, 64, 128}): fp32 throughout.
  * A row that keeps no block has dQ = 0; a key block that no row keeps has dK = dV = 0. Sums
  * run in a fixed order (no atomics): equal inputs give equal bits.
@@ -412,6 +413,9 @@ FVA_API int fva_cache_route(const fva_cache* cache, const fva_seqs* seqs, const 
  * right but its rounding order is not fixed; otherwise equal inputs give equal bits).
  * An entry outside the sequence's blocks sets FVA_DEVERR_BAD_LIST and is skipped.
  * Every softmax statistic and sum is float32; scale <= 0 selects 1/sqrt(d).
+ * Keys and values are read once per 16 query heads of a key head. With accumulate the workspace
+ * holds a float32 score per query head and table slot, B * H * 64 * max_blocks of them: for tables
+ * much wider than their sequences that is the larger part of it.
  */
 FVA_API size_t fva_cache_attn_workspace_bytes(const fva_cache* cache, int B, int max_blocks, int H, int accumulate);
 FVA_API int fva_cache_attn(const fva_cache* cache, const fva_seqs* seqs, const void* q_dev, int H, int64_t q_stride,
