@@ -127,7 +127,8 @@ class CachedAttention:
 
     append() and evict() change the page table and lengths on the host and copy them to the
     device; attend() touches only device state and may be captured into a CUDA graph and
-    replayed between them. An append() or evict() that raises leaves the streams as they were.
+    replayed between them. An append() that raises leaves the streams as they were, and so does an
+    evict(), but for streams it has cut before the failure where it cut them in turn.
     """
 
     def __init__(self, B: int, H: int, Hkv: int, d: int, n_pages: int, max_blocks: int, dtype=torch.bfloat16,
@@ -217,8 +218,8 @@ class CachedAttention:
             for b in cut[first:end]:
                 free += self.pages[b][::-1]
             groups.append(slice(first, end))
-        # As in append(): what can fail comes before what the streams are known by, and before the
-        # first group's old pages may be written.
+        # As in append(): what can fail comes before what the streams are known by. A group's old pages
+        # may be the next one's new ones, so each group is booked when its call is made.
         with torch.cuda.device(self.table.device), torch.cuda.stream(st):
             every = torch.arange(keep, dtype=torch.int32, device=self.table.device)
             kept = torch.empty((self.B, self.cache.k.shape[1], keep), dtype=torch.int32, device=self.table.device)
@@ -235,13 +236,13 @@ class CachedAttention:
                 for g in groups:
                     fva.fva_cache_evict(self.cache, table[g], length[g], keep, n_sink, n_recent, dst[g], out[g], new_len[g],
                                         self.evict_ws, self.dev_status, st)
-                self.table[at], self.length[at] = new_table, new_len
-        self.free = free
-        for b, pages in zip(cut, fresh):
-            self.pages[b], self.lengths[b] = pages, keep
-        if cut and some:
-            with torch.cuda.device(self.table.device), torch.cuda.stream(st):
-                kept[at] = out
+                    self.table[at[g]], self.length[at[g]] = new_table[g], new_len[g]
+                    del self.free[len(self.free) - room * (g.stop - g.start):]
+                    for b, pages in zip(cut[g], fresh[g]):
+                        self.free += self.pages[b][::-1]
+                        self.pages[b], self.lengths[b] = pages, keep
+                if some:
+                    kept[at] = out
         return kept
 
 

@@ -157,7 +157,7 @@ def evicted(att, keep, sink, recent):
     (12, [200, 100, 0, 64], 64),          # room for all that are cut
     (9, [200, 100, 64, 1], 200),          # nothing to cut, and a single page free
     (9, [200, 64, 64, 64], 100),          # one of four, and just the two pages for it
-    (15, [200, 130, 190, 140], 70),       # all are cut, one at a time: two pages are free
+    (15, [200, 130, 190, 140], 70),       # all are cut, in turn: one, two (its four pages are free then), one
     (18, [128, 320, 100, 321], 130),      # two of four, one at a time, out of order with the others
     (9, [65, 129, 63, 65], 64),           # a page is enough
 ])
@@ -179,3 +179,35 @@ def test_evict_without_a_page_is_refused(streams):
         att.evict(64, 2, 8)
     assert state(att) == before
     evicted(att, 200, 2, 8)
+
+
+@pytest.mark.parametrize("nth,done", [(2, 1), (3, 3)])  # (two pages are free: one stream, two, one)
+def test_evict_that_fails_between_groups_keeps_every_stream_whole(streams, monkeypatch, nth, done):
+    """Where the streams are cut in turn and the nth call fails, those before it are cut and the others
+    as they were: no stream is left with pages that another one has been given."""
+    att = streams(B=4, n_pages=15)
+    x = tokens(660)
+    lens = [200, 130, 190, 140]
+    att.append(x, x.flip(0), lens)
+    att.cache.mass.uniform_(0, 1)
+    keys, masses = [held(att, b) for b in range(4)], []
+    for b, n in enumerate(lens):
+        at = torch.arange(n)
+        masses.append(att.cache.mass[att.table[b, at // 64].long(), :, at % 64])
+    evict, calls = fva.fva_cache_evict, []
+
+    def fails(*a, **k):
+        calls.append(a)
+        if len(calls) == nth:
+            raise KeyboardInterrupt
+        evict(*a, **k)
+    with monkeypatch.context() as m:
+        m.setattr(fva, "fva_cache_evict", fails)
+        with pytest.raises(KeyboardInterrupt):
+            att.evict(70, 2, 8)
+    check(att)
+    assert att.lengths == [70] * done + lens[done:]
+    for b in range(4):
+        for g in range(HKV):
+            want = CO.evict(masses[b][:, g].numpy(), 70, 2, 8) if b < done else slice(None)
+            assert torch.equal(held(att, b)[:, g], keys[b][want, g])
